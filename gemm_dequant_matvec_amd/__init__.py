@@ -99,12 +99,38 @@ _lib.qmv_q8x_bytes.argtypes = [_i64, _i64, ctypes.POINTER(ctypes.c_size_t)]
 _lib.qmv_q8x_bytes.restype = _int
 _lib.qmv_gemm.argtypes = [_int, _i64, _i64, _i64, _vp, _vp, _int, _vp, _int, _vp]
 _lib.qmv_gemm.restype = _int
+_lib.qmv_gemm_glu.argtypes = [_int, _i64, _i64, _i64, _vp, _vp, _vp, _int, _int, _vp, _int, _vp, _vp, _vp]
+_lib.qmv_gemm_glu.restype = _int
+_lib.qmv_gemm_glu_backward.argtypes = [_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _int, _int, _vp, _vp, _vp, _vp,
+                                       ctypes.c_size_t, _vp]
+_lib.qmv_gemm_glu_backward.restype = _int
+_lib.qmv_gemm_glu_backward_bytes.argtypes = [_int, _i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)]
+_lib.qmv_gemm_glu_backward_bytes.restype = _int
+
+
+class QmvRopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64)]
+
+
+class QmvRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+_lib.qmv_rope.argtypes = [_i64, _i64, _i64, _int, _int, ctypes.POINTER(QmvRopeTensor), _int, _vp, _vp, ctypes.c_float,
+                          _int, _vp]
+_lib.qmv_rope.restype = _int
+_lib.qmv_rope_freqs.argtypes = [_i64, ctypes.c_double, ctypes.POINTER(QmvRopeScaling), ctypes.POINTER(ctypes.c_float)]
+_lib.qmv_rope_freqs.restype = _int
 _lib.qmv_dequant.argtypes = [_int, _i64, _i64, _vp, _vp, _vp]
 _lib.qmv_dequant.restype = _int
 
 EXPORTS = ("qmv_abi_version", "qmv_status_string", "qmv_last_error", "qmv_packed_bytes",
            "qmv_pack", "qmv_matvec", "qmv_matvec_ex", "qmv_matvec_swiglu", "qmv_matvec_grouped", "qmv_gemm",
            "qmv_dequant", "qmv_quantize_x", "qmv_q8x_bytes")
+LAYER_EXPORTS = ("qmv_gemm_glu", "qmv_gemm_glu_backward", "qmv_gemm_glu_backward_bytes", "qmv_rope", "qmv_rope_freqs")
 
 
 class QmvError(RuntimeError):
@@ -361,6 +387,157 @@ def gemm(fmt, W: torch.Tensor, X: torch.Tensor, N: int, K: int, Y: torch.Tensor 
     _check(_lib.qmv_gemm(_fmt(fmt), N, K, M, _ptr(W), _ptr(X), _DTYPES[X.dtype], _ptr(Y),
                          _DTYPES[Y.dtype], _stream(stream)))
     return Y
+
+
+ACTS = {"silu": 1, "gelu_tanh": 2, "gelu": 3}
+ROPE_LAYOUTS = {"half": 1, "interleaved": 2}
+ROPE_KINDS = {"linear": 1, "ntk": 2, "parts": 3}
+
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in ACTS:
+            raise ValueError(f"unknown activation {act!r}; one of {sorted(ACTS)}")
+        return ACTS[act]
+    return int(act)
+
+
+def _same(t: torch.Tensor, like: torch.Tensor, shape: tuple, what: str) -> torch.Tensor:
+    """t must be of this shape, and of like's dtype and device."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {shape}")
+    _need_dtype(t, like.dtype, what)
+    if t.device != like.device:
+        raise ValueError(f"{what} is on {t.device}, expected {like.device}")
+    return t
+
+
+def gemm_glu(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, X: torch.Tensor, N: int, K: int, act="silu",
+             H: torch.Tensor | None = None, G: torch.Tensor | None = None, U: torch.Tensor | None = None,
+             save: bool = False, stream=None):
+    """H [M][N] = act(X W_gate^T) * (X W_up^T) for X [M][K] (bf16 or f16, as H), in one kernel.
+
+    act: "silu", "gelu_tanh" or "gelu".  With save=True (or G and U given) the
+    two products are kept for gemm_glu_backward and (H, G, U) is returned.
+    """
+    M = X.shape[0]
+    if X.dim() != 2 or X.shape[1] != K:
+        raise ValueError(f"X has shape {tuple(X.shape)}, expected [M][{K}]")
+    if X.dtype not in _DTYPES:
+        raise ValueError("X dtype must be float32, float16 or bfloat16")
+    if (G is None) != (U is None):
+        raise ValueError("G and U go together")
+    _need(W_gate, packed_bytes(fmt, N, K), "W_gate")
+    _need(W_up, packed_bytes(fmt, N, K), "W_up")
+    keep = save or G is not None
+    H, G, U = (None if t is None and i and not keep else
+               torch.empty((M, N), dtype=X.dtype, device=X.device) if t is None else _same(t, X, (M, N), "HGU"[i])
+               for i, t in enumerate((H, G, U)))
+    _check(_lib.qmv_gemm_glu(_fmt(fmt), N, K, M, _ptr(W_gate), _ptr(W_up), _ptr(X), _DTYPES[X.dtype], _act(act),
+                             _ptr(H), _DTYPES[H.dtype], _ptr(G), _ptr(U), _stream(stream)))
+    return (H, G, U) if keep else H
+
+
+def gemm_glu_backward_bytes(fmt, N: int, K: int, M: int) -> int:
+    """Bytes of scratch memory that gemm_glu_backward needs for these sizes."""
+    out = ctypes.c_size_t(0)
+    _check(_lib.qmv_gemm_glu_backward_bytes(_fmt(fmt), N, K, M, ctypes.byref(out)))
+    return out.value
+
+
+def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
+                      dH: torch.Tensor, N: int, K: int, act="silu", dG: torch.Tensor | None = None,
+                      dU: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """(dX [M][K], dG [M][N], dU [M][N]) of gemm_glu for the gradient dH [M][N] of H,
+    from its saved G and U; all of one dtype.  dG and dU may be given as two of
+    the buffers G, U and dH.  workspace: scratch memory of
+    gemm_glu_backward_bytes bytes, allocated when absent."""
+    M = G.shape[0]
+    if G.dtype not in _DTYPES:
+        raise ValueError("G dtype must be float32, float16 or bfloat16")
+    _need(W_gate, packed_bytes(fmt, N, K), "W_gate")
+    _need(W_up, packed_bytes(fmt, N, K), "W_up")
+    _same(G, G, (M, N), "G")
+    _same(U, G, (M, N), "U")
+    _same(dH, G, (M, N), "dH")
+    dG = torch.empty_like(G) if dG is None else _same(dG, G, (M, N), "dG")
+    dU = torch.empty_like(G) if dU is None else _same(dU, G, (M, N), "dU")
+    dX = torch.empty((M, K), dtype=G.dtype, device=G.device) if dX is None else _same(dX, G, (M, K), "dX")
+    nbytes = gemm_glu_backward_bytes(fmt, N, K, M)
+    if workspace is None and nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=G.device)
+    if nbytes:
+        _need(workspace, nbytes, "workspace")
+    _check(_lib.qmv_gemm_glu_backward(_fmt(fmt), N, K, M, _ptr(W_gate), _ptr(W_up), _ptr(G), _ptr(U), _ptr(dH),
+                                      _DTYPES[G.dtype], _act(act), _ptr(dG), _ptr(dU), _ptr(dX), _ptr(workspace),
+                                      nbytes, _stream(stream)))
+    return dX, dG, dU
+
+
+def rope_freqs(R: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0, original: float = 0.0,
+               low: float = 1.0, high: float = 32.0, device="cuda") -> torch.Tensor:
+    """The R/2 rotary frequencies base^(-2i/R) as f32, stretched for a longer
+    context by scaling: "linear" (all divided by factor), "ntk" (a larger base)
+    or "parts" (pairs with fewer than `low` turns over the `original` context
+    divided by factor, those with more than `high` kept, a ramp between)."""
+    host = torch.empty(max(0, R // 2), dtype=torch.float32)
+    sc = None
+    if scaling is not None:
+        if scaling not in ROPE_KINDS:
+            raise ValueError(f"unknown scaling {scaling!r}; one of {sorted(ROPE_KINDS)}")
+        sc = ctypes.byref(QmvRopeScaling(ROPE_KINDS[scaling], factor, original, low, high))
+    _check(_lib.qmv_rope_freqs(R, base, sc, ctypes.cast(host.data_ptr(), ctypes.POINTER(ctypes.c_float))))
+    return host.to(device)
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torch.Tensor, layout="half",
+         amplitude: float = 1.0, inverse: bool = False, q_out: torch.Tensor | None = None,
+         k_out: torch.Tensor | None = None, stream=None):
+    """Rotary positions of q [T][heads][D] and k [T][kv_heads][D] (or None) at pos
+    int64 [T], in one launch; returns (q_out, k_out).
+
+    freqs f32 [R/2] names the frequencies of the first R values of every head
+    (the rest is copied); layout "half" pairs (i, i + R/2), "interleaved"
+    (2i, 2i + 1).  The cosines and sines are multiplied by amplitude.
+    inverse=True turns back: the gradient of the forward call.  q and k may be
+    strided (slices of one fused product) as long as a head's values are
+    adjacent; q_out=q, k_out=k works in place.
+    """
+    if layout in ROPE_LAYOUTS:
+        layout = ROPE_LAYOUTS[layout]
+    elif isinstance(layout, str):
+        raise ValueError(f"unknown layout {layout!r}; one of {sorted(ROPE_LAYOUTS)}")
+    if q.dim() != 3:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [T][heads][D]")
+    T, _, D = q.shape
+    if q.dtype not in _DTYPES:
+        raise ValueError("q dtype must be float32, float16 or bfloat16")
+    _need_dtype(pos, torch.int64, "pos")
+    _need_dtype(freqs, torch.float32, "freqs")
+    _need(pos, T * 8, "pos")
+    R = 2 * freqs.numel()
+    arr = (QmvRopeTensor * 2)()
+    outs = []
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            outs.append(None)
+            continue
+        _same(x, q, (T, x.shape[1] if x.dim() == 3 else -1, D), name)
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else _same(y, x, tuple(x.shape),
+                                                                                          name + "_out")
+        t = arr[sum(o is not None for o in outs)]
+        for v, what in ((x, name), (y, name + "_out")):
+            if not v.is_cuda:
+                raise ValueError("tensors passed to libqmv must live on the GPU")
+            if v.stride(2) != 1 and D > 1:
+                raise ValueError(f"the values of a head of {what} must be adjacent")
+        t.x, t.y, t.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
+        t.x_token, t.x_head, t.y_token, t.y_head = x.stride(0), x.stride(1), y.stride(0), y.stride(1)
+        outs.append(y)
+    _check(_lib.qmv_rope(T, D, R, layout, sum(o is not None for o in outs), arr, _DTYPES[q.dtype], _ptr(pos),
+                         _ptr(freqs), amplitude, int(inverse), _stream(stream)))
+    return tuple(outs)
 
 
 def dequant(fmt, W: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None,

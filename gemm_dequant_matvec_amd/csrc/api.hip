@@ -6,6 +6,7 @@
 // naming the tensor; pytensor-ml issue 53, PR 18 acceptance rules: fail with
 // the missing capability named, not at token 1).
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -318,6 +319,170 @@ int qmv_quantize_x(int64_t K, int64_t batch, const float* x, void* xq, void* str
   if ((st = check_device())) return st;
   return launched(qmv::launch_quantize_x(K, batch, x, static_cast<uint8_t*>(xq), as_stream(stream)),
                   "quantize_x");
+}
+
+// Arguments that qmv_gemm_glu and its backward pass share.
+static int check_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up, int dtype,
+                     const char* dtype_name, int act) {
+  int st;
+  if ((st = check_fmt(fmt))) return st;
+  if ((st = check_shape(fmt, N, K, M, "M"))) return st;
+  if (!W_gate) return fail(QMV_ERR_NULL, "W_gate is NULL");
+  if (!W_up) return fail(QMV_ERR_NULL, "W_up is NULL");
+  if (dtype != QMV_F32 && dtype != QMV_F16 && dtype != QMV_BF16 && dtype != QMV_Q8X)
+    return fail(QMV_ERR_DTYPE, "%s=%d is not a qmv_dtype", dtype_name, dtype);
+  if (dtype != QMV_F16 && dtype != QMV_BF16)
+    return fail(QMV_ERR_UNSUPPORTED, "the gated products take and write bf16 or f16");
+  if (act < QMV_ACT_SILU || act > QMV_ACT_GELU) return fail(QMV_ERR_UNSUPPORTED, "act=%d is not a qmv_act", act);
+  if (!aligned(W_gate, 16)) return fail(QMV_ERR_ALIGN, "W_gate is not 16-byte aligned");
+  if (!aligned(W_up, 16)) return fail(QMV_ERR_ALIGN, "W_up is not 16-byte aligned");
+  // the grid holds M / 128 (or M / 32 up to 32) row tiles in y, elements are 64-bit indexed
+  if (M > int64_t(65535) * 128) return fail(QMV_ERR_OVERFLOW, "M=%lld too large for one launch", (long long)M);
+  if (N > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return fail(QMV_ERR_OVERFLOW, "N or K too large");
+  if (M * N / 2048 >= (int64_t(1) << 31) - 1 || M * K / 1024 >= (int64_t(1) << 31) - 1)
+    return fail(QMV_ERR_OVERFLOW, "M * N or M * K too large for one launch");
+  return QMV_OK;
+}
+
+static int check_buffer(const void* p, const char* name) {
+  if (!p) return fail(QMV_ERR_NULL, "%s is NULL", name);
+  if (!aligned(p, 16)) return fail(QMV_ERR_ALIGN, "%s is not 16-byte aligned", name);
+  return QMV_OK;
+}
+
+int qmv_gemm_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up, const void* X,
+                 int x_dtype, int act, void* H, int h_dtype, void* G, void* U, void* stream) {
+  int st;
+  if ((st = check_glu(fmt, N, K, M, W_gate, W_up, x_dtype, "x_dtype", act))) return st;
+  if (h_dtype != QMV_F32 && h_dtype != QMV_F16 && h_dtype != QMV_BF16 && h_dtype != QMV_Q8X)
+    return fail(QMV_ERR_DTYPE, "h_dtype=%d is not a qmv_dtype", h_dtype);
+  if (h_dtype != x_dtype) return fail(QMV_ERR_UNSUPPORTED, "h_dtype must be x_dtype");
+  if ((st = check_buffer(X, "X"))) return st;
+  if ((st = check_buffer(H, "H"))) return st;
+  if ((G != nullptr) != (U != nullptr)) return fail(QMV_ERR_NULL, "%s is NULL and %s is not", G ? "U" : "G", G ? "G" : "U");
+  if (G && ((st = check_buffer(G, "G")) || (st = check_buffer(U, "U")))) return st;
+  if ((st = check_device())) return st;
+  return launched(qmv::launch_glu_fwd(fmt, N, K, M, static_cast<const uint8_t*>(W_gate),
+                                      static_cast<const uint8_t*>(W_up), static_cast<const uint16_t*>(X),
+                                      x_dtype == QMV_F16, act, static_cast<uint16_t*>(H), static_cast<uint16_t*>(G),
+                                      static_cast<uint16_t*>(U), as_stream(stream)),
+                  "gemm_glu");
+}
+
+static size_t glu_backward_bytes(int64_t N, int64_t K, int64_t M) {
+  const int splits = qmv::glu_backward_splits(N, K, M);
+  return splits > 1 ? size_t(splits) * size_t(M) * size_t(K) * 4 : 0;
+}
+
+int qmv_gemm_glu_backward_bytes(int fmt, int64_t N, int64_t K, int64_t M, size_t* out_bytes) {
+  int st;
+  if ((st = check_fmt(fmt))) return st;
+  if ((st = check_shape(fmt, N, K, M, "M"))) return st;
+  if (!out_bytes) return fail(QMV_ERR_NULL, "out_bytes is NULL");
+  if (M > (int64_t(1) << 40) / K) return fail(QMV_ERR_OVERFLOW, "M * K too large");
+  *out_bytes = glu_backward_bytes(N, K, M);
+  return ok();
+}
+
+int qmv_gemm_glu_backward(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up,
+                          const void* G, const void* U, const void* dH, int dtype, int act, void* dG, void* dU,
+                          void* dX, void* ws, size_t ws_bytes, void* stream) {
+  int st;
+  if ((st = check_glu(fmt, N, K, M, W_gate, W_up, dtype, "dtype", act))) return st;
+  const void* bufs[] = {G, U, dH, dG, dU, dX};
+  const char* names[] = {"G", "U", "dH", "dG", "dU", "dX"};
+  for (int i = 0; i < 6; ++i)
+    if ((st = check_buffer(bufs[i], names[i]))) return st;
+  if (dG == dU) return fail(QMV_ERR_UNSUPPORTED, "dG and dU are the same buffer");
+  for (int i = 0; i < 5; ++i)
+    if (dX == bufs[i]) return fail(QMV_ERR_UNSUPPORTED, "dX is the buffer of %s", names[i]);
+  const size_t need = glu_backward_bytes(N, K, M);
+  if (need) {
+    if ((st = check_buffer(ws, "ws"))) return st;
+    if (ws_bytes < need)
+      return fail(QMV_ERR_SHAPE, "ws_bytes=%llu, the call needs %llu", (unsigned long long)ws_bytes,
+                  (unsigned long long)need);
+  }
+  if ((st = check_device())) return st;
+  return launched(qmv::launch_glu_bwd(fmt, N, K, M, static_cast<const uint8_t*>(W_gate),
+                                      static_cast<const uint8_t*>(W_up), static_cast<const uint16_t*>(G),
+                                      static_cast<const uint16_t*>(U), static_cast<const uint16_t*>(dH),
+                                      dtype == QMV_F16, act, static_cast<uint16_t*>(dG), static_cast<uint16_t*>(dU),
+                                      static_cast<uint16_t*>(dX), static_cast<float*>(ws),
+                                      qmv::glu_backward_splits(N, K, M), as_stream(stream)),
+                  "gemm_glu_backward");
+}
+
+int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_rope_tensor* tensors, int dtype,
+             const int64_t* pos, const float* freqs, float amplitude, int inverse, void* stream) {
+  int st;
+  if (T < 1) return fail(QMV_ERR_SHAPE, "T=%lld must be >= 1", (long long)T);
+  if (D < 1) return fail(QMV_ERR_SHAPE, "D=%lld must be >= 1", (long long)D);
+  if (R < 2 || R % 2 || R > D || R > 4096)
+    return fail(QMV_ERR_SHAPE, "R=%lld must be even, in [2, min(D, 4096)] (D=%lld)", (long long)R, (long long)D);
+  if (layout != QMV_ROPE_HALF && layout != QMV_ROPE_INTERLEAVED)
+    return fail(QMV_ERR_UNSUPPORTED, "layout=%d is not a qmv_rope_layout", layout);
+  if (count < 1 || count > QMV_ROPE_MAX)
+    return fail(QMV_ERR_SHAPE, "count=%d must be in [1, %d]", count, QMV_ROPE_MAX);
+  if (!tensors) return fail(QMV_ERR_NULL, "tensors is NULL");
+  if (!pos) return fail(QMV_ERR_NULL, "pos is NULL");
+  if (!freqs) return fail(QMV_ERR_NULL, "freqs is NULL");
+  if (dtype != QMV_F32 && dtype != QMV_F16 && dtype != QMV_BF16 && dtype != QMV_Q8X)
+    return fail(QMV_ERR_DTYPE, "dtype=%d is not a qmv_dtype", dtype);
+  if (dtype == QMV_Q8X) return fail(QMV_ERR_UNSUPPORTED, "rope takes f32, f16 or bf16");
+  if (!aligned(pos, 8)) return fail(QMV_ERR_ALIGN, "pos is not 8-byte aligned");
+  if (!aligned(freqs, 4)) return fail(QMV_ERR_ALIGN, "freqs is not 4-byte aligned");
+  const int64_t lim = int64_t(1) << 31;
+  int64_t heads = 0;
+  for (int i = 0; i < count; ++i) {
+    const qmv_rope_tensor& t = tensors[i];
+    if (t.heads < 1) return fail(QMV_ERR_SHAPE, "tensors[%d].heads=%lld must be >= 1", i, (long long)t.heads);
+    if (!t.x) return fail(QMV_ERR_NULL, "tensors[%d].x is NULL", i);
+    if (!t.y) return fail(QMV_ERR_NULL, "tensors[%d].y is NULL", i);
+    if (!aligned(t.x, dtype == QMV_F32 ? 4 : 2)) return fail(QMV_ERR_ALIGN, "tensors[%d].x is not aligned to its element", i);
+    if (!aligned(t.y, dtype == QMV_F32 ? 4 : 2)) return fail(QMV_ERR_ALIGN, "tensors[%d].y is not aligned to its element", i);
+    if (t.x == t.y && (t.x_token != t.y_token || t.x_head != t.y_head))
+      return fail(QMV_ERR_UNSUPPORTED, "tensors[%d] is in place with other strides", i);
+    if (t.heads >= lim) return fail(QMV_ERR_OVERFLOW, "tensors[%d].heads too large", i);
+    heads += t.heads;
+  }
+  // a block of tokens is indexed with 32-bit ints, the grid counts tokens
+  if (D >= lim || heads > (lim - 1) / D || T >= lim) return fail(QMV_ERR_OVERFLOW, "T or heads * D too large");
+  if ((st = check_device())) return st;
+  return launched(qmv::launch_rope(T, int(D), int(R), layout, count, tensors, dtype, pos, freqs, amplitude, inverse,
+                                   as_stream(stream)),
+                  "rope");
+}
+
+int qmv_rope_freqs(int64_t R, double base, const qmv_rope_scaling* scaling, float* freqs) {
+  if (R < 2 || R % 2 || R > 4096) return fail(QMV_ERR_SHAPE, "R=%lld must be even, in [2, 4096]", (long long)R);
+  if (!freqs) return fail(QMV_ERR_NULL, "freqs is NULL");
+  if (!(std::isfinite(base) && base > 0)) return fail(QMV_ERR_UNSUPPORTED, "base must be finite and > 0");
+  if (scaling) {
+    const qmv_rope_scaling& c = *scaling;
+    if (c.kind < QMV_ROPE_LINEAR || c.kind > QMV_ROPE_PARTS)
+      return fail(QMV_ERR_UNSUPPORTED, "scaling->kind=%d is not a qmv_rope_kind", c.kind);
+    if (!(std::isfinite(c.factor) && c.factor >= 1))
+      return fail(QMV_ERR_UNSUPPORTED, "scaling->factor must be finite and >= 1");
+    if (c.kind == QMV_ROPE_NTK) {
+      if (R < 4) return fail(QMV_ERR_SHAPE, "R=%lld must be >= 4 for QMV_ROPE_NTK", (long long)R);
+      base *= std::pow(c.factor, double(R) / double(R - 2));
+    }
+    if (c.kind == QMV_ROPE_PARTS &&
+        !(std::isfinite(c.original) && c.original > 0 && std::isfinite(c.low) && std::isfinite(c.high) && c.low < c.high))
+      return fail(QMV_ERR_UNSUPPORTED, "scaling->original must be > 0 and low < high, all finite");
+  }
+  for (int64_t i = 0; i < R / 2; ++i) {
+    double f = std::pow(base, -2.0 * double(i) / double(R));
+    if (scaling && scaling->kind == QMV_ROPE_LINEAR) f /= scaling->factor;
+    if (scaling && scaling->kind == QMV_ROPE_PARTS) {
+      const double r = scaling->original * f / 6.283185307179586;
+      const double c = std::fmin(1.0, std::fmax(0.0, (r - scaling->low) / (scaling->high - scaling->low)));
+      f *= c + (1.0 - c) / scaling->factor;
+    }
+    freqs[i] = static_cast<float>(f);
+  }
+  return ok();
 }
 
 int qmv_dequant(int fmt, int64_t N, int64_t K, const void* W, float* out, void* stream) {

@@ -1,0 +1,331 @@
+// Shared by the many-token products (glu_fwd*.hip, glu_bwd*.hip): the 16-bit
+// types, the matrix-core fragments, the LDS tile and the decoding of packed
+// weights to the 16-bit operand type.
+//
+// Every format's weight is w = a * t + b with a code byte t in 0..255 and f32
+// (a, b) per 32-weight unit (per 16 weights in Q6K); one fma gives the value of
+// the format's definition: a * t is exact or the only rounding is the one the
+// definition has too (W4A16: s q - s z with s z exact; Q4K, Q5K: the one
+// subtraction; per-row int8: s t - 128 s = s q rounded once).  It is then
+// rounded once, to nearest even, to the operand type.
+#pragma once
+
+#include "qmv_internal.h"
+
+namespace qmv {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Two f32 to two 16-bit values, round to nearest even, first in the low half.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  const f32x2 v = {a, b};
+  if constexpr (F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+template <bool F16>
+__device__ __forceinline__ float unpack16(uint32_t bits) {  // low 16 bits
+  if constexpr (F16) return f16_bits_to_f32(bits & 0xFFFFu);
+  else return bf16_bits_to_f32(bits);
+}
+
+template <bool F16>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {  // 32x32, 16 deep
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {  // 16x16, 32 deep
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Workgroup barrier for LDS traffic only (global loads stay in flight).
+__device__ __forceinline__ void lds_barrier16() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// 16-byte load of eight 16-bit values at any 2-byte aligned address.
+__device__ __forceinline__ u32x4 load8(const uint16_t* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+
+// The first n (0..7) of eight 16-bit values at p, zeros behind them; nothing
+// past p[n - 1] is read.
+__device__ __forceinline__ u32x4 load_part(const uint16_t* p, int n) {
+  uint32_t o[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) o[e >> 1] |= uint32_t(p[e]) << (16 * (e & 1));
+  return u32x4{o[0], o[1], o[2], o[3]};
+}
+
+// ------------------------------------------------------------------ LDS tile
+// Rows of 64 16-bit values (128 bytes, eight 16-byte pieces).  16 lanes reach
+// all 64 banks at once if their pieces differ in address bits 4..7, so piece c
+// of row r sits at
+//   row slot  r with its lowest bit exchanged for r0 ^ r6   (address bit 7)
+//   piece     c ^ ((r >> 1) ^ (r >> 3)) & 7                 (address bits 4..6)
+// which is free of conflicts both for 16 consecutive rows of one piece (the
+// fragment reads, the forward pass's writes) and for rows 8 apart (the
+// transposing writes of the backward pass).
+__device__ __forceinline__ int tile_at(int r, int c) {  // in 16-byte pieces
+  const int row = (r & ~1) | ((r ^ (r >> 6)) & 1);
+  return row * 8 + (c ^ (((r >> 1) ^ (r >> 3)) & 7));
+}
+
+// ------------------------------------------------------------ packed weights
+
+struct Mat {  // one packed matrix on the device
+  const uint8_t* p[4];
+};
+
+inline Mat mat_of(const uint8_t* W, const Planes& p) {
+  Mat m;
+  for (int i = 0; i < 4; ++i) m.p[i] = W + p.off[i];
+  return m;
+}
+
+struct Affine {  // w = a t + b; a1, b1 for the second 16 weights (Q6K), else as a0, b0
+  float a0, b0, a1, b1;
+};
+
+constexpr bool is_byte(int fmt) { return fmt == QMV_Q8_0 || fmt == QMV_I8_ROW; }
+constexpr bool is_fifth(int fmt) { return fmt == QMV_Q5_0 || fmt == QMV_Q5K; }
+constexpr bool is_super(int fmt) { return fmt == QMV_Q4K || fmt == QMV_Q5K; }
+
+// What the scales of one unit are loaded as.
+template <int FMT>
+struct MetaRaw {
+  u32x4 v;  // super-block record, or v[0], v[1]
+};
+
+template <int FMT>
+__device__ __forceinline__ MetaRaw<FMT> load_meta(const Mat& w, int64_t row, int u, int K) {
+  MetaRaw<FMT> m;
+  if constexpr (FMT == QMV_Q8_0 || FMT == QMV_Q4_0) {
+    m.v[0] = reinterpret_cast<const uint16_t*>(w.p[1])[row * (K >> 5) + u];
+  } else if constexpr (FMT == QMV_Q5_0) {
+    m.v[0] = reinterpret_cast<const uint16_t*>(w.p[2])[row * (K >> 5) + u];
+  } else if constexpr (FMT == QMV_W4A16_G64) {
+    m.v[0] = reinterpret_cast<const uint32_t*>(w.p[1])[row * (K >> 6) + (u >> 1)];
+  } else if constexpr (is_super(FMT)) {
+    m.v = reinterpret_cast<const u32x4*>(w.p[FMT == QMV_Q4K ? 1 : 2])[row * (K >> 8) + (u >> 3)];
+  } else if constexpr (FMT == QMV_Q6K) {
+    m.v[0] = reinterpret_cast<const uint16_t*>(w.p[2])[row * (K >> 5) + u];
+    m.v[1] = reinterpret_cast<const uint16_t*>(w.p[3])[row * (K >> 8) + (u >> 3)];
+  } else if constexpr (FMT == QMV_I8_ROW) {
+    m.v[0] = reinterpret_cast<const uint32_t*>(w.p[1])[row];
+  }
+  return m;
+}
+
+template <int FMT>
+__device__ __forceinline__ Affine affine_of(const MetaRaw<FMT>& m, int u) {
+  Affine f{0.f, 0.f, 0.f, 0.f};
+  if constexpr (FMT == QMV_Q8_0) {
+    f.a0 = f16_bits_to_f32(m.v[0]);
+    f.b0 = -128.0f * f.a0;
+  } else if constexpr (FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
+    f.a0 = f16_bits_to_f32(m.v[0]);
+    f.b0 = (FMT == QMV_Q4_0 ? -8.0f : -16.0f) * f.a0;
+  } else if constexpr (FMT == QMV_W4A16_G64) {
+    f.a0 = f16_bits_to_f32(m.v[0] & 0xFFFFu);
+    f.b0 = -(f.a0 * f16_bits_to_f32(m.v[0] >> 16));
+  } else if constexpr (is_super(FMT)) {
+    const uint32_t r1 = m.v[1], r2 = m.v[2], r3 = m.v[3];
+    const int sh = 6 * (u & 7);
+    const uint64_t lo = uint64_t(r1) | (uint64_t(r2) << 32);        // bits 0..63 of the 96
+    const uint64_t hi = uint64_t(r2 >> 16) | (uint64_t(r3) << 16);  // bits 48..95
+    f.a0 = f16_bits_to_f32(m.v[0] & 0xFFFFu) * static_cast<float>(uint32_t(lo >> sh) & 63u);
+    f.b0 = -(f16_bits_to_f32(m.v[0] >> 16) * static_cast<float>(uint32_t(hi >> sh) & 63u));
+  } else if constexpr (FMT == QMV_Q6K) {
+    const float d = f16_bits_to_f32(m.v[1]);
+    f.a0 = d * static_cast<float>(static_cast<int8_t>(m.v[0] & 0xFFu));
+    f.a1 = d * static_cast<float>(static_cast<int8_t>((m.v[0] >> 8) & 0xFFu));
+    f.b0 = -32.0f * f.a0;
+    f.b1 = -32.0f * f.a1;
+  } else if constexpr (FMT == QMV_I8_ROW) {
+    const uint32_t s = m.v[0];
+    f.a0 = __builtin_bit_cast(float, s);
+    f.b0 = -128.0f * f.a0;
+  }
+  return f;
+}
+
+// The codes of eight weights as loaded: q0 (and q1 for 8-bit codes) and the
+// word that holds their higher bits.
+struct Word8 {
+  uint32_t q0, q1, qh;
+};
+
+// Eight weights of word i (0..3) of a unit, in f32.
+template <int FMT>
+__device__ __forceinline__ void decode8(const Word8& c, const Affine& f, int i, float (&w)[8]) {
+  const float a = (FMT == QMV_Q6K && i >= 2) ? f.a1 : f.a0, b = (FMT == QMV_Q6K && i >= 2) ? f.b1 : f.b0;
+  if constexpr (is_byte(FMT)) {
+    const uint32_t lo = c.q0 ^ 0x80808080u, hi = c.q1 ^ 0x80808080u;  // q + 128
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[k] = fmaf(a, static_cast<float>((lo >> (8 * k)) & 0xFFu), b);
+      w[4 + k] = fmaf(a, static_cast<float>((hi >> (8 * k)) & 0xFFu), b);
+    }
+  } else {
+    uint32_t ev = c.q0 & 0x0F0F0F0Fu, od = (c.q0 >> 4) & 0x0F0F0F0Fu;  // codes 0, 2, 4, 6 and 1, 3, 5, 7
+    if constexpr (is_fifth(FMT)) {
+      ev |= ((c.qh >> (2 * i)) & 0x01010101u) << 4;
+      od |= ((c.qh >> (2 * i + 1)) & 0x01010101u) << 4;
+    } else if constexpr (FMT == QMV_Q6K) {
+      ev |= ((c.qh >> (4 * (i & 1))) & 0x03030303u) << 4;
+      od |= ((c.qh >> (4 * (i & 1) + 2)) & 0x03030303u) << 4;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[2 * k] = fmaf(a, static_cast<float>((ev >> (8 * k)) & 0xFFu), b);
+      w[2 * k + 1] = fmaf(a, static_cast<float>((od >> (8 * k)) & 0xFFu), b);
+    }
+  }
+}
+
+// One unit (32 weights of one row), as loaded.
+template <int FMT>
+struct UnitRaw {
+  static constexpr int NQ = FMT == QMV_DENSE_BF16 ? 4 : is_byte(FMT) ? 2 : 1;
+  u32x4 q[NQ];
+  u32x2 qh;
+  MetaRaw<FMT> m;
+};
+
+template <int FMT>
+__device__ __forceinline__ UnitRaw<FMT> load_unit(const Mat& w, int64_t row, int u, int K) {
+  UnitRaw<FMT> r;
+  constexpr int NQ = UnitRaw<FMT>::NQ;
+  const u32x4* q = reinterpret_cast<const u32x4*>(w.p[0]) + (row * (K >> 5) + u) * NQ;
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) r.q[i] = q[i];
+  if constexpr (is_fifth(FMT)) r.qh[0] = reinterpret_cast<const uint32_t*>(w.p[1])[row * (K >> 5) + u];
+  if constexpr (FMT == QMV_Q6K) r.qh = reinterpret_cast<const u32x2*>(w.p[1])[row * (K >> 5) + u];
+  r.m = load_meta<FMT>(w, row, u, K);
+  return r;
+}
+
+// Word i (0..3) of a unit: its eight weights as one 16-byte piece.
+template <int FMT, bool F16>
+__device__ __forceinline__ u32x4 unit_piece(const UnitRaw<FMT>& r, const Affine& f, int i) {
+  if constexpr (FMT == QMV_DENSE_BF16) {
+    if constexpr (!F16) return r.q[i];
+    u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t v = r.q[i][e];
+      o[e] = pack16<F16>(bf16_bits_to_f32(v & 0xFFFFu), bf16_bits_to_f32(v >> 16));
+    }
+    return o;
+  } else {
+    Word8 c;
+    if constexpr (is_byte(FMT)) {
+      c.q0 = r.q[i >> 1][2 * (i & 1)];
+      c.q1 = r.q[i >> 1][2 * (i & 1) + 1];
+    } else {
+      c.q0 = r.q[0][i];
+    }
+    if constexpr (is_fifth(FMT)) c.qh = r.qh[0];
+    if constexpr (FMT == QMV_Q6K) c.qh = r.qh[i >> 1];
+    float w[8];
+    decode8<FMT>(c, f, i, w);
+    return u32x4{pack16<F16>(w[0], w[1]), pack16<F16>(w[2], w[3]), pack16<F16>(w[4], w[5]), pack16<F16>(w[6], w[7])};
+  }
+}
+
+// Eight weights (word i of unit u) of one row, as loaded, for the transposing
+// backward tile.
+template <int FMT>
+struct WordRaw {
+  u32x4 q;  // q[0], q[1] unless dense
+  uint32_t qh;
+  MetaRaw<FMT> m;
+};
+
+template <int FMT>
+__device__ __forceinline__ WordRaw<FMT> load_word(const Mat& w, int64_t row, int u, int i, int K) {
+  WordRaw<FMT> r;
+  const int64_t word = row * (K >> 3) + 4 * u + i;
+  if constexpr (FMT == QMV_DENSE_BF16) {
+    r.q = reinterpret_cast<const u32x4*>(w.p[0])[word];
+  } else if constexpr (is_byte(FMT)) {
+    const u32x2 v = reinterpret_cast<const u32x2*>(w.p[0])[word];
+    r.q[0] = v[0];
+    r.q[1] = v[1];
+  } else {
+    r.q[0] = reinterpret_cast<const uint32_t*>(w.p[0])[word];
+  }
+  if constexpr (is_fifth(FMT)) r.qh = reinterpret_cast<const uint32_t*>(w.p[1])[row * (K >> 5) + u];
+  if constexpr (FMT == QMV_Q6K) r.qh = reinterpret_cast<const uint32_t*>(w.p[1])[row * (K >> 4) + 2 * u + (i >> 1)];
+  r.m = load_meta<FMT>(w, row, u, K);
+  return r;
+}
+
+template <int FMT>
+__device__ __forceinline__ void word_values(const WordRaw<FMT>& r, int u, int i, float (&w)[8]) {
+  if constexpr (FMT == QMV_DENSE_BF16) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t v = r.q[e];
+      w[2 * e] = bf16_bits_to_f32(v & 0xFFFFu);
+      w[2 * e + 1] = bf16_bits_to_f32(v >> 16);
+    }
+  } else {
+    const Word8 c{r.q[0], r.q[1], r.qh};
+    const Affine f = affine_of<FMT>(r.m, u);
+    decode8<FMT>(c, f, i, w);
+  }
+}
+
+// ---------------------------------------------------------------- activations
+// act(g), and act'(g) for the backward pass.  exp and reciprocal are the
+// hardware's (about 1 ulp in f32), far below the 16-bit rounding of the result.
+__device__ __forceinline__ float sigmoid16(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
+__device__ __forceinline__ float gelu_tanh_arg(float g) {  // 2 sqrt(2/pi) (g + 0.044715 g^3): (1 + tanh(z)) / 2 = sigmoid(2 z)
+  const float c = fminf(fmaxf(g, -20.0f), 20.0f);  // saturated far before 20: keeps g^3 finite
+  return 1.5957691216057308f * fmaf(0.044715f * c * c, c, c);
+}
+
+__device__ __forceinline__ float act_value(int act, float g) {
+  if (act == QMV_ACT_SILU) return g * sigmoid16(g);
+  if (act == QMV_ACT_GELU_TANH) return g * sigmoid16(gelu_tanh_arg(g));
+  return 0.5f * g * erfcf(-0.70710678118654752f * g);
+}
+
+__device__ __forceinline__ void act_both(int act, float g, float& a, float& da) {
+  if (act == QMV_ACT_SILU) {
+    const float s = sigmoid16(g);
+    a = g * s;
+    da = s * fmaf(g, 1.0f - s, 1.0f);
+  } else if (act == QMV_ACT_GELU_TANH) {
+    const float s = sigmoid16(gelu_tanh_arg(g));
+    const float c = fminf(fmaxf(g, -20.0f), 20.0f);
+    a = g * s;
+    da = fmaf(g * s, (1.0f - s) * 1.5957691216057308f * fmaf(0.134145f * c, c, 1.0f), s);
+  } else {
+    const float p = 0.5f * erfcf(-0.70710678118654752f * g);
+    a = g * p;
+    da = fmaf(g, 0.3989422804014327f * __expf(-0.5f * g * g), p);
+  }
+}
+
+}  // namespace qmv

@@ -1,0 +1,15 @@
+// Backward pass of the gated products, formats Q4_0, Q5_0, Q5K.
+#include "glu_bwd.h"
+
+namespace qmv {
+
+hipError_t launch_glu_bwd_c(int fmt, bool f16, const GluBwdArgs& p, int splits, hipStream_t s) {
+  switch (fmt) {
+    case QMV_Q4_0: return f16 ? glu_bwd_go<QMV_Q4_0, true>(p, splits, s) : glu_bwd_go<QMV_Q4_0, false>(p, splits, s);
+    case QMV_Q5_0: return f16 ? glu_bwd_go<QMV_Q5_0, true>(p, splits, s) : glu_bwd_go<QMV_Q5_0, false>(p, splits, s);
+    case QMV_Q5K: return f16 ? glu_bwd_go<QMV_Q5K, true>(p, splits, s) : glu_bwd_go<QMV_Q5K, false>(p, splits, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace qmv

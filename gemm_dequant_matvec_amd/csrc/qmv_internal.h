@@ -6,7 +6,7 @@
 #include <stdint.h>
 #include <stddef.h>
 
-#include "../../include/qmv.h"
+#include "../../include/qmv_layer.h"
 
 namespace qmv {
 
@@ -154,5 +154,13 @@ int64_t q8x_record_bytes(int64_t K);  // bytes per vector of a QMV_Q8X buffer
 hipError_t launch_quantize_x(int64_t K, int64_t batch, const float* x, uint8_t* xq, hipStream_t s);
 hipError_t launch_gemm(int fmt, int64_t N, int64_t K, int64_t M, const uint8_t* W,
                        const uint16_t* X, uint16_t* Y, hipStream_t s);
+hipError_t launch_glu_fwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_t* Wg, const uint8_t* Wu,
+                          const uint16_t* X, bool f16, int act, uint16_t* H, uint16_t* G, uint16_t* U, hipStream_t s);
+int glu_backward_splits(int64_t N, int64_t K, int64_t M);  // partial sums of dX per output
+hipError_t launch_glu_bwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_t* Wg, const uint8_t* Wu,
+                          const uint16_t* G, const uint16_t* U, const uint16_t* dH, bool f16, int act, uint16_t* dG,
+                          uint16_t* dU, uint16_t* dX, float* ws, int splits, hipStream_t s);
+hipError_t launch_rope(int64_t T, int D, int R, int layout, int count, const qmv_rope_tensor* t, int dtype,
+                       const int64_t* pos, const float* freqs, float amplitude, int inverse, hipStream_t s);
 
 }  // namespace qmv
