@@ -76,16 +76,44 @@ __device__ __forceinline__ u32x4 load_part(const uint16_t* p, int n) {
 
 // ------------------------------------------------------------------ LDS tile
 // Rows of 64 16-bit values (128 bytes, eight 16-byte pieces).  16 lanes reach
-// all 64 banks at once if their pieces differ in address bits 4..7, so piece c
-// of row r sits at
-//   row slot  r with its lowest bit exchanged for r0 ^ r6   (address bit 7)
-//   piece     c ^ ((r >> 1) ^ (r >> 3)) & 7                 (address bits 4..6)
-// which is free of conflicts both for 16 consecutive rows of one piece (the
-// fragment reads, the forward pass's writes) and for rows 8 apart (the
-// transposing writes of the backward pass).
+// all 64 banks at once if their pieces differ in address bits 4..7.  Piece c of
+// row r sits at c ^ (r / 2 % 8) of its row: free of conflicts for 16
+// consecutive rows of one piece, and a fragment 32 rows on is a constant offset
+// away.  The transposing writes of the backward pass also touch rows 8 apart,
+// so there the row's lowest bit is exchanged for r0 ^ r6 and the piece also
+// takes r / 8 % 8.
 __device__ __forceinline__ int tile_at(int r, int c) {  // in 16-byte pieces
+  return r * 8 + (c ^ ((r >> 1) & 7));
+}
+__device__ __forceinline__ int tile_at_t(int r, int c) {
   const int row = (r & ~1) | ((r ^ (r >> 6)) & 1);
   return row * 8 + (c ^ (((r >> 1) ^ (r >> 3)) & 7));
+}
+
+// -------------------------------------------------------- workgroups to tiles
+// Consecutive workgroups go to the 8 XCDs in turn, each with an L2 of its own.
+// Here an XCD takes a contiguous eighth of the tiles, and tiles count through
+// bands of kBand token tiles, so the 32 tiles an XCD works on at a time share 4
+// token and 8 weight tiles.
+struct TileId {
+  int x, y;
+};
+#ifndef VAR_BAND
+#define VAR_BAND 4
+#endif
+constexpr int kBand = VAR_BAND;
+__device__ __forceinline__ TileId tile_of_block(int nx, int bx, int ny, int by) {
+  const int X = (nx + bx - 1) / bx, Y = (ny + by - 1) / by, all = X * Y;
+  const int b = blockIdx.x, xcd = b & 7, per = all >> 3, more = all & 7;
+#ifdef VAR_NOXCD
+  const int t = b;
+#else
+  const int t = xcd * per + min(xcd, more) + (b >> 3);
+#endif
+  // XCD i takes per tiles, the first `more` one extra
+  const int band = t / (kBand * X), in = t - band * kBand * X;
+  const int high = min(kBand, Y - band * kBand);
+  return TileId{in / high, band * kBand + in % high};
 }
 
 // ------------------------------------------------------------ packed weights
@@ -98,6 +126,38 @@ inline Mat mat_of(const uint8_t* W, const Planes& p) {
   Mat m;
   for (int i = 0; i < 4; ++i) m.p[i] = W + p.off[i];
   return m;
+}
+
+// Bytes of one row of plane i.
+template <int FMT>
+__device__ __forceinline__ uint32_t row_bytes(int i, int K) {
+  if constexpr (FMT == QMV_Q8_0) return i ? K >> 4 : K;
+  else if constexpr (FMT == QMV_Q6K) return i == 0 ? K >> 1 : i == 1 ? K >> 2 : i == 2 ? K >> 4 : K >> 7;
+  else if constexpr (FMT == QMV_Q5_0 || FMT == QMV_Q5K) return i == 0 ? K >> 1 : i == 1 ? K >> 3 : K >> 4;
+  else if constexpr (FMT == QMV_DENSE_BF16) return 2 * K;
+  else if constexpr (FMT == QMV_I8_ROW) return i ? 4 : K;
+  else return i ? K >> 4 : K >> 1;  // W4A16_G64, Q4K, Q4_0
+}
+
+template <int FMT>
+constexpr int kPlanes = FMT == QMV_DENSE_BF16 ? 1 : FMT == QMV_Q6K ? 4 : FMT == QMV_Q5_0 || FMT == QMV_Q5K ? 3 : 2;
+
+// The matrix from row n on.  Loads below take a row relative to it, so that
+// with a uniform n every address is a scalar base and a 32-bit lane offset.
+template <int FMT>
+__device__ __forceinline__ Mat from_row(const Mat& w, int64_t n, int K) {
+  Mat m;
+#pragma unroll
+  for (int i = 0; i < kPlanes<FMT>; ++i) m.p[i] = w.p[i] + n * row_bytes<FMT>(i, K);
+  return m;
+}
+
+// A T at byte `row` (a lane's) + `u` of a plane.  LANE: u differs between lanes
+// too and joins the 32-bit offset; else it joins the scalar base.
+template <class T, bool LANE = true>
+__device__ __forceinline__ T load_at(const uint8_t* plane, uint32_t row, int64_t u = 0) {
+  if constexpr (LANE) return *reinterpret_cast<const T*>(plane + (row + uint32_t(u)));
+  else return *reinterpret_cast<const T*>((plane + u) + row);
 }
 
 struct Affine {  // w = a t + b; a1, b1 for the second 16 weights (Q6K), else as a0, b0
@@ -114,22 +174,23 @@ struct MetaRaw {
   u32x4 v;  // super-block record, or v[0], v[1]
 };
 
-template <int FMT>
-__device__ __forceinline__ MetaRaw<FMT> load_meta(const Mat& w, int64_t row, int u, int K) {
+// The scales of unit u of row r.
+template <int FMT, bool LANE>
+__device__ __forceinline__ MetaRaw<FMT> load_meta(const Mat& w, uint32_t r, int u, int K) {
   MetaRaw<FMT> m;
-  if constexpr (FMT == QMV_Q8_0 || FMT == QMV_Q4_0) {
-    m.v[0] = reinterpret_cast<const uint16_t*>(w.p[1])[row * (K >> 5) + u];
-  } else if constexpr (FMT == QMV_Q5_0) {
-    m.v[0] = reinterpret_cast<const uint16_t*>(w.p[2])[row * (K >> 5) + u];
+  constexpr int P = kPlanes<FMT> - 1;  // the plane of the scales (Q6K: of d)
+  const uint32_t at = r * row_bytes<FMT>(P, K);
+  if constexpr (FMT == QMV_Q8_0 || FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
+    m.v[0] = load_at<uint16_t, LANE>(w.p[P], at, 2 * u);
   } else if constexpr (FMT == QMV_W4A16_G64) {
-    m.v[0] = reinterpret_cast<const uint32_t*>(w.p[1])[row * (K >> 6) + (u >> 1)];
+    m.v[0] = load_at<uint32_t, LANE>(w.p[P], at, 4 * (u >> 1));
   } else if constexpr (is_super(FMT)) {
-    m.v = reinterpret_cast<const u32x4*>(w.p[FMT == QMV_Q4K ? 1 : 2])[row * (K >> 8) + (u >> 3)];
+    m.v = load_at<u32x4, LANE>(w.p[P], at, 16 * (u >> 3));
   } else if constexpr (FMT == QMV_Q6K) {
-    m.v[0] = reinterpret_cast<const uint16_t*>(w.p[2])[row * (K >> 5) + u];
-    m.v[1] = reinterpret_cast<const uint16_t*>(w.p[3])[row * (K >> 8) + (u >> 3)];
+    m.v[0] = load_at<uint16_t, LANE>(w.p[2], r * row_bytes<FMT>(2, K), 2 * u);
+    m.v[1] = load_at<uint16_t, LANE>(w.p[3], at, 2 * (u >> 3));
   } else if constexpr (FMT == QMV_I8_ROW) {
-    m.v[0] = reinterpret_cast<const uint32_t*>(w.p[1])[row];
+    m.v[0] = load_at<uint32_t>(w.p[1], at);
   }
   return m;
 }
@@ -210,17 +271,18 @@ struct UnitRaw {
   MetaRaw<FMT> m;
 };
 
-template <int FMT>
-__device__ __forceinline__ UnitRaw<FMT> load_unit(const Mat& w, int64_t row, int u, int K) {
-  UnitRaw<FMT> r;
+// Unit u of row r.
+template <int FMT, bool LANE>
+__device__ __forceinline__ UnitRaw<FMT> load_unit(const Mat& w, uint32_t r, int u, int K) {
+  UnitRaw<FMT> x;
   constexpr int NQ = UnitRaw<FMT>::NQ;
-  const u32x4* q = reinterpret_cast<const u32x4*>(w.p[0]) + (row * (K >> 5) + u) * NQ;
+  const uint32_t at = r * row_bytes<FMT>(0, K);
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) r.q[i] = q[i];
-  if constexpr (is_fifth(FMT)) r.qh[0] = reinterpret_cast<const uint32_t*>(w.p[1])[row * (K >> 5) + u];
-  if constexpr (FMT == QMV_Q6K) r.qh = reinterpret_cast<const u32x2*>(w.p[1])[row * (K >> 5) + u];
-  r.m = load_meta<FMT>(w, row, u, K);
-  return r;
+  for (int i = 0; i < NQ; ++i) x.q[i] = load_at<u32x4, LANE>(w.p[0], at, int64_t(u) * (16 * NQ) + 16 * i);
+  if constexpr (is_fifth(FMT)) x.qh[0] = load_at<uint32_t, LANE>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
+  if constexpr (FMT == QMV_Q6K) x.qh = load_at<u32x2, LANE>(w.p[1], r * row_bytes<FMT>(1, K), 8 * u);
+  x.m = load_meta<FMT, LANE>(w, r, u, K);
+  return x;
 }
 
 // Word i (0..3) of a unit: its eight weights as one 16-byte piece.
@@ -260,23 +322,25 @@ struct WordRaw {
   MetaRaw<FMT> m;
 };
 
+// Word i of unit u of row r.
 template <int FMT>
-__device__ __forceinline__ WordRaw<FMT> load_word(const Mat& w, int64_t row, int u, int i, int K) {
-  WordRaw<FMT> r;
-  const int64_t word = row * (K >> 3) + 4 * u + i;
+__device__ __forceinline__ WordRaw<FMT> load_word(const Mat& w, uint32_t r, int u, int i, int K) {
+  WordRaw<FMT> x;
+  const int word = 4 * u + i;
+  const uint32_t at = r * row_bytes<FMT>(0, K);
   if constexpr (FMT == QMV_DENSE_BF16) {
-    r.q = reinterpret_cast<const u32x4*>(w.p[0])[word];
+    x.q = load_at<u32x4>(w.p[0], at, 16 * word);
   } else if constexpr (is_byte(FMT)) {
-    const u32x2 v = reinterpret_cast<const u32x2*>(w.p[0])[word];
-    r.q[0] = v[0];
-    r.q[1] = v[1];
+    const u32x2 v = load_at<u32x2>(w.p[0], at, 8 * word);
+    x.q[0] = v[0];
+    x.q[1] = v[1];
   } else {
-    r.q[0] = reinterpret_cast<const uint32_t*>(w.p[0])[word];
+    x.q[0] = load_at<uint32_t>(w.p[0], at, 4 * word);
   }
-  if constexpr (is_fifth(FMT)) r.qh = reinterpret_cast<const uint32_t*>(w.p[1])[row * (K >> 5) + u];
-  if constexpr (FMT == QMV_Q6K) r.qh = reinterpret_cast<const uint32_t*>(w.p[1])[row * (K >> 4) + 2 * u + (i >> 1)];
-  r.m = load_meta<FMT>(w, row, u, K);
-  return r;
+  if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
+  if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t>(w.p[1], r * row_bytes<FMT>(1, K), 8 * u + 4 * (i >> 1));
+  x.m = load_meta<FMT, true>(w, r, u, K);
+  return x;
 }
 
 template <int FMT>
@@ -305,18 +369,28 @@ __device__ __forceinline__ float gelu_tanh_arg(float g) {  // 2 sqrt(2/pi) (g + 
   return 1.5957691216057308f * fmaf(0.044715f * c * c, c, c);
 }
 
-__device__ __forceinline__ float act_value(int act, float g) {
-  if (act == QMV_ACT_SILU) return g * sigmoid16(g);
-  if (act == QMV_ACT_GELU_TANH) return g * sigmoid16(gelu_tanh_arg(g));
-  return 0.5f * g * erfcf(-0.70710678118654752f * g);
+// The activation is a template argument where many values go through one
+// (as a runtime choice every value paid for all three: 16 us per workgroup of
+// 256 x 128 outputs).
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+  if constexpr (ACT == QMV_ACT_SILU) return g * sigmoid16(g);
+  else if constexpr (ACT == QMV_ACT_GELU_TANH) return g * sigmoid16(gelu_tanh_arg(g));
+  else return 0.5f * g * erfcf(-0.70710678118654752f * g);
 }
 
-__device__ __forceinline__ void act_both(int act, float g, float& a, float& da) {
-  if (act == QMV_ACT_SILU) {
+__device__ __forceinline__ float act_of(int act, float g) {
+  return act == QMV_ACT_SILU ? act_value<QMV_ACT_SILU>(g)
+         : act == QMV_ACT_GELU_TANH ? act_value<QMV_ACT_GELU_TANH>(g) : act_value<QMV_ACT_GELU>(g);
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_both(float g, float& a, float& da) {
+  if constexpr (ACT == QMV_ACT_SILU) {
     const float s = sigmoid16(g);
     a = g * s;
     da = s * fmaf(g, 1.0f - s, 1.0f);
-  } else if (act == QMV_ACT_GELU_TANH) {
+  } else if constexpr (ACT == QMV_ACT_GELU_TANH) {
     const float s = sigmoid16(gelu_tanh_arg(g));
     const float c = fminf(fmaxf(g, -20.0f), 20.0f);
     a = g * s;

@@ -21,9 +21,9 @@ constexpr int kThreads = 256;
 // dG = dH U act'(G), dU = dH act(G), eight values per thread.  Each thread
 // reads its values before it writes them, so dG and dU may be any of the
 // inputs' buffers.  n values in all.
-template <bool F16>
+template <bool F16, int ACT>
 __global__ __launch_bounds__(kThreads) void glu_dgates_kernel(const uint16_t* g, const uint16_t* u, const uint16_t* dh,
-                                                              uint16_t* dg, uint16_t* du, int64_t n, int act) {
+                                                              uint16_t* dg, uint16_t* du, int64_t n) {
   const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8;
   if (at >= n) return;
   const bool whole = at + 8 <= n;
@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kThreads) void glu_dgates_kernel(const uint16_t* g,
     for (int e = 0; e < 2; ++e) {
       const uint32_t gw = gv[i], uw = uv[i], hw = hv[i];
       float av, da;
-      act_both(act, unpack16<F16>(e ? gw >> 16 : gw & 0xFFFFu), av, da);
+      act_both<ACT>(unpack16<F16>(e ? gw >> 16 : gw & 0xFFFFu), av, da);
       const float d = unpack16<F16>(e ? hw >> 16 : hw & 0xFFFFu);
       a[e] = d * unpack16<F16>(e ? uw >> 16 : uw & 0xFFFFu) * da;
       b[e] = d * av;
@@ -82,8 +82,7 @@ int glu_backward_splits(int64_t N, int64_t K, int64_t M) {
 hipError_t launch_glu_fwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_t* Wg, const uint8_t* Wu,
                           const uint16_t* X, bool f16, int act, uint16_t* H, uint16_t* G, uint16_t* U, hipStream_t s) {
   const Planes pl = planes_of(fmt, N, K);
-  GluFwdArgs p{mat_of(Wg, pl), mat_of(Wu, pl), X, H, G, U, int(M), int(N), int(K), act, 0};
-  p.vec = N % 4 == 0;  // bases are 16-byte aligned
+  const GluFwdArgs p{mat_of(Wg, pl), mat_of(Wu, pl), X, H, G, U, int(M), int(N), int(K), act};
   switch (fmt) {
     case QMV_W4A16_G64: case QMV_Q4K: case QMV_DENSE_BF16: return launch_glu_fwd_a(fmt, f16, p, s);
     case QMV_Q8_0: case QMV_Q6K: case QMV_I8_ROW: return launch_glu_fwd_b(fmt, f16, p, s);
@@ -97,8 +96,13 @@ hipError_t launch_glu_bwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_
   const Planes pl = planes_of(fmt, N, K);
   const int64_t mn = M * N, mk = M * K;
   const dim3 eg(static_cast<unsigned>((mn + 8 * kThreads - 1) / (8 * kThreads)));
-  if (f16) hipLaunchKernelGGL(glu_dgates_kernel<true>, eg, dim3(kThreads), 0, s, G, U, dH, dG, dU, mn, act);
-  else hipLaunchKernelGGL(glu_dgates_kernel<false>, eg, dim3(kThreads), 0, s, G, U, dH, dG, dU, mn, act);
+  auto gates = [&]<int ACT>() {
+    if (f16) hipLaunchKernelGGL((glu_dgates_kernel<true, ACT>), eg, dim3(kThreads), 0, s, G, U, dH, dG, dU, mn);
+    else hipLaunchKernelGGL((glu_dgates_kernel<false, ACT>), eg, dim3(kThreads), 0, s, G, U, dH, dG, dU, mn);
+  };
+  if (act == QMV_ACT_SILU) gates.template operator()<QMV_ACT_SILU>();
+  else if (act == QMV_ACT_GELU_TANH) gates.template operator()<QMV_ACT_GELU_TANH>();
+  else gates.template operator()<QMV_ACT_GELU>();
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int steps = int(2 * ((N + 63) / 64));

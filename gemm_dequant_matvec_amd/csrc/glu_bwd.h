@@ -46,14 +46,14 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
   auto load = [&](Set& s, int step) {
     const bool up = step >= half;
     const int nb = 64 * (up ? step - half : step);
-    const Mat& w = up ? p.wu : p.wg;
+    const Mat wn = from_row<FMT>(up ? p.wu : p.wg, nb, K);
     const uint16_t* d = up ? p.du : p.dg;
 #pragma unroll
     for (int j = 0; j < BPT; ++j) {
       const int id = (j * NT + tid) % BR, kg = id % KG, ng = id / KG;
       const int kw = min((k0 >> 3) + kg, (K >> 3) - 1);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s.w[j][e] = load_word<FMT>(w, min(nb + 8 * ng + e, N - 1), kw >> 2, kw & 3, K);
+      for (int e = 0; e < 8; ++e) s.w[j][e] = load_word<FMT>(wn, min(nb + 8 * ng + e, N - 1) - nb, kw >> 2, kw & 3, K);
     }
 #pragma unroll
     for (int j = 0; j < XPT; ++j) {
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
         for (int k = 0; k < 8; ++k) o[k][e] = pack16<F16>(ina ? a[k] : 0.0f, inb ? b[k] : 0.0f);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) As[buf][tile_at(8 * kg + k, ng)] = o[k];
+      for (int k = 0; k < 8; ++k) As[buf][tile_at_t(8 * kg + k, ng)] = o[k];
     }
   };
 
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
     for (int s = 0; s < 4; ++s) {
       u32x4 a[RB], b[TB];
 #pragma unroll
-      for (int i = 0; i < RB; ++i) a[i] = As[buf][tile_at((wr * RB + i) * 32 + fr, 2 * s + fh)];
+      for (int i = 0; i < RB; ++i) a[i] = As[buf][tile_at_t((wr * RB + i) * 32 + fr, 2 * s + fh)];
 #pragma unroll
       for (int i = 0; i < TB; ++i) b[i] = Xs[buf][tile_at((wt * TB + i) * 32 + fr, 2 * s + fh)];
 #pragma unroll
