@@ -152,12 +152,29 @@ __device__ __forceinline__ Mat from_row(const Mat& w, int64_t n, int K) {
   return m;
 }
 
+// Keeps a uniform address in scalar registers: without it the compiler adds the
+// lane offset first and carries a 64-bit address per lane and load through the
+// loop (and spills them).
+#define QMV_GLOBAL __attribute__((address_space(1)))
+__device__ __forceinline__ const QMV_GLOBAL uint8_t* scalar_base(const uint8_t* p) {
+  const QMV_GLOBAL uint8_t* g = (const QMV_GLOBAL uint8_t*)p;
+  asm volatile("" : "+s"(g));
+  return g;
+}
+
+// Keeps the widening of a lane offset next to its use, where it folds into the
+// address (hoisted out of the loop it becomes a 64-bit value per lane).
+__device__ __forceinline__ uint32_t lane_offset(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // A T at byte `row` (a lane's) + `u` of a plane.  LANE: u differs between lanes
 // too and joins the 32-bit offset; else it joins the scalar base.
 template <class T, bool LANE = true>
 __device__ __forceinline__ T load_at(const uint8_t* plane, uint32_t row, int64_t u = 0) {
   if constexpr (LANE) return *reinterpret_cast<const T*>(plane + (row + uint32_t(u)));
-  else return *reinterpret_cast<const T*>((plane + u) + row);
+  else return *(const QMV_GLOBAL T*)(scalar_base(plane + u) + lane_offset(row));
 }
 
 struct Affine {  // w = a t + b; a1, b1 for the second 16 weights (Q6K), else as a0, b0
@@ -311,6 +328,95 @@ __device__ __forceinline__ u32x4 unit_piece(const UnitRaw<FMT>& r, const Affine&
     decode8<FMT>(c, f, i, w);
     return u32x4{pack16<F16>(w[0], w[1]), pack16<F16>(w[2], w[3]), pack16<F16>(w[4], w[5]), pack16<F16>(w[6], w[7])};
   }
+}
+
+// Several consecutive units of one row, loaded together: about a 64-byte line
+// of codes, so that a line is fetched once and not again for every step (one
+// unit per step and lane fetched each 128-byte line four times, and its
+// scales' line 32 times: 222 us of loads alone under 162 us of MFMA).
+template <int FMT>
+constexpr int kRun = is_byte(FMT) || FMT == QMV_DENSE_BF16 ? 2 : 4;
+
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
+
+template <int FMT>
+struct RunRaw {
+  static constexpr int UQ = kRun<FMT>, NQ = UnitRaw<FMT>::NQ;
+  u32x4 q[UQ * NQ];
+  u32x4 qh[2];  // 16 (fifth bits) or 32 bytes (Q6K)
+  u32x4 m;
+  uint32_t d;
+};
+
+// Units u .. u + UQ - 1 of row r, u a multiple of UQ, all inside the row; u is
+// a lane's only in `half` (0 or 1 runs further).
+template <int FMT>
+__device__ __forceinline__ RunRaw<FMT> load_run(const Mat& w, uint32_t r, int u, int half, int K) {
+  RunRaw<FMT> x;
+  constexpr int UQ = kRun<FMT>, NQ = UnitRaw<FMT>::NQ;
+  const uint32_t at = r * row_bytes<FMT>(0, K) + half * (UQ * NQ * 16);
+#pragma unroll
+  for (int i = 0; i < UQ * NQ; ++i) x.q[i] = load_at<u32x4, false>(w.p[0], at, int64_t(u) * (16 * NQ) + 16 * i);
+  constexpr int P = kPlanes<FMT> - 1;
+  const uint32_t mt = r * row_bytes<FMT>(P, K);
+  if constexpr (is_fifth(FMT))
+    x.qh[0] = load_at<u32x4_a4, false>(w.p[1], r * row_bytes<FMT>(1, K) + 4 * UQ * half, 4 * u);
+  if constexpr (FMT == QMV_Q8_0) {
+    x.m[0] = load_at<u32_a2, false>(w.p[P], mt + 2 * UQ * half, 2 * u);
+  } else if constexpr (FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
+    const u32x2 v = load_at<u32x2_a2, false>(w.p[P], mt + 2 * UQ * half, 2 * u);
+    x.m[0] = v[0];
+    x.m[1] = v[1];
+  } else if constexpr (FMT == QMV_W4A16_G64) {
+    const u32x2 v = load_at<u32x2_a2, false>(w.p[P], mt + 2 * UQ * half, 2 * u);
+    x.m[0] = v[0];
+    x.m[1] = v[1];
+  } else if constexpr (is_super(FMT)) {
+    x.m = load_at<u32x4, false>(w.p[P], mt, 16 * (u >> 3));
+  } else if constexpr (FMT == QMV_Q6K) {
+    const uint32_t h = r * row_bytes<FMT>(1, K) + 32 * half;
+    x.qh[0] = load_at<u32x4, false>(w.p[1], h, 8 * u);
+    x.qh[1] = load_at<u32x4, false>(w.p[1], h, 8 * u + 16);
+    const u32x2 v = load_at<u32x2_a2, false>(w.p[2], r * row_bytes<FMT>(2, K) + 8 * half, 2 * u);
+    x.m[0] = v[0];
+    x.m[1] = v[1];
+    x.d = load_at<uint16_t, false>(w.p[3], mt, 2 * (u >> 3));
+  } else if constexpr (FMT == QMV_I8_ROW) {
+    x.m[0] = load_at<uint32_t>(w.p[1], mt);
+  }
+  return x;
+}
+
+// Unit j of a run (j known at compile time).
+template <int FMT>
+__device__ __forceinline__ UnitRaw<FMT> unit_of(const RunRaw<FMT>& x, int j) {
+  UnitRaw<FMT> u;
+  constexpr int NQ = UnitRaw<FMT>::NQ;
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) u.q[i] = x.q[j * NQ + i];
+  if constexpr (is_fifth(FMT)) u.qh[0] = x.qh[0][j];
+  if constexpr (FMT == QMV_Q6K) {
+    u.qh[0] = x.qh[j >> 1][2 * (j & 1)];
+    u.qh[1] = x.qh[j >> 1][2 * (j & 1) + 1];
+    u.m.v[0] = (x.m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+    u.m.v[1] = x.d;
+  } else if constexpr (FMT == QMV_Q8_0 || FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
+    u.m.v[0] = (x.m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+  } else if constexpr (FMT == QMV_W4A16_G64) {
+    u.m.v[0] = x.m[j >> 1];
+  } else {
+    u.m.v = x.m;
+  }
+  return u;
+}
+
+// 16 bytes from global memory straight into LDS: the wave's 64 pieces land at
+// `dst` (uniform) in lane order.
+__device__ __forceinline__ void copy_to_lds(const uint8_t* base, uint32_t off, u32x4* dst) {
+  __builtin_amdgcn_global_load_lds((const QMV_GLOBAL void*)(scalar_base(base) + lane_offset(off)),
+                                   (void __attribute__((address_space(3)))*)dst, 16, 0, 0);
 }
 
 // Eight weights (word i of unit u) of one row, as loaded, for the transposing

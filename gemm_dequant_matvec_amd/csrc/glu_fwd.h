@@ -1,6 +1,8 @@
 // The gated products of many tokens, H = act(X Wg^T) * (X Wu^T), on the matrix cores.
 #pragma once
 
+#include <utility>
+
 #include "gemm16.h"
 
 namespace qmv {
@@ -15,74 +17,54 @@ struct GluFwdArgs {
 namespace {
 
 // RB, TB: 32-row blocks of weights (half gate, half up) and of tokens per wave;
-// WR x WT waves.  A step takes 64 of K.
+// WR x WT waves.
+//
+// A step takes 64 of K, two units of every weight row.  Tokens go straight from
+// global memory to LDS, weights through registers: thread tid decodes one unit
+// per step and matrix half into the operand type, once per workgroup, and
+// writes it to LDS for the next step while the current step's products run.
+// UQ steps (a run) use the weights of one load: the first units of their steps
+// are the UQ consecutive units of the run's first half, the second ones those
+// of its other half; the tokens' pieces follow this order of k.  What is left
+// of K behind the last whole run goes step by step in plain order.
 template <int FMT, bool F16, int RB, int TB, int WR, int WT>
 __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs p) {
   constexpr int NT = 64 * WR * WT;
   constexpr int BR = 32 * RB * WR, BN = BR / 2, BM = 32 * TB * WT;
   constexpr int UPT = 2 * BR / NT;      // weight units per thread and step
   constexpr int XPT = BM * 8 / NT;      // 16-byte token pieces per thread and step
-  static_assert(UPT * NT == 2 * BR && XPT * NT == BM * 8 && RB % 2 == 0);
+  constexpr int UQ = kRun<FMT>;
+  static_assert(UPT * NT == 2 * BR && XPT * NT == BM * 8 && RB % 2 == 0 && UQ % 2 == 0);
 
-  __shared__ u32x4 As[2][BR * 8];
-  __shared__ u32x4 Xs[2][BM * 8];
-
-  // let the tiles' addresses escape: otherwise the compiler knows that no asm
+  // two of each, as variables of their own: the compiler then knows that a copy
+  // into one does not concern the reads of the other
+  __shared__ u32x4 A0[BR * 8], A1[BR * 8], X0[BM * 8], X1[BM * 8];
+  // let their addresses escape: otherwise the compiler knows that no asm
   // statement can touch them and moves LDS reads across the fences below
-  asm volatile("" ::"v"(&As[0][0]), "v"(&Xs[0][0]) : "memory");
+  asm volatile("" ::"v"(A0), "v"(A1), "v"(X0), "v"(X1) : "memory");
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / WT, wt = wave % WT;
   const TileId id0 = tile_of_block(p.N, BN, p.M, BM);
   const int n0 = id0.x * BN, m0 = id0.y * BM;
-  const int K = p.K, U = K >> 5, last = ((K + 63) >> 6) - 1;
+  const int K = p.K, U = K >> 5;
 
   // Thread tid stages units of weight row n0 + tid % BN: of the gate or the up
   // matrix and of which half of the step goes by wave, so that the addresses
   // are scalar bases and one lane offset per plane.
   const uint32_t wrow = min(n0 + tid % BN, p.N - 1) - n0;
-  const int wq = wave / (BN / 64);                       // gate / up and half of this wave's first unit
+  const int wq = wave / (BN / 64);  // gate / up and half of this wave's first unit
+  constexpr int QPW = 4 / UPT;      // (matrix, half) pairs that the waves cover at once
   const Mat wg = from_row<FMT>(p.wg, n0, K), wu = from_row<FMT>(p.wu, n0, K);
-  constexpr int QPW = (2 * BR / 64) / UPT / (BN / 64);   // (matrix, half) pairs that the waves cover at once
   const int arow = ((tid % BN) / (16 * RB)) * 32 * RB + (tid % BN) % (16 * RB);
-  // token pieces: row tid / 8 + j * NT / 8, piece tid % 8
+  // Token pieces: LDS slot tid + j * NT is row tid / 8 + j * NT / 8, piece
+  // c = 4 half + i by the tile's order.
   const uint8_t* xb = reinterpret_cast<const uint8_t*>(p.x + int64_t(m0) * K);
+  const int xc = (tid & 7) ^ ((tid >> 4) & 7);
   uint32_t xo[XPT];
 #pragma unroll
   for (int j = 0; j < XPT; ++j) xo[j] = uint32_t(min(m0 + j * (NT / 8) + (tid >> 3), p.M - 1) - m0) * uint32_t(2 * K);
-
-  struct Set {
-    UnitRaw<FMT> w[UPT];
-    u32x4 x[XPT];
-  };
-  auto load = [&](Set& s, int step) {
-    const int whole = 2 * step + 1 < U;  // else half a step: its first half twice
-#pragma unroll
-    for (int j = 0; j < UPT; ++j) {
-      const int q = wq + j * QPW, uu = q >> 1;
-      s.w[j] = load_unit<FMT, false>(q & 1 ? wu : wg, wrow, 2 * step + (whole ? uu : 0), K);
-    }
-    const uint32_t c = 16 * (tid & (whole ? 7 : 3));
-#pragma unroll
-    for (int j = 0; j < XPT; ++j) s.x[j] = load_at<u32x4>(xb + 128 * int64_t(step), xo[j] + c);
-  };
-  // part i (0..3) of a step's staging: word i of the thread's units, and its
-  // share of the token pieces
-  auto stage = [&](const Set& s, int step, int buf, int i) {
-#pragma unroll
-    for (int j = 0; j < XPT; ++j) {
-      if (j * 4 / XPT != i) continue;
-      const int id = j * NT + tid;
-      Xs[buf][tile_at(id >> 3, id & 7)] = s.x[j];
-    }
-#pragma unroll
-    for (int j = 0; j < UPT; ++j) {
-      const int q = wq + j * QPW, uu = q >> 1;
-      As[buf][tile_at(arow + (q & 1) * 16 * RB, 4 * uu + i)] =
-          unit_piece<FMT, F16>(s.w[j], affine_of<FMT>(s.w[j].m, 2 * step + uu), i);
-    }
-  };
 
   f32x16 acc[RB][TB];
 #pragma unroll
@@ -96,11 +78,11 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   struct Frag {
     u32x4 a[RB], b[TB];
   };
-  auto read = [&](Frag& f, int buf, int s) {
+  auto read = [&](Frag& f, const u32x4* A, const u32x4* X, int s) {
 #pragma unroll
-    for (int i = 0; i < RB; ++i) f.a[i] = As[buf][tile_at((wr * RB + i) * 32 + fr, 2 * s + fh)];
+    for (int i = 0; i < RB; ++i) f.a[i] = A[tile_at((wr * RB + i) * 32 + fr, 2 * s + fh)];
 #pragma unroll
-    for (int i = 0; i < TB; ++i) f.b[i] = Xs[buf][tile_at((wt * TB + i) * 32 + fr, 2 * s + fh)];
+    for (int i = 0; i < TB; ++i) f.b[i] = X[tile_at((wt * TB + i) * 32 + fr, 2 * s + fh)];
   };
   auto mul = [&](const Frag& f) {
 #pragma unroll
@@ -108,61 +90,110 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
 #pragma unroll
       for (int j = 0; j < TB; ++j) acc[i][j] = mfma32<F16>(f.a[i], f.b[j], acc[i][j]);
   };
-  // One step: products of buffer `buf` while the next step (already in `next`)
-  // is decoded into the other buffer and the one after it is loaded into `then`.
-  // The fences keep the loads at the top and the LDS traffic spread.
   auto fence = [] {
     asm volatile("" ::: "memory");
-#ifndef VAR_NOSB
     __builtin_amdgcn_sched_barrier(0);
-#endif
-  };
-  auto step = [&](int st, int buf, Set& then, const Set& next) {
-    Frag f0, f1;
-    read(f0, buf, 0);
-    load(then, min(st + 2, last));
-    fence();
-    read(f1, buf, 1);
-    stage(next, st + 1, buf ^ 1, 0);
-    mul(f0);
-    fence();
-    read(f0, buf, 2);
-    stage(next, st + 1, buf ^ 1, 1);
-    mul(f1);
-    fence();
-    read(f1, buf, 3);
-    stage(next, st + 1, buf ^ 1, 2);
-    mul(f0);
-    fence();
-    stage(next, st + 1, buf ^ 1, 3);
-    mul(f1);
-    lds_barrier16();
   };
 
-  // whole steps, then half a step (K is a multiple of 32): units and pieces
-  // past K are loaded from clamped addresses and never multiplied
-  const int nf = K >> 6;
-  Set s0, s1;
-  load(s0, 0);
-  load(s1, min(1, last));
+  // ---- whole runs
+  const int runs = U / (2 * UQ);
+  struct Set {
+    RunRaw<FMT> w[UPT];
+  };
+  auto load = [&](Set& s, int run) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) stage(s0, 0, 0, i);
-  lds_barrier16();
-  int st = 0;
-  for (; st + 1 < nf; st += 2) {
-    step(st, 0, s0, s1);
-    step(st + 1, 1, s1, s0);
+    for (int j = 0; j < UPT; ++j) {
+      const int q = wq + j * QPW;
+      s.w[j] = load_run<FMT>(q & 1 ? wu : wg, wrow, 2 * UQ * run, q >> 1, K);
+    }
+  };
+  // words i of unit j of each run into tile A
+  auto decode = [&](const Set& s, int run, int j, int i, u32x4* A) {
+#pragma unroll
+    for (int t = 0; t < UPT; ++t) {
+      const int q = wq + t * QPW, uu = q >> 1;
+      const UnitRaw<FMT> u = unit_of<FMT>(s.w[t], j);
+      A[tile_at(arow + (q & 1) * 16 * RB, 4 * uu + i)] =
+          unit_piece<FMT, F16>(u, affine_of<FMT>(u.m, 2 * UQ * run + UQ * uu + j), i);
+    }
+  };
+  const uint32_t xk = ((xc >> 2) * 32 * UQ + (xc & 3) * 8) * 2;  // this lane's piece of a run's step
+  auto copy_x = [&](int run, int j, u32x4* X) {
+    const uint8_t* b = xb + (int64_t(run) * (64 * UQ) + 32 * j) * 2;
+#pragma unroll
+    for (int t = 0; t < XPT; ++t) copy_to_lds(b, xo[t] + xk, X + t * NT + wave * 64);
+  };
+  if (runs > 0) {
+    Set cur, next;
+    load(cur, 0);
+    copy_x(0, 0, X0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) decode(cur, 0, 0, i, A0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier16();
+#pragma unroll 1
+    for (int run = 0; run < runs; ++run) {
+      const int then = min(run + 1, runs - 1);
+      [&]<int... J>(std::integer_sequence<int, J...>) {
+        (([&] {
+           constexpr bool odd = J & 1, end = J + 1 == UQ;
+           const u32x4 *A = odd ? A1 : A0, *X = odd ? X1 : X0;
+           u32x4 *An = odd ? A0 : A1, *Xn = odd ? X0 : X1;
+           Frag f0, f1;
+           read(f0, A, X, 0);
+           copy_x(end ? then : run, end ? 0 : J + 1, Xn);
+           if (J == 0) load(next, then);
+           fence();
+           auto dec = [&](int i) { decode(end ? next : cur, end ? then : run, end ? 0 : J + 1, i, An); };
+           read(f1, A, X, 1);
+           dec(0);
+           mul(f0);
+           fence();
+           read(f0, A, X, 2);
+           dec(1);
+           mul(f1);
+           fence();
+           read(f1, A, X, 3);
+           dec(2);
+           mul(f0);
+           fence();
+           dec(3);
+           mul(f1);
+           // this wave's copies into Xn have landed (the read makes the compiler
+           // wait for them, with a count that leaves younger loads in flight)
+           const uint32_t landed = reinterpret_cast<const uint32_t*>(Xn)[tid];
+           asm volatile("" ::"v"(landed));
+           lds_barrier16();
+         }()),
+         ...);
+      }(std::make_integer_sequence<int, UQ>{});
+      cur = next;
+    }
   }
-  if (st < nf) {
-    step(st, 0, s0, s1);
-    ++st;
-  }
-  if (K & 32) {
-    Frag f0, f1;
-    read(f0, st & 1, 0);
-    read(f1, st & 1, 1);
-    mul(f0);
-    mul(f1);
+
+  // ---- the rest of K, step by step
+  for (int u0 = runs * 2 * UQ; u0 < U; u0 += 2) {
+    const bool whole = u0 + 1 < U;  // else one unit: its pieces twice, the second half not multiplied
+#pragma unroll
+    for (int t = 0; t < XPT; ++t)
+      X0[tid + t * NT] = load_at<u32x4>(xb, xo[t] + 64 * u0 + 16 * (whole ? xc : xc & 3));
+#pragma unroll
+    for (int t = 0; t < UPT; ++t) {
+      const int q = wq + t * QPW, uu = q >> 1, u = u0 + (whole ? uu : 0);
+      const UnitRaw<FMT> r = load_unit<FMT, false>(q & 1 ? wu : wg, wrow, u, K);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        A0[tile_at(arow + (q & 1) * 16 * RB, 4 * uu + i)] = unit_piece<FMT, F16>(r, affine_of<FMT>(r.m, u), i);
+    }
+    lds_barrier16();
+    Frag f;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (s < 2 || whole) {
+        read(f, A0, X0, s);
+        mul(f);
+      }
+    lds_barrier16();
   }
 
   // C fragment: lane holds rows n = 8 q + 4 fh + e (q, e in 0..3) of token
@@ -170,7 +201,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   // are done with), so that rows of up to 128 bytes leave whole.
   lds_barrier16();
   constexpr int HB = RB / 2;                       // 32-row blocks of outputs
-  u32x4* mine = &As[0][0] + wave * (32 * 8);       // 32 tokens x 64 values
+  u32x4* mine = A0 + wave * (32 * 8);              // 32 tokens x 64 values
   const int nw = n0 + wr * HB * 32;
   auto put = [&](uint16_t* y, int j, auto value) {
 #pragma unroll
