@@ -85,6 +85,10 @@ __device__ __forceinline__ u32x4 load_part(const uint16_t* p, int n) {
 __device__ __forceinline__ int tile_at(int r, int c) {  // in 16-byte pieces
   return r * 8 + (c ^ ((r >> 1) & 7));
 }
+// The same for rows of 32 values (64 bytes, four pieces).
+__device__ __forceinline__ int tile32_at(int r, int c) {
+  return r * 4 + (c ^ ((r >> 2) & 3));
+}
 __device__ __forceinline__ int tile_at_t(int r, int c) {
   const int row = (r & ~1) | ((r ^ (r >> 6)) & 1);
   return row * 8 + (c ^ (((r >> 1) ^ (r >> 3)) & 7));
@@ -251,10 +255,9 @@ struct Word8 {
   uint32_t q0, q1, qh;
 };
 
-// Eight weights of word i (0..3) of a unit, in f32.
+// Eight weights a t + b of word i (0..3) of a unit, in f32.
 template <int FMT>
-__device__ __forceinline__ void decode8(const Word8& c, const Affine& f, int i, float (&w)[8]) {
-  const float a = (FMT == QMV_Q6K && i >= 2) ? f.a1 : f.a0, b = (FMT == QMV_Q6K && i >= 2) ? f.b1 : f.b0;
+__device__ __forceinline__ void decode8(const Word8& c, float a, float b, int i, float (&w)[8]) {
   if constexpr (is_byte(FMT)) {
     const uint32_t lo = c.q0 ^ 0x80808080u, hi = c.q1 ^ 0x80808080u;  // q + 128
 #pragma unroll
@@ -325,63 +328,142 @@ __device__ __forceinline__ u32x4 unit_piece(const UnitRaw<FMT>& r, const Affine&
     if constexpr (is_fifth(FMT)) c.qh = r.qh[0];
     if constexpr (FMT == QMV_Q6K) c.qh = r.qh[i >> 1];
     float w[8];
-    decode8<FMT>(c, f, i, w);
+    const bool second = FMT == QMV_Q6K && i >= 2;
+    decode8<FMT>(c, second ? f.a1 : f.a0, second ? f.b1 : f.b0, i, w);
     return u32x4{pack16<F16>(w[0], w[1]), pack16<F16>(w[2], w[3]), pack16<F16>(w[4], w[5]), pack16<F16>(w[6], w[7])};
   }
 }
 
-// Several consecutive units of one row, loaded together: about a 64-byte line
-// of codes, so that a line is fetched once and not again for every step (one
-// unit per step and lane fetched each 128-byte line four times, and its
-// scales' line 32 times: 222 us of loads alone under 162 us of MFMA).
+// Half a unit: words 2 h and 2 h + 1 (16 weights), and the halves of kRun
+// consecutive units of one row, loaded together: the lines of codes and scales
+// are then fetched once and not again for every stage (one unit per step and
+// lane fetched each 128-byte line of codes four times, and its scales' line 32
+// times: 222 us of loads alone under 162 us of MFMA).
 template <int FMT>
-constexpr int kRun = is_byte(FMT) || FMT == QMV_DENSE_BF16 ? 2 : 4;
+constexpr int kRun = is_byte(FMT) || FMT == QMV_DENSE_BF16 ? 4 : 8;
 
-typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+template <int FMT>
+struct HalfRaw {
+  u32x4 q[2];  // codes: two dwords; 8-bit: four; dense: eight
+  uint32_t qh;
+  MetaRaw<FMT> m;
+};
+
+// Offset and bytes of half a unit's codes.
+template <int FMT>
+constexpr int kHalfBytes = FMT == QMV_DENSE_BF16 ? 32 : is_byte(FMT) ? 16 : 8;
+
+template <int FMT, bool LANE>
+__device__ __forceinline__ void load_half_codes(u32x4 (&q)[2], const Mat& w, uint32_t r, int u, int h, int K) {
+  constexpr int B = kHalfBytes<FMT>;
+  const uint32_t at = r * row_bytes<FMT>(0, K) + B * h;
+  const int64_t ub = int64_t(u) * (2 * B);
+  if constexpr (B == 8) {
+    const u32x2 v = load_at<u32x2, LANE>(w.p[0], at, ub);
+    q[0][0] = v[0];
+    q[0][1] = v[1];
+  } else {
+    q[0] = load_at<u32x4, LANE>(w.p[0], at, ub);
+    if constexpr (B == 32) q[1] = load_at<u32x4, LANE>(w.p[0], at, ub + 16);
+  }
+}
+
+// Half h (a lane's) of unit u.
+template <int FMT>
+__device__ __forceinline__ HalfRaw<FMT> load_half(const Mat& w, uint32_t r, int u, int h, int K) {
+  HalfRaw<FMT> x;
+  load_half_codes<FMT, false>(x.q, w, r, u, h, K);
+  if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t, false>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
+  if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t, false>(w.p[1], r * row_bytes<FMT>(1, K) + 4 * h, 8 * u);
+  x.m = load_meta<FMT, false>(w, r, u, K);
+  return x;
+}
+
+// Word i (0, 1) of half h of unit u as one 16-byte piece.
+template <int FMT, bool F16>
+__device__ __forceinline__ u32x4 half_piece(const HalfRaw<FMT>& r, int u, int h, int i) {
+  if constexpr (FMT == QMV_DENSE_BF16) {
+    if constexpr (!F16) return r.q[i];
+    u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t v = r.q[i][e];
+      o[e] = pack16<F16>(bf16_bits_to_f32(v & 0xFFFFu), bf16_bits_to_f32(v >> 16));
+    }
+    return o;
+  } else {
+    Word8 c;
+    if constexpr (is_byte(FMT)) {
+      c.q0 = r.q[0][2 * i];
+      c.q1 = r.q[0][2 * i + 1];
+    } else {
+      c.q0 = r.q[0][i];
+    }
+    c.qh = r.qh;
+    const Affine f = affine_of<FMT>(r.m, u);
+    float w[8];
+    // Q6K: h selects the sub-block; word 2 h + i's high bits are those of word i
+    decode8<FMT>(c, FMT == QMV_Q6K && h ? f.a1 : f.a0, FMT == QMV_Q6K && h ? f.b1 : f.b0, FMT == QMV_Q6K ? i : 2 * h + i, w);
+    return u32x4{pack16<F16>(w[0], w[1]), pack16<F16>(w[2], w[3]), pack16<F16>(w[4], w[5]), pack16<F16>(w[6], w[7])};
+  }
+}
+
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-typedef uint32_t u32_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
 template <int FMT>
 struct RunRaw {
-  static constexpr int UQ = kRun<FMT>, NQ = UnitRaw<FMT>::NQ;
-  u32x4 q[UQ * NQ];
-  u32x4 qh[2];  // 16 (fifth bits) or 32 bytes (Q6K)
-  u32x4 m;
+  u32x4 q[kRun<FMT> * (FMT == QMV_DENSE_BF16 ? 2 : 1)];
+  uint32_t qh[8];
+  u32x4 m;  // the scales of the whole run
   uint32_t d;
 };
 
-// Units u .. u + UQ - 1 of row r, u a multiple of UQ, all inside the row; u is
-// a lane's only in `half` (0 or 1 runs further).
+// Loads of codes in load_run, one instruction each at least.
 template <int FMT>
-__device__ __forceinline__ RunRaw<FMT> load_run(const Mat& w, uint32_t r, int u, int half, int K) {
+constexpr int kRunLoads = kRun<FMT> * (FMT == QMV_DENSE_BF16 ? 2 : 1);
+
+// Halves h of units u .. u + kRun - 1; u is a multiple of kRun and the run is
+// inside the row.
+template <int FMT>
+__device__ __forceinline__ RunRaw<FMT> load_run(const Mat& w, uint32_t r, int u, int h, int K) {
   RunRaw<FMT> x;
-  constexpr int UQ = kRun<FMT>, NQ = UnitRaw<FMT>::NQ;
-  const uint32_t at = r * row_bytes<FMT>(0, K) + half * (UQ * NQ * 16);
+  constexpr int S = kRun<FMT>, P = kPlanes<FMT> - 1;
 #pragma unroll
-  for (int i = 0; i < UQ * NQ; ++i) x.q[i] = load_at<u32x4, false>(w.p[0], at, int64_t(u) * (16 * NQ) + 16 * i);
-  constexpr int P = kPlanes<FMT> - 1;
-  const uint32_t mt = r * row_bytes<FMT>(P, K);
-  if constexpr (is_fifth(FMT))
-    x.qh[0] = load_at<u32x4_a4, false>(w.p[1], r * row_bytes<FMT>(1, K) + 4 * UQ * half, 4 * u);
+  for (int s = 0; s < S; ++s) {
+    u32x4 q[2];
+    load_half_codes<FMT, false>(q, w, r, u + s, h, K);
+    if constexpr (FMT == QMV_DENSE_BF16) {
+      x.q[2 * s] = q[0];
+      x.q[2 * s + 1] = q[1];
+    } else {
+      x.q[s] = q[0];
+    }
+  }
+  const uint32_t mt = r * row_bytes<FMT>(P, K), ht = r * row_bytes<FMT>(1, K);
+  if constexpr (is_fifth(FMT)) {
+    const u32x4 a = load_at<u32x4_a4, false>(w.p[1], ht, 4 * u), b = load_at<u32x4_a4, false>(w.p[1], ht, 4 * u + 16);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      x.qh[s] = a[s];
+      x.qh[4 + s] = b[s];
+    }
+  }
   if constexpr (FMT == QMV_Q8_0) {
-    x.m[0] = load_at<u32_a2, false>(w.p[P], mt + 2 * UQ * half, 2 * u);
+    const u32x2 v = load_at<u32x2_a2, false>(w.p[P], mt, 2 * u);
+    x.m[0] = v[0];
+    x.m[1] = v[1];
   } else if constexpr (FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
-    const u32x2 v = load_at<u32x2_a2, false>(w.p[P], mt + 2 * UQ * half, 2 * u);
-    x.m[0] = v[0];
-    x.m[1] = v[1];
+    x.m = load_at<u32x4_a2, false>(w.p[P], mt, 2 * u);
   } else if constexpr (FMT == QMV_W4A16_G64) {
-    const u32x2 v = load_at<u32x2_a2, false>(w.p[P], mt + 2 * UQ * half, 2 * u);
-    x.m[0] = v[0];
-    x.m[1] = v[1];
+    x.m = load_at<u32x4_a4, false>(w.p[P], mt, 2 * u);
   } else if constexpr (is_super(FMT)) {
     x.m = load_at<u32x4, false>(w.p[P], mt, 16 * (u >> 3));
   } else if constexpr (FMT == QMV_Q6K) {
-    const uint32_t h = r * row_bytes<FMT>(1, K) + 32 * half;
-    x.qh[0] = load_at<u32x4, false>(w.p[1], h, 8 * u);
-    x.qh[1] = load_at<u32x4, false>(w.p[1], h, 8 * u + 16);
-    const u32x2 v = load_at<u32x2_a2, false>(w.p[2], r * row_bytes<FMT>(2, K) + 8 * half, 2 * u);
-    x.m[0] = v[0];
-    x.m[1] = v[1];
+#pragma unroll
+    for (int s = 0; s < S; ++s) x.qh[s] = load_at<uint32_t, false>(w.p[1], ht + 4 * h, 8 * (u + s));
+    x.m = load_at<u32x4, false>(w.p[2], r * row_bytes<FMT>(2, K), 2 * u);
     x.d = load_at<uint16_t, false>(w.p[3], mt, 2 * (u >> 3));
   } else if constexpr (FMT == QMV_I8_ROW) {
     x.m[0] = load_at<uint32_t>(w.p[1], mt);
@@ -389,27 +471,26 @@ __device__ __forceinline__ RunRaw<FMT> load_run(const Mat& w, uint32_t r, int u,
   return x;
 }
 
-// Unit j of a run (j known at compile time).
+// The half of unit u + s of a run (s known at compile time).
 template <int FMT>
-__device__ __forceinline__ UnitRaw<FMT> unit_of(const RunRaw<FMT>& x, int j) {
-  UnitRaw<FMT> u;
-  constexpr int NQ = UnitRaw<FMT>::NQ;
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) u.q[i] = x.q[j * NQ + i];
-  if constexpr (is_fifth(FMT)) u.qh[0] = x.qh[0][j];
-  if constexpr (FMT == QMV_Q6K) {
-    u.qh[0] = x.qh[j >> 1][2 * (j & 1)];
-    u.qh[1] = x.qh[j >> 1][2 * (j & 1) + 1];
-    u.m.v[0] = (x.m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-    u.m.v[1] = x.d;
-  } else if constexpr (FMT == QMV_Q8_0 || FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
-    u.m.v[0] = (x.m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-  } else if constexpr (FMT == QMV_W4A16_G64) {
-    u.m.v[0] = x.m[j >> 1];
+__device__ __forceinline__ HalfRaw<FMT> half_of(const RunRaw<FMT>& x, int s) {
+  HalfRaw<FMT> r;
+  if constexpr (FMT == QMV_DENSE_BF16) {
+    r.q[0] = x.q[2 * s];
+    r.q[1] = x.q[2 * s + 1];
   } else {
-    u.m.v = x.m;
+    r.q[0] = x.q[s];
   }
-  return u;
+  r.qh = x.qh[s];
+  if constexpr (FMT == QMV_Q6K || FMT == QMV_Q8_0 || FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
+    r.m.v[0] = (x.m[s >> 1] >> (16 * (s & 1))) & 0xFFFFu;
+    r.m.v[1] = x.d;
+  } else if constexpr (FMT == QMV_W4A16_G64) {
+    r.m.v[0] = x.m[s >> 1];
+  } else {
+    r.m.v = x.m;
+  }
+  return r;
 }
 
 // 16 bytes from global memory straight into LDS: the wave's 64 pieces land at
@@ -461,7 +542,8 @@ __device__ __forceinline__ void word_values(const WordRaw<FMT>& r, int u, int i,
   } else {
     const Word8 c{r.q[0], r.q[1], r.qh};
     const Affine f = affine_of<FMT>(r.m, u);
-    decode8<FMT>(c, f, i, w);
+    const bool second = FMT == QMV_Q6K && i >= 2;
+    decode8<FMT>(c, second ? f.a1 : f.a0, second ? f.b1 : f.b0, i, w);
   }
 }
 

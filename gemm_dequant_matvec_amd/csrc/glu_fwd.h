@@ -19,29 +19,32 @@ namespace {
 // RB, TB: 32-row blocks of weights (half gate, half up) and of tokens per wave;
 // WR x WT waves.
 //
-// A step takes 64 of K, two units of every weight row.  Tokens go straight from
-// global memory to LDS, weights through registers: thread tid decodes one unit
-// per step and matrix half into the operand type, once per workgroup, and
-// writes it to LDS for the next step while the current step's products run.
-// UQ steps (a run) use the weights of one load: the first units of their steps
-// are the UQ consecutive units of the run's first half, the second ones those
-// of its other half; the tokens' pieces follow this order of k.  What is left
-// of K behind the last whole run goes step by step in plain order.
+// K goes by in stages of 32: one unit of every weight row and 64 bytes of every
+// token, in a ring of four LDS tiles each.  Tokens go straight from global
+// memory to LDS, three stages ahead; weights go through registers: a pair of
+// threads decodes one unit into the operand type, once per workgroup, two
+// stages ahead.  The first fragments of a stage are
+// read before the barrier that ends the stage before it, so no wave waits for
+// LDS behind a barrier (with 64-deep steps in two buffers, all read after the
+// barrier, a step took 1.85 us for 0.92 us of MFMA).
 template <int FMT, bool F16, int RB, int TB, int WR, int WT>
 __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs p) {
   constexpr int NT = 64 * WR * WT;
   constexpr int BR = 32 * RB * WR, BN = BR / 2, BM = 32 * TB * WT;
-  constexpr int UPT = 2 * BR / NT;      // weight units per thread and step
-  constexpr int XPT = BM * 8 / NT;      // 16-byte token pieces per thread and step
-  constexpr int UQ = kRun<FMT>;
-  static_assert(UPT * NT == 2 * BR && XPT * NT == BM * 8 && RB % 2 == 0 && UQ % 2 == 0);
+  constexpr int XPT = BM * 4 / NT;      // 16-byte token pieces per thread and stage
+  constexpr int SR = kRun<FMT>;          // stages per run
+  static_assert(2 * BR == NT && XPT * NT == BM * 4 && RB % 2 == 0 && SR % 4 == 0);
 
-  // two of each, as variables of their own: the compiler then knows that a copy
-  // into one does not concern the reads of the other
-  __shared__ u32x4 A0[BR * 8], A1[BR * 8], X0[BM * 8], X1[BM * 8];
+  // variables of their own: the compiler then knows that a copy into one does
+  // not concern the reads of the others
+  __shared__ u32x4 A0[BR * 4], A1[BR * 4], A2[BR * 4], A3[BR * 4];
+  __shared__ u32x4 X0[BM * 4], X1[BM * 4], X2[BM * 4], X3[BM * 4];
   // let their addresses escape: otherwise the compiler knows that no asm
   // statement can touch them and moves LDS reads across the fences below
-  asm volatile("" ::"v"(A0), "v"(A1), "v"(X0), "v"(X1) : "memory");
+  asm volatile("" ::"v"(A0), "v"(A1), "v"(A2), "v"(A3) : "memory");
+  asm volatile("" ::"v"(X0), "v"(X1), "v"(X2), "v"(X3) : "memory");
+  auto At = [&]<int S>() { return (S & 3) == 0 ? A0 : (S & 3) == 1 ? A1 : (S & 3) == 2 ? A2 : A3; };
+  auto Xt = [&]<int S>() { return (S & 3) == 0 ? X0 : (S & 3) == 1 ? X1 : (S & 3) == 2 ? X2 : X3; };
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -50,21 +53,21 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   const int n0 = id0.x * BN, m0 = id0.y * BM;
   const int K = p.K, U = K >> 5;
 
-  // Thread tid stages units of weight row n0 + tid % BN: of the gate or the up
-  // matrix and of which half of the step goes by wave, so that the addresses
-  // are scalar bases and one lane offset per plane.
-  const uint32_t wrow = min(n0 + tid % BN, p.N - 1) - n0;
-  const int wq = wave / (BN / 64);  // gate / up and half of this wave's first unit
-  constexpr int QPW = 4 / UPT;      // (matrix, half) pairs that the waves cover at once
-  const Mat wg = from_row<FMT>(p.wg, n0, K), wu = from_row<FMT>(p.wu, n0, K);
-  const int arow = ((tid % BN) / (16 * RB)) * 32 * RB + (tid % BN) % (16 * RB);
-  // Token pieces: LDS slot tid + j * NT is row tid / 8 + j * NT / 8, piece
-  // c = 4 half + i by the tile's order.
+  // Threads 2 i and 2 i + 1 decode the halves of weight row i: gate or up goes
+  // by wave, so that the addresses are scalar bases and one lane offset per
+  // plane.
+  const int half = tid & 1, ri = tid >> 1;
+  const bool up = wave >= WR * WT / 2;
+  const uint32_t wrow = min(n0 + ri % BN, p.N - 1) - n0;
+  const Mat w = from_row<FMT>(up ? p.wu : p.wg, n0, K);
+  const int arow = ((ri % BN) / (16 * RB)) * 32 * RB + (ri % BN) % (16 * RB) + (up ? 16 * RB : 0);
+  // Token pieces: LDS slot tid + t * NT of a tile is row (tid + t * NT) / 4.
   const uint8_t* xb = reinterpret_cast<const uint8_t*>(p.x + int64_t(m0) * K);
-  const int xc = (tid & 7) ^ ((tid >> 4) & 7);
   uint32_t xo[XPT];
 #pragma unroll
-  for (int j = 0; j < XPT; ++j) xo[j] = uint32_t(min(m0 + j * (NT / 8) + (tid >> 3), p.M - 1) - m0) * uint32_t(2 * K);
+  for (int t = 0; t < XPT; ++t)
+    xo[t] = uint32_t(min(m0 + t * (NT / 4) + (tid >> 2), p.M - 1) - m0) * uint32_t(2 * K) +
+            16 * ((tid & 3) ^ ((tid >> 4) & 3));
 
   f32x16 acc[RB][TB];
 #pragma unroll
@@ -80,9 +83,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   };
   auto read = [&](Frag& f, const u32x4* A, const u32x4* X, int s) {
 #pragma unroll
-    for (int i = 0; i < RB; ++i) f.a[i] = A[tile_at((wr * RB + i) * 32 + fr, 2 * s + fh)];
+    for (int i = 0; i < RB; ++i) f.a[i] = A[tile32_at((wr * RB + i) * 32 + fr, 2 * s + fh)];
 #pragma unroll
-    for (int i = 0; i < TB; ++i) f.b[i] = X[tile_at((wt * TB + i) * 32 + fr, 2 * s + fh)];
+    for (int i = 0; i < TB; ++i) f.b[i] = X[tile32_at((wt * TB + i) * 32 + fr, 2 * s + fh)];
   };
   auto mul = [&](const Frag& f) {
 #pragma unroll
@@ -94,105 +97,83 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
+  auto copy_x = [&](int u, u32x4* X) {  // unit u of the tokens
+#pragma unroll
+    for (int t = 0; t < XPT; ++t) copy_to_lds(xb + 64 * int64_t(u), xo[t], X + t * NT + wave * 64);
+  };
 
   // ---- whole runs
-  const int runs = U / (2 * UQ);
-  struct Set {
-    RunRaw<FMT> w[UPT];
-  };
-  auto load = [&](Set& s, int run) {
-#pragma unroll
-    for (int j = 0; j < UPT; ++j) {
-      const int q = wq + j * QPW;
-      s.w[j] = load_run<FMT>(q & 1 ? wu : wg, wrow, 2 * UQ * run, q >> 1, K);
-    }
-  };
-  // words i of unit j of each run into tile A
-  auto decode = [&](const Set& s, int run, int j, int i, u32x4* A) {
-#pragma unroll
-    for (int t = 0; t < UPT; ++t) {
-      const int q = wq + t * QPW, uu = q >> 1;
-      const UnitRaw<FMT> u = unit_of<FMT>(s.w[t], j);
-      A[tile_at(arow + (q & 1) * 16 * RB, 4 * uu + i)] =
-          unit_piece<FMT, F16>(u, affine_of<FMT>(u.m, 2 * UQ * run + UQ * uu + j), i);
-    }
-  };
-  const uint32_t xk = ((xc >> 2) * 32 * UQ + (xc & 3) * 8) * 2;  // this lane's piece of a run's step
-  auto copy_x = [&](int run, int j, u32x4* X) {
-    const uint8_t* b = xb + (int64_t(run) * (64 * UQ) + 32 * j) * 2;
-#pragma unroll
-    for (int t = 0; t < XPT; ++t) copy_to_lds(b, xo[t] + xk, X + t * NT + wave * 64);
-  };
+  const int runs = U / SR;
   if (runs > 0) {
-    Set cur, next;
-    load(cur, 0);
-    copy_x(0, 0, X0);
+    const int last = runs * SR - 1;
+    RunRaw<FMT> cur, next;
+    auto decode = [&](const RunRaw<FMT>& x, int u, int s, int i, u32x4* A) {  // u: unit of stage s
+      A[tile32_at(arow, 2 * half + i)] = half_piece<FMT, F16>(half_of<FMT>(x, s), u, half, i);
+    };
+    cur = load_run<FMT>(w, wrow, 0, half, K);
+    copy_x(0, X0);
+    copy_x(1, X1);
+    copy_x(2, X2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) decode(cur, 0, 0, i, A0);
+    for (int i = 0; i < 2; ++i) {
+      decode(cur, 0, 0, i, A0);
+      decode(cur, 1, 1, i, A1);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier16();
+    Frag f0, f1;
+    read(f0, A0, X0, 0);
 #pragma unroll 1
     for (int run = 0; run < runs; ++run) {
-      const int then = min(run + 1, runs - 1);
-      [&]<int... J>(std::integer_sequence<int, J...>) {
+      const int u0 = run * SR, then = min(u0 + SR, last + 1 - SR);
+      [&]<int... H>(std::integer_sequence<int, H...>) {
         (([&] {
-           constexpr bool odd = J & 1, end = J + 1 == UQ;
-           const u32x4 *A = odd ? A1 : A0, *X = odd ? X1 : X0;
-           u32x4 *An = odd ? A0 : A1, *Xn = odd ? X0 : X1;
-           Frag f0, f1;
-           read(f0, A, X, 0);
-           copy_x(end ? then : run, end ? 0 : J + 1, Xn);
-           if (J == 0) load(next, then);
+           const u32x4 *A = At.template operator()<H>(), *X = Xt.template operator()<H>();
+           const u32x4 *A1n = At.template operator()<H + 1>(), *X1n = Xt.template operator()<H + 1>();
+           u32x4* A2n = At.template operator()<H + 2>();
+           auto dec = [&](int i) {
+             if constexpr (H + 2 >= SR) decode(next, then + H + 2 - SR, H + 2 - SR, i, A2n);
+             else decode(cur, u0 + H + 2, H + 2, i, A2n);
+           };
+           copy_x(min(u0 + H + 3, last), Xt.template operator()<H + 3>());
            fence();
-           auto dec = [&](int i) { decode(end ? next : cur, end ? then : run, end ? 0 : J + 1, i, An); };
+           if constexpr (H == 0) next = load_run<FMT>(w, wrow, then, half, K);
            read(f1, A, X, 1);
            dec(0);
            mul(f0);
            fence();
-           read(f0, A, X, 2);
+           read(f0, A1n, X1n, 0);
            dec(1);
            mul(f1);
            fence();
-           read(f1, A, X, 3);
-           dec(2);
-           mul(f0);
-           fence();
-           dec(3);
-           mul(f1);
-           // this wave's copies into Xn have landed (the read makes the compiler
-           // wait for them, with a count that leaves younger loads in flight)
-           const uint32_t landed = reinterpret_cast<const uint32_t*>(Xn)[tid];
-           asm volatile("" ::"v"(landed));
+           // Stage H + 2 is whole once the copies of the stage before this one have
+           // landed.  Certainly issued after those: this stage's copies, and in a
+           // run's first two stages the loads of the next run's codes.
+           asm volatile("s_waitcnt vmcnt(%0)" ::"n"(XPT + (H < 2 ? kRunLoads<FMT> : 0)) : "memory");
            lds_barrier16();
          }()),
          ...);
-      }(std::make_integer_sequence<int, UQ>{});
+      }(std::make_integer_sequence<int, SR>{});
       cur = next;
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the copies past the end
+    lds_barrier16();
   }
 
-  // ---- the rest of K, step by step
-  for (int u0 = runs * 2 * UQ; u0 < U; u0 += 2) {
-    const bool whole = u0 + 1 < U;  // else one unit: its pieces twice, the second half not multiplied
+  // ---- the rest of K, one unit at a time
+  for (int u = runs * SR; u < U; ++u) {
 #pragma unroll
-    for (int t = 0; t < XPT; ++t)
-      X0[tid + t * NT] = load_at<u32x4>(xb, xo[t] + 64 * u0 + 16 * (whole ? xc : xc & 3));
+    for (int t = 0; t < XPT; ++t) X0[tid + t * NT] = load_at<u32x4>(xb, xo[t] + 64 * u);
+    const HalfRaw<FMT> r = load_half<FMT>(w, wrow, u, half, K);
 #pragma unroll
-    for (int t = 0; t < UPT; ++t) {
-      const int q = wq + t * QPW, uu = q >> 1, u = u0 + (whole ? uu : 0);
-      const UnitRaw<FMT> r = load_unit<FMT, false>(q & 1 ? wu : wg, wrow, u, K);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        A0[tile_at(arow + (q & 1) * 16 * RB, 4 * uu + i)] = unit_piece<FMT, F16>(r, affine_of<FMT>(r.m, u), i);
-    }
+    for (int i = 0; i < 2; ++i) A0[tile32_at(arow, 2 * half + i)] = half_piece<FMT, F16>(r, u, half, i);
     lds_barrier16();
     Frag f;
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      if (s < 2 || whole) {
-        read(f, A0, X0, s);
-        mul(f);
-      }
+    for (int s = 0; s < 2; ++s) {
+      read(f, A0, X0, s);
+      mul(f);
+    }
     lds_barrier16();
   }
 
@@ -201,7 +182,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   // are done with), so that rows of up to 128 bytes leave whole.
   lds_barrier16();
   constexpr int HB = RB / 2;                       // 32-row blocks of outputs
-  u32x4* mine = A0 + wave * (32 * 8);              // 32 tokens x 64 values
+  u32x4* mine = (wave & 1 ? A1 : A0) + (wave >> 1) * (32 * 8);  // 32 tokens x 64 values
   const int nw = n0 + wr * HB * 32;
   auto put = [&](uint16_t* y, int j, auto value) {
 #pragma unroll
