@@ -334,13 +334,16 @@ __device__ __forceinline__ u32x4 unit_piece(const UnitRaw<FMT>& r, const Affine&
   }
 }
 
-// Half a unit: words 2 h and 2 h + 1 (16 weights), and the halves of kRun
-// consecutive units of one row, loaded together: the lines of codes and scales
-// are then fetched once and not again for every stage (one unit per step and
-// lane fetched each 128-byte line of codes four times, and its scales' line 32
-// times: 222 us of loads alone under 162 us of MFMA).
+// Half a unit: words 2 h and 2 h + 1 (16 weights).  The codes of kChunk
+// consecutive units of a row are 64 bytes, which go to LDS as they are (a line
+// is then fetched once, by four neighbouring lanes; one unit per step and lane
+// instead fetched each 128-byte line four times, and its scales' line 32 times:
+// 222 us of loads alone under 162 us of MFMA).  The scales of kRun units are
+// loaded together.
 template <int FMT>
-constexpr int kRun = is_byte(FMT) || FMT == QMV_DENSE_BF16 ? 4 : 8;
+constexpr int kChunk = FMT == QMV_DENSE_BF16 ? 1 : is_byte(FMT) ? 2 : 4;
+template <int FMT>
+constexpr int kRun = kChunk<FMT> == 4 ? 8 : 4;
 
 template <int FMT>
 struct HalfRaw {
@@ -349,30 +352,36 @@ struct HalfRaw {
   MetaRaw<FMT> m;
 };
 
-// Offset and bytes of half a unit's codes.
+// A tile of 64-byte rows of codes: the half h of unit s of row r (0 <= s < kChunk).
 template <int FMT>
-constexpr int kHalfBytes = FMT == QMV_DENSE_BF16 ? 32 : is_byte(FMT) ? 16 : 8;
-
-template <int FMT, bool LANE>
-__device__ __forceinline__ void load_half_codes(u32x4 (&q)[2], const Mat& w, uint32_t r, int u, int h, int K) {
-  constexpr int B = kHalfBytes<FMT>;
-  const uint32_t at = r * row_bytes<FMT>(0, K) + B * h;
-  const int64_t ub = int64_t(u) * (2 * B);
-  if constexpr (B == 8) {
-    const u32x2 v = load_at<u32x2, LANE>(w.p[0], at, ub);
+__device__ __forceinline__ void read_codes(u32x4 (&q)[2], const u32x4* R, int r, int s, int h) {
+  if constexpr (FMT == QMV_DENSE_BF16) {
+    q[0] = R[tile32_at(r, 2 * h)];
+    q[1] = R[tile32_at(r, 2 * h + 1)];
+  } else if constexpr (is_byte(FMT)) {
+    q[0] = R[tile32_at(r, 2 * s + h)];
+  } else {
+    const u32x2 v = reinterpret_cast<const u32x2*>(R + tile32_at(r, s))[h];
     q[0][0] = v[0];
     q[0][1] = v[1];
-  } else {
-    q[0] = load_at<u32x4, LANE>(w.p[0], at, ub);
-    if constexpr (B == 32) q[1] = load_at<u32x4, LANE>(w.p[0], at, ub + 16);
   }
 }
 
-// Half h (a lane's) of unit u.
+// Half h (a lane's) of unit u, from global memory.
 template <int FMT>
 __device__ __forceinline__ HalfRaw<FMT> load_half(const Mat& w, uint32_t r, int u, int h, int K) {
   HalfRaw<FMT> x;
-  load_half_codes<FMT, false>(x.q, w, r, u, h, K);
+  constexpr int B = 32 / kChunk<FMT>;  // bytes of half a unit's codes
+  const uint32_t at = r * row_bytes<FMT>(0, K) + B * h;
+  const int64_t ub = int64_t(u) * (2 * B);
+  if constexpr (B == 8) {
+    const u32x2 v = load_at<u32x2, false>(w.p[0], at, ub);
+    x.q[0][0] = v[0];
+    x.q[0][1] = v[1];
+  } else {
+    x.q[0] = load_at<u32x4, false>(w.p[0], at, ub);
+    if constexpr (B == 32) x.q[1] = load_at<u32x4, false>(w.p[0], at, ub + 16);
+  }
   if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t, false>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
   if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t, false>(w.p[1], r * row_bytes<FMT>(1, K) + 4 * h, 8 * u);
   x.m = load_meta<FMT, false>(w, r, u, K);
@@ -412,35 +421,24 @@ typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
+// The scales and high bits of a run, for half h.
 template <int FMT>
-struct RunRaw {
-  u32x4 q[kRun<FMT> * (FMT == QMV_DENSE_BF16 ? 2 : 1)];
+struct RunMeta {
   uint32_t qh[8];
-  u32x4 m;  // the scales of the whole run
+  u32x4 m;
   uint32_t d;
 };
 
-// Loads of codes in load_run, one instruction each at least.
+// Loads of load_run_meta, at least.
 template <int FMT>
-constexpr int kRunLoads = kRun<FMT> * (FMT == QMV_DENSE_BF16 ? 2 : 1);
+constexpr int kMetaLoads = FMT == QMV_DENSE_BF16 ? 0 : is_fifth(FMT) ? 3 : FMT == QMV_Q6K ? 10 : 1;
 
-// Halves h of units u .. u + kRun - 1; u is a multiple of kRun and the run is
+// Units u .. u + kRun - 1 of row r; u is a multiple of kRun and the run is
 // inside the row.
 template <int FMT>
-__device__ __forceinline__ RunRaw<FMT> load_run(const Mat& w, uint32_t r, int u, int h, int K) {
-  RunRaw<FMT> x;
+__device__ __forceinline__ RunMeta<FMT> load_run_meta(const Mat& w, uint32_t r, int u, int h, int K) {
+  RunMeta<FMT> x;
   constexpr int S = kRun<FMT>, P = kPlanes<FMT> - 1;
-#pragma unroll
-  for (int s = 0; s < S; ++s) {
-    u32x4 q[2];
-    load_half_codes<FMT, false>(q, w, r, u + s, h, K);
-    if constexpr (FMT == QMV_DENSE_BF16) {
-      x.q[2 * s] = q[0];
-      x.q[2 * s + 1] = q[1];
-    } else {
-      x.q[s] = q[0];
-    }
-  }
   const uint32_t mt = r * row_bytes<FMT>(P, K), ht = r * row_bytes<FMT>(1, K);
   if constexpr (is_fifth(FMT)) {
     const u32x4 a = load_at<u32x4_a4, false>(w.p[1], ht, 4 * u), b = load_at<u32x4_a4, false>(w.p[1], ht, 4 * u + 16);
@@ -471,16 +469,9 @@ __device__ __forceinline__ RunRaw<FMT> load_run(const Mat& w, uint32_t r, int u,
   return x;
 }
 
-// The half of unit u + s of a run (s known at compile time).
+// The scales of unit u + s of a run (s known at compile time).
 template <int FMT>
-__device__ __forceinline__ HalfRaw<FMT> half_of(const RunRaw<FMT>& x, int s) {
-  HalfRaw<FMT> r;
-  if constexpr (FMT == QMV_DENSE_BF16) {
-    r.q[0] = x.q[2 * s];
-    r.q[1] = x.q[2 * s + 1];
-  } else {
-    r.q[0] = x.q[s];
-  }
+__device__ __forceinline__ void meta_of(HalfRaw<FMT>& r, const RunMeta<FMT>& x, int s) {
   r.qh = x.qh[s];
   if constexpr (FMT == QMV_Q6K || FMT == QMV_Q8_0 || FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
     r.m.v[0] = (x.m[s >> 1] >> (16 * (s & 1))) & 0xFFFFu;
@@ -490,7 +481,6 @@ __device__ __forceinline__ HalfRaw<FMT> half_of(const RunRaw<FMT>& x, int s) {
   } else {
     r.m.v = x.m;
   }
-  return r;
 }
 
 // 16 bytes from global memory straight into LDS: the wave's 64 pieces land at

@@ -21,9 +21,10 @@ namespace {
 //
 // K goes by in stages of 32: one unit of every weight row and 64 bytes of every
 // token, in a ring of four LDS tiles each.  Tokens go straight from global
-// memory to LDS, three stages ahead; weights go through registers: a pair of
-// threads decodes one unit into the operand type, once per workgroup, two
-// stages ahead.  The first fragments of a stage are
+// memory to LDS, three stages ahead.  So do the weights' codes, 64 bytes of
+// every row at a time into two more tiles; from there a pair of threads decodes
+// one unit of a row into the operand type, once per workgroup, two stages ahead.
+// The first fragments of a stage are
 // read before the barrier that ends the stage before it, so no wave waits for
 // LDS behind a barrier (with 64-deep steps in two buffers, all read after the
 // barrier, a step took 1.85 us for 0.92 us of MFMA).
@@ -32,17 +33,18 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   constexpr int NT = 64 * WR * WT;
   constexpr int BR = 32 * RB * WR, BN = BR / 2, BM = 32 * TB * WT;
   constexpr int XPT = BM * 4 / NT;      // 16-byte token pieces per thread and stage
-  constexpr int SR = kRun<FMT>;          // stages per run
+  constexpr int SR = kRun<FMT>, SC = kChunk<FMT>;  // stages per run and per tile of codes
   static_assert(2 * BR == NT && XPT * NT == BM * 4 && RB % 2 == 0 && SR % 4 == 0);
 
   // variables of their own: the compiler then knows that a copy into one does
   // not concern the reads of the others
   __shared__ u32x4 A0[BR * 4], A1[BR * 4], A2[BR * 4], A3[BR * 4];
   __shared__ u32x4 X0[BM * 4], X1[BM * 4], X2[BM * 4], X3[BM * 4];
+  __shared__ u32x4 R0[BR * 4], R1[BR * 4];  // rows of codes: gate 0 .. BN - 1, then up
   // let their addresses escape: otherwise the compiler knows that no asm
   // statement can touch them and moves LDS reads across the fences below
   asm volatile("" ::"v"(A0), "v"(A1), "v"(A2), "v"(A3) : "memory");
-  asm volatile("" ::"v"(X0), "v"(X1), "v"(X2), "v"(X3) : "memory");
+  asm volatile("" ::"v"(X0), "v"(X1), "v"(X2), "v"(X3), "v"(R0), "v"(R1) : "memory");
   auto At = [&]<int S>() { return (S & 3) == 0 ? A0 : (S & 3) == 1 ? A1 : (S & 3) == 2 ? A2 : A3; };
   auto Xt = [&]<int S>() { return (S & 3) == 0 ? X0 : (S & 3) == 1 ? X1 : (S & 3) == 2 ? X2 : X3; };
 
@@ -59,7 +61,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   const int half = tid & 1, ri = tid >> 1;
   const bool up = wave >= WR * WT / 2;
   const uint32_t wrow = min(n0 + ri % BN, p.N - 1) - n0;
-  const Mat w = from_row<FMT>(up ? p.wu : p.wg, n0, K);
+  const Mat wg = from_row<FMT>(p.wg, n0, K), wu = from_row<FMT>(p.wu, n0, K), w = up ? wu : wg;
+  // Codes: thread tid copies piece tid % 4 (by the tile's order) of gate and of up row tid / 4.
+  const uint32_t co = uint32_t(min(n0 + (tid >> 2), p.N - 1) - n0) * row_bytes<FMT>(0, K) + 16 * ((tid & 3) ^ ((tid >> 4) & 3));
   const int arow = ((ri % BN) / (16 * RB)) * 32 * RB + (ri % BN) % (16 * RB) + (up ? 16 * RB : 0);
   // Token pieces: LDS slot tid + t * NT of a tile is row (tid + t * NT) / 4.
   const uint8_t* xb = reinterpret_cast<const uint8_t*>(p.x + int64_t(m0) * K);
@@ -102,59 +106,102 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
     for (int t = 0; t < XPT; ++t) copy_to_lds(xb + 64 * int64_t(u), xo[t], X + t * NT + wave * 64);
   };
 
+  auto copy_codes = [&](int u, u32x4* R) {  // units u .. u + SC - 1
+    copy_to_lds(wg.p[0] + int64_t(u) * (64 / SC), co, R + wave * 64);
+    copy_to_lds(wu.p[0] + int64_t(u) * (64 / SC), co, R + BN * 4 + wave * 64);
+  };
+
   // ---- whole runs
   const int runs = U / SR;
   if (runs > 0) {
-    const int last = runs * SR - 1;
-    RunRaw<FMT> cur, next;
-    auto decode = [&](const RunRaw<FMT>& x, int u, int s, int i, u32x4* A) {  // u: unit of stage s
-      A[tile32_at(arow, 2 * half + i)] = half_piece<FMT, F16>(half_of<FMT>(x, s), u, half, i);
+    // Workgroups start at different runs: in step they would all read the same
+    // columns of rows a power of two apart, which lie on few L2 channels.
+    int ua = id0.y % runs * SR;  // first unit of the current run
+    RunMeta<FMT> cur, next;
+    // words i of the unit of stage s of a run (first unit u, scales x) from codes R
+    auto decode = [&](const u32x4 (&codes)[2], const RunMeta<FMT>& x, int u, int s, u32x4* A, int i) {
+      HalfRaw<FMT> r;
+      r.q[0] = codes[0];
+      r.q[1] = codes[1];
+      meta_of<FMT>(r, x, s);
+      A[tile32_at(arow, 2 * half + i)] = half_piece<FMT, F16>(r, u + s, half, i);
     };
-    cur = load_run<FMT>(w, wrow, 0, half, K);
-    copy_x(0, X0);
-    copy_x(1, X1);
-    copy_x(2, X2);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      decode(cur, 0, 0, i, A0);
-      decode(cur, 1, 1, i, A1);
-    }
+    // Tile of codes of stage s (of this run or, past SR, the next).
+    auto Rt = [&]<int S>() { return (S / SC) & 1 ? R1 : R0; };
+    cur = load_run_meta<FMT>(w, wrow, ua, half, K);
+    copy_codes(ua, R0);
+    copy_codes(ua + SC, R1);
+    copy_x(ua, X0);
+    copy_x(ua + 1, X1);
+    copy_x(ua + 2, X2);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier16();
+    [&]<int... S>(std::integer_sequence<int, S...>) {
+      (([&] {
+         u32x4 c[2];
+         read_codes<FMT>(c, Rt.template operator()<S>(), ri, S % SC, half);
+#pragma unroll
+         for (int i = 0; i < 2; ++i) decode(c, cur, ua, S, S ? A1 : A0, i);
+       }()),
+       ...);
+    }(std::make_integer_sequence<int, 2>{});
+    lds_barrier16();
+    if constexpr (SC == 1) {  // both tiles of codes are used up
+      copy_codes(ua + 2, R0);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      lds_barrier16();
+    }
     Frag f0, f1;
+    u32x4 c[2][2];
     read(f0, A0, X0, 0);
+    if constexpr (SC == 4) read_codes<FMT>(c[0], R0, ri, 2, half);
 #pragma unroll 1
     for (int run = 0; run < runs; ++run) {
-      const int u0 = run * SR, then = min(u0 + SR, last + 1 - SR);
+      const int then = ua + SR < runs * SR ? ua + SR : 0;
       [&]<int... H>(std::integer_sequence<int, H...>) {
         (([&] {
            const u32x4 *A = At.template operator()<H>(), *X = Xt.template operator()<H>();
            const u32x4 *A1n = At.template operator()<H + 1>(), *X1n = Xt.template operator()<H + 1>();
            u32x4* A2n = At.template operator()<H + 2>();
-           auto dec = [&](int i) {
-             if constexpr (H + 2 >= SR) decode(next, then + H + 2 - SR, H + 2 - SR, i, A2n);
-             else decode(cur, u0 + H + 2, H + 2, i, A2n);
-           };
-           copy_x(min(u0 + H + 3, last), Xt.template operator()<H + 3>());
+           // The stage decoded here is H + 2.  When it is the first of its tile of
+           // codes, the other tile is done with: its next codes (those behind this
+           // tile's) go there.
+           constexpr int D = H + 2;
+           constexpr bool fresh = D % SC == 0;
+           constexpr int NC = D + SC;  // first stage of the codes to copy
+           if constexpr (fresh) copy_codes(NC < SR ? ua + NC : NC < 2 * SR ? then + NC - SR : 0, Rt.template operator()<NC>());
+           copy_x(H + 3 < SR ? ua + H + 3 : then + H + 3 - SR, Xt.template operator()<H + 3>());
            fence();
-           if constexpr (H == 0) next = load_run<FMT>(w, wrow, then, half, K);
+           if constexpr (H == 0) next = load_run_meta<FMT>(w, wrow, then, half, K);
+           // Where a tile of codes lasts four stages, a stage's codes are read in the
+           // stage before.
+           if constexpr (SC < 4) read_codes<FMT>(c[H & 1], Rt.template operator()<D>(), ri, D % SC, half);
            read(f1, A, X, 1);
+           auto dec = [&](int i) {
+             if constexpr (D >= SR) decode(c[H & 1], next, then, D - SR, A2n, i);
+             else decode(c[H & 1], cur, ua, D, A2n, i);
+           };
            dec(0);
            mul(f0);
            fence();
            read(f0, A1n, X1n, 0);
+           if constexpr (SC == 4) read_codes<FMT>(c[(H + 1) & 1], Rt.template operator()<D + 1>(), ri, (D + 1) % SC, half);
            dec(1);
            mul(f1);
            fence();
            // Stage H + 2 is whole once the copies of the stage before this one have
            // landed.  Certainly issued after those: this stage's copies, and in a
-           // run's first two stages the loads of the next run's codes.
-           asm volatile("s_waitcnt vmcnt(%0)" ::"n"(XPT + (H < 2 ? kRunLoads<FMT> : 0)) : "memory");
+           // run's first two stages the loads of the next run's scales.  Codes are
+           // older than their stage's tokens, and used two stages later or more
+           // (SC = 1: in the next stage, so only the tokens' copies may be left).
+           constexpr int left = XPT + (SC == 1 ? 0 : (fresh ? 2 : 0) + (H < 2 ? kMetaLoads<FMT> : 0));
+           asm volatile("s_waitcnt vmcnt(%0)" ::"n"(left) : "memory");
            lds_barrier16();
          }()),
          ...);
       }(std::make_integer_sequence<int, SR>{});
       cur = next;
+      ua = then;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the copies past the end
     lds_barrier16();
