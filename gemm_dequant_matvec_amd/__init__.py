@@ -14,6 +14,7 @@ Importing this package fails loudly when the library has not been built
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -119,7 +120,7 @@ class QmvRopeScaling(ctypes.Structure):
                 ("low", ctypes.c_double), ("high", ctypes.c_double)]
 
 
-_lib.qmv_rope.argtypes = [_i64, _i64, _i64, _int, _int, ctypes.POINTER(QmvRopeTensor), _int, _vp, _vp, ctypes.c_float,
+_lib.qmv_rope.argtypes = [_i64, _i64, _i64, _int, _int, _vp, _int, _vp, _vp, ctypes.c_float,
                           _int, _vp]
 _lib.qmv_rope.restype = _int
 _lib.qmv_rope_freqs.argtypes = [_i64, ctypes.c_double, ctypes.POINTER(QmvRopeScaling), ctypes.POINTER(ctypes.c_float)]
@@ -393,6 +394,11 @@ ACTS = {"silu": 1, "gelu_tanh": 2, "gelu": 3}
 ROPE_LAYOUTS = {"half": 1, "interleaved": 2}
 ROPE_KINDS = {"linear": 1, "ntk": 2, "parts": 3}
 
+# The many-token operators below are called once or twice per layer, for single
+# tokens too: their checks are kept to attribute reads (sizes are cached, the
+# stream comes as a raw handle), a few microseconds per call.
+_packed_bytes_cached = functools.lru_cache(maxsize=None)(packed_bytes)
+
 
 def _act(act) -> int:
     if isinstance(act, str):
@@ -402,13 +408,44 @@ def _act(act) -> int:
     return int(act)
 
 
-def _same(t: torch.Tensor, like: torch.Tensor, shape: tuple, what: str) -> torch.Tensor:
-    """t must be of this shape, and of like's dtype and device."""
-    if tuple(t.shape) != shape:
+def _on_current_device(t: torch.Tensor, stream) -> int:
+    """The raw stream for a call whose tensors are on t's device, which has to be
+    the current one: kernels are launched there."""
+    if not t.is_cuda:
+        raise ValueError("tensors passed to libqmv must live on the GPU")
+    device = t.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on device {device}, the current device is {torch._C._cuda_getDevice()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on device {stream.device.index}, the tensors on {device}")
+    return stream.cuda_stream
+
+
+def _weight(W: torch.Tensor, nbytes: int, device: int, what: str) -> int:
+    """Pointer of a packed matrix."""
+    if W.nbytes < nbytes:
+        raise ValueError(f"{what} holds {W.nbytes} bytes, the call needs {nbytes}")
+    if not W.is_contiguous():
+        raise ValueError("tensors passed to libqmv must be contiguous")
+    if W.get_device() != device:
+        raise ValueError(f"{what} is on {W.device}, the call's tensors on device {device}")
+    return W.data_ptr()
+
+
+def _like(t: torch.Tensor | None, like: torch.Tensor, shape: tuple, what: str) -> torch.Tensor:
+    """t, or a new tensor in its place: of this shape, contiguous, of like's dtype and device."""
+    if t is None:
+        return like.new_empty(shape)
+    if t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {shape}")
-    _need_dtype(t, like.dtype, what)
-    if t.device != like.device:
+    if t.dtype != like.dtype:
+        raise ValueError(f"{what} must be {like.dtype}, got {t.dtype}")
+    if t.get_device() != like.get_device():
         raise ValueError(f"{what} is on {t.device}, expected {like.device}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libqmv must be contiguous")
     return t
 
 
@@ -420,22 +457,26 @@ def gemm_glu(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, X: torch.Tensor, N: 
     act: "silu", "gelu_tanh" or "gelu".  With save=True (or G and U given) the
     two products are kept for gemm_glu_backward and (H, G, U) is returned.
     """
-    M = X.shape[0]
     if X.dim() != 2 or X.shape[1] != K:
         raise ValueError(f"X has shape {tuple(X.shape)}, expected [M][{K}]")
     if X.dtype not in _DTYPES:
         raise ValueError("X dtype must be float32, float16 or bfloat16")
     if (G is None) != (U is None):
         raise ValueError("G and U go together")
-    _need(W_gate, packed_bytes(fmt, N, K), "W_gate")
-    _need(W_up, packed_bytes(fmt, N, K), "W_up")
-    keep = save or G is not None
-    H, G, U = (None if t is None and i and not keep else
-               torch.empty((M, N), dtype=X.dtype, device=X.device) if t is None else _same(t, X, (M, N), "HGU"[i])
-               for i, t in enumerate((H, G, U)))
-    _check(_lib.qmv_gemm_glu(_fmt(fmt), N, K, M, _ptr(W_gate), _ptr(W_up), _ptr(X), _DTYPES[X.dtype], _act(act),
-                             _ptr(H), _DTYPES[H.dtype], _ptr(G), _ptr(U), _stream(stream)))
-    return (H, G, U) if keep else H
+    shape, dt, f, a = (X.shape[0], N), _DTYPES[X.dtype], _fmt(fmt), _act(act)
+    s, device = _on_current_device(X, stream), X.get_device()
+    nbytes = _packed_bytes_cached(f, N, K)
+    wg, wu = _weight(W_gate, nbytes, device, "W_gate"), _weight(W_up, nbytes, device, "W_up")
+    if not X.is_contiguous():
+        raise ValueError("tensors passed to libqmv must be contiguous")
+    H = _like(H, X, shape, "H")
+    if not save and G is None:
+        _check(_lib.qmv_gemm_glu(f, N, K, shape[0], wg, wu, X.data_ptr(), dt, a, H.data_ptr(), dt, None, None, s))
+        return H
+    G, U = _like(G, X, shape, "G"), _like(U, X, shape, "U")
+    _check(_lib.qmv_gemm_glu(f, N, K, shape[0], wg, wu, X.data_ptr(), dt, a, H.data_ptr(), dt, G.data_ptr(),
+                             U.data_ptr(), s))
+    return H, G, U
 
 
 def gemm_glu_backward_bytes(fmt, N: int, K: int, M: int) -> int:
@@ -453,25 +494,29 @@ def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Te
     from its saved G and U; all of one dtype.  dG and dU may be given as two of
     the buffers G, U and dH.  workspace: scratch memory of
     gemm_glu_backward_bytes bytes, allocated when absent."""
-    M = G.shape[0]
     if G.dtype not in _DTYPES:
         raise ValueError("G dtype must be float32, float16 or bfloat16")
-    _need(W_gate, packed_bytes(fmt, N, K), "W_gate")
-    _need(W_up, packed_bytes(fmt, N, K), "W_up")
-    _same(G, G, (M, N), "G")
-    _same(U, G, (M, N), "U")
-    _same(dH, G, (M, N), "dH")
-    dG = torch.empty_like(G) if dG is None else _same(dG, G, (M, N), "dG")
-    dU = torch.empty_like(G) if dU is None else _same(dU, G, (M, N), "dU")
-    dX = torch.empty((M, K), dtype=G.dtype, device=G.device) if dX is None else _same(dX, G, (M, K), "dX")
-    nbytes = gemm_glu_backward_bytes(fmt, N, K, M)
-    if workspace is None and nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=G.device)
+    shape, f, a = (G.shape[0], N), _fmt(fmt), _act(act)
+    M = shape[0]
+    _like(G, G, shape, "G")
+    _like(U, G, shape, "U")
+    _like(dH, G, shape, "dH")
+    s, device = _on_current_device(G, stream), G.get_device()
+    nbytes = _packed_bytes_cached(f, N, K)
+    wg, wu = _weight(W_gate, nbytes, device, "W_gate"), _weight(W_up, nbytes, device, "W_up")
+    dG, dU, dX = _like(dG, G, shape, "dG"), _like(dU, G, shape, "dU"), _like(dX, G, (M, K), "dX")
+    nbytes = gemm_glu_backward_bytes(f, N, K, M)
+    ws = None
     if nbytes:
-        _need(workspace, nbytes, "workspace")
-    _check(_lib.qmv_gemm_glu_backward(_fmt(fmt), N, K, M, _ptr(W_gate), _ptr(W_up), _ptr(G), _ptr(U), _ptr(dH),
-                                      _DTYPES[G.dtype], _act(act), _ptr(dG), _ptr(dU), _ptr(dX), _ptr(workspace),
-                                      nbytes, _stream(stream)))
+        if workspace is None:
+            if stream is None:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=G.device)
+            else:  # memory of the stream that the call runs on
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=G.device)
+        ws = _weight(workspace, nbytes, device, "workspace")
+    _check(_lib.qmv_gemm_glu_backward(f, N, K, M, wg, wu, G.data_ptr(), U.data_ptr(), dH.data_ptr(),
+                                      _DTYPES[G.dtype], a, dG.data_ptr(), dU.data_ptr(), dX.data_ptr(), ws, nbytes, s))
     return dX, dG, dU
 
 
@@ -489,6 +534,24 @@ def rope_freqs(R: int, base: float = 10000.0, scaling: str | None = None, factor
         sc = ctypes.byref(QmvRopeScaling(ROPE_KINDS[scaling], factor, original, low, high))
     _check(_lib.qmv_rope_freqs(R, base, sc, ctypes.cast(host.data_ptr(), ctypes.POINTER(ctypes.c_float))))
     return host.to(device)
+
+
+_RopeFields = ctypes.c_int64 * 14  # two qmv_rope_tensor, all of whose fields are 8 bytes
+
+
+def _rope_out(x: torch.Tensor, y: torch.Tensor | None, what: str) -> torch.Tensor:
+    if y is None:
+        return x.new_empty(x.shape)
+    if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != x.get_device():
+        raise ValueError(f"{what}_out must have {what}'s shape, dtype and device")
+    return y
+
+
+def _rope_fields(x: torch.Tensor, y: torch.Tensor, what: str) -> tuple:
+    (xt, xh, xd), (yt, yh, yd) = x.stride(), y.stride()
+    if (xd != 1 or yd != 1) and x.shape[2] > 1:
+        raise ValueError(f"the values of a head of {what} must be adjacent")
+    return x.data_ptr(), y.data_ptr(), x.shape[1], xt, xh, yt, yh
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torch.Tensor, layout="half",
@@ -515,29 +578,23 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torc
         raise ValueError("q dtype must be float32, float16 or bfloat16")
     _need_dtype(pos, torch.int64, "pos")
     _need_dtype(freqs, torch.float32, "freqs")
-    _need(pos, T * 8, "pos")
-    R = 2 * freqs.numel()
-    arr = (QmvRopeTensor * 2)()
-    outs = []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            outs.append(None)
-            continue
-        _same(x, q, (T, x.shape[1] if x.dim() == 3 else -1, D), name)
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else _same(y, x, tuple(x.shape),
-                                                                                          name + "_out")
-        t = arr[sum(o is not None for o in outs)]
-        for v, what in ((x, name), (y, name + "_out")):
-            if not v.is_cuda:
-                raise ValueError("tensors passed to libqmv must live on the GPU")
-            if v.stride(2) != 1 and D > 1:
-                raise ValueError(f"the values of a head of {what} must be adjacent")
-        t.x, t.y, t.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
-        t.x_token, t.x_head, t.y_token, t.y_head = x.stride(0), x.stride(1), y.stride(0), y.stride(1)
-        outs.append(y)
-    _check(_lib.qmv_rope(T, D, R, layout, sum(o is not None for o in outs), arr, _DTYPES[q.dtype], _ptr(pos),
-                         _ptr(freqs), amplitude, int(inverse), _stream(stream)))
-    return tuple(outs)
+    if pos.numel() != T:
+        raise ValueError(f"pos holds {pos.numel()} positions, q {T} tokens")
+    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype != q.dtype):
+        raise ValueError(f"k has shape {tuple(k.shape)} and {k.dtype}, expected [{T}][heads][{D}] and {q.dtype}")
+    s, device = _on_current_device(q, stream), q.get_device()
+    if pos.get_device() != device or freqs.get_device() != device or (k is not None and k.get_device() != device):
+        raise ValueError("q, k, pos and freqs must be on one device")
+    if not (pos.is_contiguous() and freqs.is_contiguous()):
+        raise ValueError("tensors passed to libqmv must be contiguous")
+    q_out = _rope_out(q, q_out, "q")
+    fields = _rope_fields(q, q_out, "q")
+    if k is not None:
+        k_out = _rope_out(k, k_out, "k")
+        fields += _rope_fields(k, k_out, "k")
+    _check(_lib.qmv_rope(T, D, 2 * freqs.numel(), layout, 1 if k is None else 2, _RopeFields(*fields), _DTYPES[q.dtype],
+                         pos.data_ptr(), freqs.data_ptr(), amplitude, inverse, s))
+    return q_out, None if k is None else k_out
 
 
 def dequant(fmt, W: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None,
