@@ -102,19 +102,11 @@ __device__ __forceinline__ int tile_at_t(int r, int c) {
 struct TileId {
   int x, y;
 };
-#ifndef VAR_BAND
-#define VAR_BAND 4
-#endif
-constexpr int kBand = VAR_BAND;
+constexpr int kBand = 4;
 __device__ __forceinline__ TileId tile_of_block(int nx, int bx, int ny, int by) {
   const int X = (nx + bx - 1) / bx, Y = (ny + by - 1) / by, all = X * Y;
   const int b = blockIdx.x, xcd = b & 7, per = all >> 3, more = all & 7;
-#ifdef VAR_NOXCD
-  const int t = b;
-#else
-  const int t = xcd * per + min(xcd, more) + (b >> 3);
-#endif
-  // XCD i takes per tiles, the first `more` one extra
+  const int t = xcd * per + min(xcd, more) + (b >> 3);  // XCD i takes per tiles, the first `more` one extra
   const int band = t / (kBand * X), in = t - band * kBand * X;
   const int high = min(kBand, Y - band * kBand);
   return TileId{in / high, band * kBand + in % high};
@@ -342,8 +334,7 @@ __device__ __forceinline__ u32x4 unit_piece(const UnitRaw<FMT>& r, const Affine&
 // loaded together.
 template <int FMT>
 constexpr int kChunk = FMT == QMV_DENSE_BF16 ? 1 : is_byte(FMT) ? 2 : 4;
-template <int FMT>
-constexpr int kRun = kChunk<FMT> == 4 ? 8 : 4;
+constexpr int kRun = 8;
 
 template <int FMT>
 struct HalfRaw {
@@ -419,7 +410,6 @@ __device__ __forceinline__ u32x4 half_piece(const HalfRaw<FMT>& r, int u, int h,
 
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
 // The scales and high bits of a run, for half h.
 template <int FMT>
@@ -438,7 +428,7 @@ constexpr int kMetaLoads = FMT == QMV_DENSE_BF16 ? 0 : is_fifth(FMT) ? 3 : FMT =
 template <int FMT>
 __device__ __forceinline__ RunMeta<FMT> load_run_meta(const Mat& w, uint32_t r, int u, int h, int K) {
   RunMeta<FMT> x;
-  constexpr int S = kRun<FMT>, P = kPlanes<FMT> - 1;
+  constexpr int S = kRun, P = kPlanes<FMT> - 1;
   const uint32_t mt = r * row_bytes<FMT>(P, K), ht = r * row_bytes<FMT>(1, K);
   if constexpr (is_fifth(FMT)) {
     const u32x4 a = load_at<u32x4_a4, false>(w.p[1], ht, 4 * u), b = load_at<u32x4_a4, false>(w.p[1], ht, 4 * u + 16);
@@ -448,11 +438,7 @@ __device__ __forceinline__ RunMeta<FMT> load_run_meta(const Mat& w, uint32_t r, 
       x.qh[4 + s] = b[s];
     }
   }
-  if constexpr (FMT == QMV_Q8_0) {
-    const u32x2 v = load_at<u32x2_a2, false>(w.p[P], mt, 2 * u);
-    x.m[0] = v[0];
-    x.m[1] = v[1];
-  } else if constexpr (FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
+  if constexpr (FMT == QMV_Q8_0 || FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
     x.m = load_at<u32x4_a2, false>(w.p[P], mt, 2 * u);
   } else if constexpr (FMT == QMV_W4A16_G64) {
     x.m = load_at<u32x4_a4, false>(w.p[P], mt, 2 * u);
@@ -483,11 +469,16 @@ __device__ __forceinline__ void meta_of(HalfRaw<FMT>& r, const RunMeta<FMT>& x, 
   }
 }
 
-// 16 bytes from global memory straight into LDS: the wave's 64 pieces land at
-// `dst` (uniform) in lane order.
-__device__ __forceinline__ void copy_to_lds(const uint8_t* base, uint32_t off, u32x4* dst) {
-  __builtin_amdgcn_global_load_lds((const QMV_GLOBAL void*)(scalar_base(base) + lane_offset(off)),
-                                   (void __attribute__((address_space(3)))*)dst, 16, 0, 0);
+// 16 bytes from global memory (buffer base + lane offset + uniform offset)
+// straight into LDS: the wave's 64 pieces land at `dst` (uniform) in lane order.
+// A buffer instruction, because the global_load_lds form counts as a flat access
+// with the compiler, which then lets every later wait drain both counters.
+typedef __amdgpu_buffer_rsrc_t Buf;
+__device__ __forceinline__ Buf buffer_of(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, -1, 0x00020000);
+}
+__device__ __forceinline__ void copy_to_lds(Buf b, uint32_t lane, uint32_t uniform, u32x4* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (void __attribute__((address_space(3)))*)dst, 16, lane, uniform, 0, 0);
 }
 
 // Eight weights (word i of unit u) of one row, as loaded, for the transposing

@@ -16,12 +16,29 @@ struct GluFwdArgs {
 
 namespace {
 
+// How many vector memory operations a wave has certainly issued by the end of
+// stage `now` after the copy of the tokens (or of the codes) in stage `from`.  A
+// stage issues the XPT copies of its tokens, then, where it starts to decode a
+// tile of codes, the two copies of the tile after the next, then, once per run,
+// the loads of the next run's scales.
+template <int FMT, int XPT>
+constexpr int issued_after(int from, bool codes, int now) {
+  int n = 0;
+  for (int s = from; s <= now; ++s) {
+    const int h = (s + 4 * kRun) % kRun;
+    if (s > from) n += XPT;
+    if ((s > from || !codes) && (h + 2) % kChunk<FMT> == 0) n += 2;
+    if (h == 0) n += kMetaLoads<FMT>;
+  }
+  return n;
+}
+
 // RB, TB: 32-row blocks of weights (half gate, half up) and of tokens per wave;
 // WR x WT waves.
 //
 // K goes by in stages of 32: one unit of every weight row and 64 bytes of every
 // token, in a ring of four LDS tiles each.  Tokens go straight from global
-// memory to LDS, three stages ahead.  So do the weights' codes, 64 bytes of
+// memory to LDS, three stages ahead (seven were no faster).  So do the weights' codes, 64 bytes of
 // every row at a time into two more tiles; from there a pair of threads decodes
 // one unit of a row into the operand type, once per workgroup, two stages ahead.
 // The first fragments of a stage are
@@ -33,8 +50,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   constexpr int NT = 64 * WR * WT;
   constexpr int BR = 32 * RB * WR, BN = BR / 2, BM = 32 * TB * WT;
   constexpr int XPT = BM * 4 / NT;      // 16-byte token pieces per thread and stage
-  constexpr int SR = kRun<FMT>, SC = kChunk<FMT>;  // stages per run and per tile of codes
-  static_assert(2 * BR == NT && XPT * NT == BM * 4 && RB % 2 == 0 && SR % 4 == 0);
+  constexpr int SR = kRun, SC = kChunk<FMT>;  // stages per run and per tile of codes
+  static_assert(2 * BR == NT && XPT * NT == BM * 4 && RB % 2 == 0);
+  constexpr int XD = 3;                 // stages that the tokens' copies run ahead
 
   // variables of their own: the compiler then knows that a copy into one does
   // not concern the reads of the others
@@ -67,6 +85,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   const int arow = ((ri % BN) / (16 * RB)) * 32 * RB + (ri % BN) % (16 * RB) + (up ? 16 * RB : 0);
   // Token pieces: LDS slot tid + t * NT of a tile is row (tid + t * NT) / 4.
   const uint8_t* xb = reinterpret_cast<const uint8_t*>(p.x + int64_t(m0) * K);
+  const Buf xbuf = buffer_of(xb), gbuf = buffer_of(wg.p[0]), ubuf = buffer_of(wu.p[0]);
   uint32_t xo[XPT];
 #pragma unroll
   for (int t = 0; t < XPT; ++t)
@@ -103,12 +122,12 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   };
   auto copy_x = [&](int u, u32x4* X) {  // unit u of the tokens
 #pragma unroll
-    for (int t = 0; t < XPT; ++t) copy_to_lds(xb + 64 * int64_t(u), xo[t], X + t * NT + wave * 64);
+    for (int t = 0; t < XPT; ++t) copy_to_lds(xbuf, xo[t], 64 * u, X + t * NT + wave * 64);
   };
 
   auto copy_codes = [&](int u, u32x4* R) {  // units u .. u + SC - 1
-    copy_to_lds(wg.p[0] + int64_t(u) * (64 / SC), co, R + wave * 64);
-    copy_to_lds(wu.p[0] + int64_t(u) * (64 / SC), co, R + BN * 4 + wave * 64);
+    copy_to_lds(gbuf, co, u * (64 / SC), R + wave * 64);
+    copy_to_lds(ubuf, co, u * (64 / SC), R + BN * 4 + wave * 64);
   };
 
   // ---- whole runs
@@ -131,9 +150,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
     cur = load_run_meta<FMT>(w, wrow, ua, half, K);
     copy_codes(ua, R0);
     copy_codes(ua + SC, R1);
-    copy_x(ua, X0);
-    copy_x(ua + 1, X1);
-    copy_x(ua + 2, X2);
+    [&]<int... S>(std::integer_sequence<int, S...>) {
+      (copy_x(ua + S, Xt.template operator()<S>()), ...);
+    }(std::make_integer_sequence<int, XD>{});
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier16();
     [&]<int... S>(std::integer_sequence<int, S...>) {
@@ -169,8 +188,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
            constexpr int D = H + 2;
            constexpr bool fresh = D % SC == 0;
            constexpr int NC = D + SC;  // first stage of the codes to copy
+           copy_x(H + XD < SR ? ua + H + XD : then + H + XD - SR, Xt.template operator()<H + XD>());
+           fence();
            if constexpr (fresh) copy_codes(NC < SR ? ua + NC : NC < 2 * SR ? then + NC - SR : 0, Rt.template operator()<NC>());
-           copy_x(H + 3 < SR ? ua + H + 3 : then + H + 3 - SR, Xt.template operator()<H + 3>());
            fence();
            if constexpr (H == 0) next = load_run_meta<FMT>(w, wrow, then, half, K);
            // Where a tile of codes lasts four stages, a stage's codes are read in the
@@ -189,12 +209,14 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
            dec(1);
            mul(f1);
            fence();
-           // Stage H + 2 is whole once the copies of the stage before this one have
-           // landed.  Certainly issued after those: this stage's copies, and in a
-           // run's first two stages the loads of the next run's scales.  Codes are
-           // older than their stage's tokens, and used two stages later or more
-           // (SC = 1: in the next stage, so only the tokens' copies may be left).
-           constexpr int left = XPT + (SC == 1 ? 0 : (fresh ? 2 : 0) + (H < 2 ? kMetaLoads<FMT> : 0));
+           // The next stage reads the tokens of stage H + 2, and the codes of the stage
+           // `code`, if they start a tile.  Everything issued after their copies may
+           // still be under way.
+           constexpr int code = SC == 4 ? H + 4 : H + 3;
+           constexpr int left_x = issued_after<FMT, XPT>(H + 2 - XD, false, H);
+           constexpr int left_c = code % SC ? 63 : issued_after<FMT, XPT>(code - SC - 2, true, H);
+           constexpr int left = left_x < left_c ? left_x : left_c;
+           static_assert(left >= 0 && left <= 63);
            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(left) : "memory");
            lds_barrier16();
          }()),
@@ -384,17 +406,16 @@ hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
       hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 4, 4>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
   }
-  const int64_t big = int64_t((p.N + 127) / 128) * ((p.M + 255) / 256);
-  if (big >= 256) {
-#ifndef VAR_CFG
-#define VAR_CFG 4, 2, 2, 4
-#define VAR_T 512
-#endif
-    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, VAR_CFG>), dim3(unsigned(int64_t((p.N + 127) / 128) * ((p.M + 255) / 256))), dim3(VAR_T), 0,
-                       s, p);
+  // Tiles of 64 outputs x 128 tokens go two to a compute unit: up to 512 of them
+  // are one round of the chip.  Past that the tile of 128 x 256 is faster, which
+  // decodes a weight once for twice the tokens.  W4A16, K = 2048, N = 5632: 352
+  // small tiles (M = 512) 42 us against 48, 528 (M = 768) 65 against 51.
+  const int64_t small = int64_t((p.N + 63) / 64) * ((p.M + 127) / 128);
+  if (small <= 512) {
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 2, 2, 2>), dim3(unsigned(small)), dim3(256), 0, s, p);
   } else {
-    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 2, 2, 2>), dim3(unsigned(int64_t((p.N + 63) / 64) * ((p.M + 127) / 128))), dim3(256), 0, s,
-                       p);
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 4, 2, 2, 4>),
+                       dim3(unsigned(int64_t((p.N + 127) / 128) * ((p.M + 255) / 256))), dim3(512), 0, s, p);
   }
   return hipGetLastError();
 }
