@@ -336,11 +336,11 @@ static int check_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gat
   if (act < QMV_ACT_SILU || act > QMV_ACT_GELU) return fail(QMV_ERR_UNSUPPORTED, "act=%d is not a qmv_act", act);
   if (!aligned(W_gate, 16)) return fail(QMV_ERR_ALIGN, "W_gate is not 16-byte aligned");
   if (!aligned(W_up, 16)) return fail(QMV_ERR_ALIGN, "W_up is not 16-byte aligned");
-  // the grid holds M / 128 (or M / 32 up to 32) row tiles in y, elements are 64-bit indexed
-  if (M > int64_t(65535) * 128) return fail(QMV_ERR_OVERFLOW, "M=%lld too large for one launch", (long long)M);
-  if (N > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return fail(QMV_ERR_OVERFLOW, "N or K too large");
-  if (M * N / 2048 >= (int64_t(1) << 31) - 1 || M * K / 1024 >= (int64_t(1) << 31) - 1)
-    return fail(QMV_ERR_OVERFLOW, "M * N or M * K too large for one launch");
+  // 256 rows of N or K 16-bit values (and 256 packed rows) are reached by 31-bit byte offsets from
+  // their first; tiles, and eighths of M * N, are counted in 32 bits
+  if (N > (int64_t(1) << 21) || K > (int64_t(1) << 21)) return fail(QMV_ERR_OVERFLOW, "N or K is past 2^21");
+  if (M >= (int64_t(1) << 31) || M * N >= (int64_t(1) << 38) || M * K >= (int64_t(1) << 38))
+    return fail(QMV_ERR_OVERFLOW, "M * N or M * K is past 2^38");
   return QMV_OK;
 }
 
@@ -370,8 +370,8 @@ int qmv_gemm_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, c
 }
 
 static size_t glu_backward_bytes(int64_t N, int64_t K, int64_t M) {
-  const int splits = qmv::glu_backward_splits(N, K, M);
-  return splits > 1 ? size_t(splits) * size_t(M) * size_t(K) * 4 : 0;
+  const qmv::GluBwdPlan p = qmv::glu_backward_plan(N, K, M);
+  return size_t(p.part_bytes + 2 * p.copy_bytes);
 }
 
 int qmv_gemm_glu_backward_bytes(int fmt, int64_t N, int64_t K, int64_t M, size_t* out_bytes) {
@@ -379,7 +379,9 @@ int qmv_gemm_glu_backward_bytes(int fmt, int64_t N, int64_t K, int64_t M, size_t
   if ((st = check_fmt(fmt))) return st;
   if ((st = check_shape(fmt, N, K, M, "M"))) return st;
   if (!out_bytes) return fail(QMV_ERR_NULL, "out_bytes is NULL");
-  if (M > (int64_t(1) << 40) / K) return fail(QMV_ERR_OVERFLOW, "M * K too large");
+  if (N > (int64_t(1) << 21) || K > (int64_t(1) << 21)) return fail(QMV_ERR_OVERFLOW, "N or K is past 2^21");
+  if (M >= (int64_t(1) << 31) || M * N >= (int64_t(1) << 38) || M * K >= (int64_t(1) << 38))
+    return fail(QMV_ERR_OVERFLOW, "M * N or M * K is past 2^38");
   *out_bytes = glu_backward_bytes(N, K, M);
   return ok();
 }
@@ -408,8 +410,7 @@ int qmv_gemm_glu_backward(int fmt, int64_t N, int64_t K, int64_t M, const void* 
                                       static_cast<const uint8_t*>(W_up), static_cast<const uint16_t*>(G),
                                       static_cast<const uint16_t*>(U), static_cast<const uint16_t*>(dH),
                                       dtype == QMV_F16, act, static_cast<uint16_t*>(dG), static_cast<uint16_t*>(dU),
-                                      static_cast<uint16_t*>(dX), static_cast<float*>(ws),
-                                      qmv::glu_backward_splits(N, K, M), as_stream(stream)),
+                                      static_cast<uint16_t*>(dX), static_cast<uint8_t*>(ws), as_stream(stream)),
                   "gemm_glu_backward");
 }
 

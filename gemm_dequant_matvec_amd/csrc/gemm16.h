@@ -79,19 +79,13 @@ __device__ __forceinline__ u32x4 load_part(const uint16_t* p, int n) {
 // all 64 banks at once if their pieces differ in address bits 4..7.  Piece c of
 // row r sits at c ^ (r / 2 % 8) of its row: free of conflicts for 16
 // consecutive rows of one piece, and a fragment 32 rows on is a constant offset
-// away.  The transposing writes of the backward pass also touch rows 8 apart,
-// so there the row's lowest bit is exchanged for r0 ^ r6 and the piece also
-// takes r / 8 % 8.
+// away. 
 __device__ __forceinline__ int tile_at(int r, int c) {  // in 16-byte pieces
   return r * 8 + (c ^ ((r >> 1) & 7));
 }
 // The same for rows of 32 values (64 bytes, four pieces).
 __device__ __forceinline__ int tile32_at(int r, int c) {
   return r * 4 + (c ^ ((r >> 2) & 3));
-}
-__device__ __forceinline__ int tile_at_t(int r, int c) {
-  const int row = (r & ~1) | ((r ^ (r >> 6)) & 1);
-  return row * 8 + (c ^ (((r >> 1) ^ (r >> 3)) & 7));
 }
 
 // -------------------------------------------------------- workgroups to tiles
@@ -169,7 +163,7 @@ __device__ __forceinline__ uint32_t lane_offset(uint32_t v) {
 // too and joins the 32-bit offset; else it joins the scalar base.
 template <class T, bool LANE = true>
 __device__ __forceinline__ T load_at(const uint8_t* plane, uint32_t row, int64_t u = 0) {
-  if constexpr (LANE) return *reinterpret_cast<const T*>(plane + (row + uint32_t(u)));
+  if constexpr (LANE) return *(const QMV_GLOBAL T*)(scalar_base(plane) + lane_offset(row + uint32_t(u)));
   else return *(const QMV_GLOBAL T*)(scalar_base(plane + u) + lane_offset(row));
 }
 
@@ -358,24 +352,24 @@ __device__ __forceinline__ void read_codes(u32x4 (&q)[2], const u32x4* R, int r,
   }
 }
 
-// Half h (a lane's) of unit u, from global memory.
-template <int FMT>
+// Half h (a lane's) of unit u (LANE: a lane's too), from global memory.
+template <int FMT, bool LANE>
 __device__ __forceinline__ HalfRaw<FMT> load_half(const Mat& w, uint32_t r, int u, int h, int K) {
   HalfRaw<FMT> x;
   constexpr int B = 32 / kChunk<FMT>;  // bytes of half a unit's codes
   const uint32_t at = r * row_bytes<FMT>(0, K) + B * h;
   const int64_t ub = int64_t(u) * (2 * B);
   if constexpr (B == 8) {
-    const u32x2 v = load_at<u32x2, false>(w.p[0], at, ub);
+    const u32x2 v = load_at<u32x2, LANE>(w.p[0], at, ub);
     x.q[0][0] = v[0];
     x.q[0][1] = v[1];
   } else {
-    x.q[0] = load_at<u32x4, false>(w.p[0], at, ub);
-    if constexpr (B == 32) x.q[1] = load_at<u32x4, false>(w.p[0], at, ub + 16);
+    x.q[0] = load_at<u32x4, LANE>(w.p[0], at, ub);
+    if constexpr (B == 32) x.q[1] = load_at<u32x4, LANE>(w.p[0], at, ub + 16);
   }
-  if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t, false>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
-  if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t, false>(w.p[1], r * row_bytes<FMT>(1, K) + 4 * h, 8 * u);
-  x.m = load_meta<FMT, false>(w, r, u, K);
+  if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t, LANE>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
+  if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t, LANE>(w.p[1], r * row_bytes<FMT>(1, K) + 4 * h, 8 * u);
+  x.m = load_meta<FMT, LANE>(w, r, u, K);
   return x;
 }
 
@@ -474,58 +468,14 @@ __device__ __forceinline__ void meta_of(HalfRaw<FMT>& r, const RunMeta<FMT>& x, 
 // A buffer instruction, because the global_load_lds form counts as a flat access
 // with the compiler, which then lets every later wait drain both counters.
 typedef __amdgpu_buffer_rsrc_t Buf;
-__device__ __forceinline__ Buf buffer_of(const void* base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, -1, 0x00020000);
+__device__ __forceinline__ Buf buffer_of(const void* base, int bytes = -1) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
+}
+__device__ __forceinline__ Buf buffer_of(const QMV_GLOBAL uint8_t* base, int bytes = -1) {
+  return buffer_of((const void*)base, bytes);
 }
 __device__ __forceinline__ void copy_to_lds(Buf b, uint32_t lane, uint32_t uniform, u32x4* dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (void __attribute__((address_space(3)))*)dst, 16, lane, uniform, 0, 0);
-}
-
-// Eight weights (word i of unit u) of one row, as loaded, for the transposing
-// backward tile.
-template <int FMT>
-struct WordRaw {
-  u32x4 q;  // q[0], q[1] unless dense
-  uint32_t qh;
-  MetaRaw<FMT> m;
-};
-
-// Word i of unit u of row r.
-template <int FMT>
-__device__ __forceinline__ WordRaw<FMT> load_word(const Mat& w, uint32_t r, int u, int i, int K) {
-  WordRaw<FMT> x;
-  const int word = 4 * u + i;
-  const uint32_t at = r * row_bytes<FMT>(0, K);
-  if constexpr (FMT == QMV_DENSE_BF16) {
-    x.q = load_at<u32x4>(w.p[0], at, 16 * word);
-  } else if constexpr (is_byte(FMT)) {
-    const u32x2 v = load_at<u32x2>(w.p[0], at, 8 * word);
-    x.q[0] = v[0];
-    x.q[1] = v[1];
-  } else {
-    x.q[0] = load_at<uint32_t>(w.p[0], at, 4 * word);
-  }
-  if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
-  if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t>(w.p[1], r * row_bytes<FMT>(1, K), 8 * u + 4 * (i >> 1));
-  x.m = load_meta<FMT, true>(w, r, u, K);
-  return x;
-}
-
-template <int FMT>
-__device__ __forceinline__ void word_values(const WordRaw<FMT>& r, int u, int i, float (&w)[8]) {
-  if constexpr (FMT == QMV_DENSE_BF16) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t v = r.q[e];
-      w[2 * e] = bf16_bits_to_f32(v & 0xFFFFu);
-      w[2 * e + 1] = bf16_bits_to_f32(v >> 16);
-    }
-  } else {
-    const Word8 c{r.q[0], r.q[1], r.qh};
-    const Affine f = affine_of<FMT>(r.m, u);
-    const bool second = FMT == QMV_Q6K && i >= 2;
-    decode8<FMT>(c, second ? f.a1 : f.a0, second ? f.b1 : f.b0, i, w);
-  }
 }
 
 // ---------------------------------------------------------------- activations

@@ -10,28 +10,17 @@ namespace qmv {
 hipError_t launch_glu_fwd_a(int fmt, bool f16, const GluFwdArgs& p, hipStream_t s);
 hipError_t launch_glu_fwd_b(int fmt, bool f16, const GluFwdArgs& p, hipStream_t s);
 hipError_t launch_glu_fwd_c(int fmt, bool f16, const GluFwdArgs& p, hipStream_t s);
-hipError_t launch_glu_bwd_a(int fmt, bool f16, const GluBwdArgs& p, int splits, hipStream_t s);
-hipError_t launch_glu_bwd_b(int fmt, bool f16, const GluBwdArgs& p, int splits, hipStream_t s);
-hipError_t launch_glu_bwd_c(int fmt, bool f16, const GluBwdArgs& p, int splits, hipStream_t s);
+hipError_t launch_glu_bwd_a(int fmt, bool f16, const GluBwdArgs& p, const GluBwdPlan& plan, hipStream_t s);
+hipError_t launch_glu_bwd_b(int fmt, bool f16, const GluBwdArgs& p, const GluBwdPlan& plan, hipStream_t s);
+hipError_t launch_glu_bwd_c(int fmt, bool f16, const GluBwdArgs& p, const GluBwdPlan& plan, hipStream_t s);
 
 namespace {
 
 constexpr int kThreads = 256;
 
-// dG = dH U act'(G), dU = dH act(G), eight values per thread.  Each thread
-// reads its values before it writes them, so dG and dU may be any of the
-// inputs' buffers.  n values in all.
+// Eight values: dG = dH U act'(G), dU = dH act(G).
 template <bool F16, int ACT>
-__global__ __launch_bounds__(kThreads) void glu_dgates_kernel(const uint16_t* g, const uint16_t* u, const uint16_t* dh,
-                                                              uint16_t* dg, uint16_t* du, int64_t n) {
-  const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8;
-  if (at >= n) return;
-  const bool whole = at + 8 <= n;
-  const int left = int(min(n - at, int64_t(8)));
-  const u32x4 gv = whole ? *reinterpret_cast<const u32x4*>(g + at) : load_part(g + at, left);
-  const u32x4 uv = whole ? *reinterpret_cast<const u32x4*>(u + at) : load_part(u + at, left);
-  const u32x4 hv = whole ? *reinterpret_cast<const u32x4*>(dh + at) : load_part(dh + at, left);
-  u32x4 og, ou;
+__device__ __forceinline__ void dgates8(u32x4 gv, u32x4 uv, u32x4 hv, u32x4& og, u32x4& ou) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float a[2], b[2];
@@ -47,16 +36,57 @@ __global__ __launch_bounds__(kThreads) void glu_dgates_kernel(const uint16_t* g,
     og[i] = pack16<F16>(a[0], a[1]);
     ou[i] = pack16<F16>(b[0], b[1]);
   }
-  if (whole) {
-    *reinterpret_cast<u32x4*>(dg + at) = og;
-    *reinterpret_cast<u32x4*>(du + at) = ou;
-  } else {
+}
+
+// The n (1 .. 8) first of eight 16-bit values to p.
+__device__ __forceinline__ void store_part(uint16_t* p, u32x4 v, int n) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) {
-        dg[at + e] = uint16_t(og[e >> 1] >> (16 * (e & 1)));
-        du[at + e] = uint16_t(ou[e >> 1] >> (16 * (e & 1)));
-      }
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t w = v[e >> 1];
+    if (e < n) p[e] = uint16_t(w >> (16 * (e & 1)));
+  }
+}
+
+// The elementwise half, n = M N values in all (a multiple of 8).  Each thread
+// reads its values before it writes them, so dG and dU may be any of the
+// inputs' buffers.  Bound by memory: 5 x 2 bytes per value.
+template <bool F16, int ACT>
+__global__ __launch_bounds__(kThreads) void glu_dgates_kernel(const uint16_t* g, const uint16_t* u, const uint16_t* dh,
+                                                              uint16_t* dg, uint16_t* du, int64_t n) {
+  const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8;
+  if (at >= n) return;
+  u32x4 og, ou;
+  dgates8<F16, ACT>(*reinterpret_cast<const u32x4*>(g + at), *reinterpret_cast<const u32x4*>(u + at),
+                    *reinterpret_cast<const u32x4*>(dh + at), og, ou);
+  *reinterpret_cast<u32x4*>(dg + at) = og;
+  *reinterpret_cast<u32x4*>(du + at) = ou;
+}
+
+// The same for rows that are no multiple of 8 long: dG and dU also go to copies
+// with rows of ld values, zeros behind the N-th, which the product reads (its
+// 16-byte pieces need the alignment).
+template <bool F16, int ACT>
+__global__ __launch_bounds__(kThreads) void glu_dgates_ragged_kernel(const uint16_t* g, const uint16_t* u,
+                                                                     const uint16_t* dh, uint16_t* dg, uint16_t* du,
+                                                                     uint16_t* cg, uint16_t* cu, int M, int N, int ld) {
+  const int64_t id = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  const int per = ld >> 3;
+  const int64_t m = id / per;
+  if (m >= M) return;
+  const int n = int(id - m * per) * 8, left = min(8, N - n);
+  const int64_t at = m * N + n;
+  const bool whole = left == 8;
+  u32x4 og, ou;
+  dgates8<F16, ACT>(whole ? load8(g + at) : load_part(g + at, left), whole ? load8(u + at) : load_part(u + at, left),
+                    whole ? load8(dh + at) : load_part(dh + at, left), og, ou);
+  *reinterpret_cast<u32x4*>(cg + m * ld + n) = og;  // dh is zero behind the row, so og and ou are
+  *reinterpret_cast<u32x4*>(cu + m * ld + n) = ou;
+  if (whole) {
+    __builtin_memcpy(dg + at, &og, 16);
+    __builtin_memcpy(du + at, &ou, 16);
+  } else {
+    store_part(dg + at, og, left);
+    store_part(du + at, ou, left);
   }
 }
 
@@ -72,11 +102,40 @@ __global__ __launch_bounds__(kThreads) void glu_join_kernel(const float* part, u
 
 }  // namespace
 
-int glu_backward_splits(int64_t N, int64_t K, int64_t M) {
-  const int64_t bm = M <= 32 ? 32 : 128;
-  const int64_t tiles = ((K + 127) / 128) * ((M + bm - 1) / bm);
-  const int64_t steps = 2 * ((N + 63) / 64);
-  return int(std::max<int64_t>(1, std::min<int64_t>({512 / tiles, steps / 4, 32})));
+// Measured on W4A16 (us): a stage of 32 rows takes 0.75 with the 256 x 256 tile
+// (one workgroup per compute unit), 0.45 with 128 x 128 alone on its unit and
+// 0.75 for two of them; a split's partial sums cost their write and read at
+// 4 TB/s and a launch.  The cut with the smallest estimate is taken.
+GluBwdPlan glu_backward_plan(int64_t N, int64_t K, int64_t M) {
+  GluBwdPlan best{};
+  const int64_t stages = 2 * ((N + 31) / 32);
+  double best_us = 0;
+  auto consider = [&](int tile, int64_t tiles, int splits) {
+    const int64_t steps = ((stages + splits - 1) / splits + 3) / 4 * 4;
+    splits = int((stages + steps - 1) / steps);  // no empty split
+    const int64_t groups = tiles * splits;
+    double rounds = 0;
+    if (tile == 2) rounds = double((groups + 255) / 256) * 0.75;
+    else if (tile == 1) rounds = groups <= 256 ? 0.45 : double((groups + 511) / 512) * 0.75;
+    else rounds = groups <= 256 ? 0.35 : groups <= 512 ? 0.45 : double((groups + 767) / 768) * 0.6;
+    double us = 8.0 + rounds * double(steps);
+    if (splits > 1) us += 3.0 + double(splits) * double(M) * double(K) * 8e-6 / 4.0;
+    if (best.tiles && us >= best_us) return;
+    best_us = us;
+    best = GluBwdPlan{tile, splits, int(steps), 0, tiles, splits > 1 ? splits * M * K * 4 : 0, 0};
+  };
+  for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+    if (splits > 1 && stages / splits < 8) break;
+    if (M <= 64) {
+      consider(0, (K + 127) / 128, splits);
+    } else {
+      consider(1, ((K + 127) / 128) * ((M + 127) / 128), splits);
+      consider(2, ((K + 255) / 256) * ((M + 255) / 256), splits);
+    }
+  }
+  best.ld = int((N + 7) / 8 * 8);
+  if (N % 8) best.copy_bytes = (M * best.ld * 2 + 15) / 16 * 16;
+  return best;
 }
 
 hipError_t launch_glu_fwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_t* Wg, const uint8_t* Wu,
@@ -92,32 +151,45 @@ hipError_t launch_glu_fwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_
 
 hipError_t launch_glu_bwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_t* Wg, const uint8_t* Wu,
                           const uint16_t* G, const uint16_t* U, const uint16_t* dH, bool f16, int act, uint16_t* dG,
-                          uint16_t* dU, uint16_t* dX, float* ws, int splits, hipStream_t s) {
+                          uint16_t* dU, uint16_t* dX, uint8_t* ws, hipStream_t s) {
   const Planes pl = planes_of(fmt, N, K);
+  const GluBwdPlan plan = glu_backward_plan(N, K, M);
   const int64_t mn = M * N, mk = M * K;
-  const dim3 eg(static_cast<unsigned>((mn + 8 * kThreads - 1) / (8 * kThreads)));
-  auto gates = [&]<int ACT>() {
-    if (f16) hipLaunchKernelGGL((glu_dgates_kernel<true, ACT>), eg, dim3(kThreads), 0, s, G, U, dH, dG, dU, mn);
-    else hipLaunchKernelGGL((glu_dgates_kernel<false, ACT>), eg, dim3(kThreads), 0, s, G, U, dH, dG, dU, mn);
+  uint16_t *cg = dG, *cu = dU;
+  if (plan.copy_bytes) {
+    cg = reinterpret_cast<uint16_t*>(ws + plan.part_bytes);
+    cu = reinterpret_cast<uint16_t*>(ws + plan.part_bytes + plan.copy_bytes);
+  }
+  auto gates = [&]<bool F16, int ACT>() {
+    if (plan.copy_bytes) {
+      const dim3 grid(unsigned((M * (plan.ld / 8) + kThreads - 1) / kThreads));
+      hipLaunchKernelGGL((glu_dgates_ragged_kernel<F16, ACT>), grid, dim3(kThreads), 0, s, G, U, dH, dG, dU, cg, cu,
+                         int(M), int(N), plan.ld);
+    } else {
+      const dim3 grid(unsigned((mn + 8 * kThreads - 1) / (8 * kThreads)));
+      hipLaunchKernelGGL((glu_dgates_kernel<F16, ACT>), grid, dim3(kThreads), 0, s, G, U, dH, dG, dU, mn);
+    }
   };
-  if (act == QMV_ACT_SILU) gates.template operator()<QMV_ACT_SILU>();
-  else if (act == QMV_ACT_GELU_TANH) gates.template operator()<QMV_ACT_GELU_TANH>();
-  else gates.template operator()<QMV_ACT_GELU>();
+  auto by_act = [&]<bool F16>() {
+    if (act == QMV_ACT_SILU) gates.template operator()<F16, QMV_ACT_SILU>();
+    else if (act == QMV_ACT_GELU_TANH) gates.template operator()<F16, QMV_ACT_GELU_TANH>();
+    else gates.template operator()<F16, QMV_ACT_GELU>();
+  };
+  if (f16) by_act.template operator()<true>();
+  else by_act.template operator()<false>();
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int steps = int(2 * ((N + 63) / 64));
-  const int per = (steps + splits - 1) / splits;
-  splits = (steps + per - 1) / per;  // no empty split
-  const GluBwdArgs p{mat_of(Wg, pl), mat_of(Wu, pl), dG, dU, dX, splits > 1 ? ws : nullptr, int(M), int(N), int(K), per};
+  float* part = plan.splits > 1 ? reinterpret_cast<float*>(ws) : nullptr;
+  const GluBwdArgs p{mat_of(Wg, pl), mat_of(Wu, pl), cg, cu, dX, part, int(M), int(N), int(K), plan.ld, plan.steps};
   switch (fmt) {
-    case QMV_W4A16_G64: case QMV_Q4K: case QMV_DENSE_BF16: e = launch_glu_bwd_a(fmt, f16, p, splits, s); break;
-    case QMV_Q8_0: case QMV_Q6K: case QMV_I8_ROW: e = launch_glu_bwd_b(fmt, f16, p, splits, s); break;
-    default: e = launch_glu_bwd_c(fmt, f16, p, splits, s); break;
+    case QMV_W4A16_G64: case QMV_Q4K: case QMV_DENSE_BF16: e = launch_glu_bwd_a(fmt, f16, p, plan, s); break;
+    case QMV_Q8_0: case QMV_Q6K: case QMV_I8_ROW: e = launch_glu_bwd_b(fmt, f16, p, plan, s); break;
+    default: e = launch_glu_bwd_c(fmt, f16, p, plan, s); break;
   }
-  if (e != hipSuccess || splits == 1) return e;
+  if (e != hipSuccess || !part) return e;
   const dim3 jg(static_cast<unsigned>((mk + 4 * kThreads - 1) / (4 * kThreads)));
-  if (f16) hipLaunchKernelGGL(glu_join_kernel<true>, jg, dim3(kThreads), 0, s, ws, dX, mk, splits);
-  else hipLaunchKernelGGL(glu_join_kernel<false>, jg, dim3(kThreads), 0, s, ws, dX, mk, splits);
+  if (f16) hipLaunchKernelGGL(glu_join_kernel<true>, jg, dim3(kThreads), 0, s, part, dX, mk, plan.splits);
+  else hipLaunchKernelGGL(glu_join_kernel<false>, jg, dim3(kThreads), 0, s, part, dX, mk, plan.splits);
   return hipGetLastError();
 }
 

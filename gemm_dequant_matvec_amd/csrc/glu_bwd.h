@@ -1,95 +1,134 @@
 // Backward pass of the gated products: dX = dG Wg + dU Wu, on the matrix cores.
 #pragma once
 
+#include <utility>
+
 #include "gemm16.h"
 
 namespace qmv {
 
 struct GluBwdArgs {
   Mat wg, wu;
-  const uint16_t *dg, *du;
+  const uint16_t *dg, *du;  // [M][ld], ld a multiple of 8; zeros where n >= N
   uint16_t* dx;
-  float* part;      // [splits][M][K] partial sums, or null: one split, dx written
-  int M, N, K;
-  int steps;        // contraction steps per split
+  float* part;              // [splits][M][K] partial sums, or null: one split, dx written
+  int M, N, K, ld;
+  int steps;                // stages per split, a multiple of 4
 };
 
 namespace {
 
-// Rows of the tile are BR columns k of dX, its depth runs over n: first the
-// gate rows, then the up rows, 64 per step.
+// The decoded tile of a stage: 32 rows n of BR columns k, as the weights lie in
+// memory.  The matrix cores want for each k eight consecutive n, which
+// ds_read_b64_tr_b16 gathers: of 16 lanes, lanes 4 j .. 4 j + 3 name 16
+// consecutive k of row j, and lane l receives the four rows' values of k = l.
+// 64-byte blocks of a row (one unit) are exchanged by n % 4 and the 16-byte
+// pieces of a pair by n / 4 % 2, so that neither these reads (four rows of one
+// unit) nor the decoders' writes (rows n and n + 4 of 8 half units) meet in a
+// bank.  In 16-byte pieces: row n, unit ul of the tile, half h, piece i.
+template <int BR>
+__device__ __forceinline__ int rows_at(int n, int ul, int h, int i) {
+  return n * (BR / 8) + (ul ^ (n & 3)) * 4 + 2 * h + (i ^ ((n >> 2) & 1));
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ u32x2 read_tr(const u32x4* A, int pos8) {  // pos8: in 8-byte units
+  lds_s16x4* p = (lds_s16x4*)(reinterpret_cast<const u32x2*>(A) + pos8);
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+}
+
+// Loads of load_half with a lane's unit, at least.
+template <int FMT>
+constexpr int kHalfLoads = FMT == QMV_Q6K ? 4 : is_fifth(FMT) ? 3 : 2;
+
+// RB, TB: 32-column blocks of dX and 32-token blocks per wave; WR x WT waves.
+//
+// The depth is n: first the gate rows, then the up rows, 32 to a stage.  Tokens
+// (dG, dU) go straight from global memory into a ring of four LDS tiles, three
+// stages ahead.  A thread decodes half a unit of one row per stage, from
+// registers that were loaded six stages ahead, into the ring of weight tiles, two
+// stages ahead (dense bf16 rows need no decoding and are copied like the
+// tokens).  As in the forward kernel the first fragments of a stage are read
+// before the barrier that ends the stage before it.
 template <int FMT, bool F16, int RB, int TB, int WR, int WT>
 __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs p) {
   constexpr int NT = 64 * WR * WT;
   constexpr int BR = 32 * RB * WR, BM = 32 * TB * WT;
-  constexpr int BPT = BR / NT > 0 ? BR / NT : 1;  // 8 x 8 weight blocks per thread and step
-  constexpr int XPT = BM * 8 / NT;
-  constexpr bool SOME = BR < NT;                   // only the first BR threads hold a block
-  static_assert((SOME || BPT * NT == BR) && XPT * NT == BM * 8);
+  constexpr int XPT = BM * 4 / NT, APT = BR * 4 / NT;  // 16-byte pieces per thread and stage
+  constexpr bool DIRECT = FMT == QMV_DENSE_BF16 && !F16;
+  static_assert(2 * BR == NT && XPT * NT == BM * 4 && APT * NT == BR * 4);
 
-  __shared__ u32x4 As[2][BR * 8];
-  __shared__ u32x4 Xs[2][BM * 8];
+  __shared__ u32x4 A0[BR * 4], A1[BR * 4], A2[BR * 4], A3[BR * 4];
+  __shared__ u32x4 X0[BM * 4], X1[BM * 4], X2[BM * 4], X3[BM * 4];
+  asm volatile("" ::"v"(A0), "v"(A1), "v"(A2), "v"(A3) : "memory");  // see the forward kernel
+  asm volatile("" ::"v"(X0), "v"(X1), "v"(X2), "v"(X3) : "memory");
+  auto At = [&]<int S>() { return (S & 3) == 0 ? A0 : (S & 3) == 1 ? A1 : (S & 3) == 2 ? A2 : A3; };
+  auto Xt = [&]<int S>() { return (S & 3) == 0 ? X0 : (S & 3) == 1 ? X1 : (S & 3) == 2 ? X2 : X3; };
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / WT, wt = wave % WT;
-  const int k0 = blockIdx.x * BR, m0 = blockIdx.y * BM;
-  const int N = p.N, K = p.K;
-  const int half = (N + 63) >> 6;  // steps per matrix
-  const int first = blockIdx.z * p.steps, ns = min(p.steps, 2 * half - first);
+  const TileId id0 = tile_of_block(p.K, BR, p.M, BM);
+  const int k0 = id0.x * BR, m0 = id0.y * BM;
+  const int N = p.N, K = p.K, U = K >> 5, ld = p.ld;
+  const int NS = (N + 31) >> 5;  // stages per matrix
+  const int first = blockIdx.y * p.steps, end = min(first + p.steps, 2 * NS);
 
-  struct Set {
-    WordRaw<FMT> w[BPT][8];
-    u32x4 x[XPT];
+  // this thread's half unit: of row nl of a stage, unit ul of the tile
+  const int half = tid & 1;
+  constexpr int UB = BR == 256 ? 1 : 0;  // bits of ul past the lowest two
+  const int nr = tid >> (4 + UB);        // row bits 0, 1, 3, 4
+  const int ul = ((tid >> 1) & 3) | (UB ? ((tid >> 4) & 1) * 4 : 0);
+  const int nl = (nr & 3) | ((tid >> 3) & 1) * 4 | (nr >> 2) * 8;
+  const int u = min((k0 >> 5) + ul, U - 1);
+  auto at_row = [&](int t, int& nb) {  // matrix and first row of stage t (clamped to the last stage)
+    t = min(t, 2 * NS - 1);
+    const bool up = t >= NS;
+    nb = 32 * (up ? t - NS : t);
+    Mat m;
+#pragma unroll
+    for (int i = 0; i < kPlanes<FMT>; ++i) m.p[i] = (up ? p.wu.p[i] : p.wg.p[i]) + int64_t(nb) * row_bytes<FMT>(i, K);
+    return m;
   };
-  constexpr int KG = BR / 8;  // groups of 8 columns
-  auto load = [&](Set& s, int step) {
-    const bool up = step >= half;
-    const int nb = 64 * (up ? step - half : step);
-    const Mat wn = from_row<FMT>(up ? p.wu : p.wg, nb, K);
-    const uint16_t* d = up ? p.du : p.dg;
+  auto load = [&](int t) {
+    int nb;
+    const Mat w = at_row(t, nb);
+    return load_half<FMT, true>(w, min(nl, N - 1 - nb), u, half, K);
+  };
+  auto decode = [&](const HalfRaw<FMT>& c, int i, u32x4* A) {
+    A[rows_at<BR>(nl, ul, half, i)] = half_piece<FMT, F16>(c, u, half, i);
+  };
+  // dense rows: LDS slot tid + t * NT is row (tid + t * NT) / (BR / 8)
+  auto copy_a = [&](int st, u32x4* A) {
+    int nb;
+    const Mat w = at_row(st, nb);
+    const Buf b = buffer_of(scalar_base(w.p[0]));
 #pragma unroll
-    for (int j = 0; j < BPT; ++j) {
-      const int id = (j * NT + tid) % BR, kg = id % KG, ng = id / KG;
-      const int kw = min((k0 >> 3) + kg, (K >> 3) - 1);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s.w[j][e] = load_word<FMT>(wn, min(nb + 8 * ng + e, N - 1) - nb, kw >> 2, kw & 3, K);
-    }
-#pragma unroll
-    for (int j = 0; j < XPT; ++j) {
-      const int id = j * NT + tid, r = id >> 3, c = id & 7;
-      const int m = min(m0 + r, p.M - 1), n = nb + 8 * c;
-      const uint16_t* q = d + int64_t(m) * N + n;
-      if (n + 8 <= N) s.x[j] = load8(q);
-      else s.x[j] = load_part(q, N - n);  // zeros where n >= N
+    for (int t = 0; t < APT; ++t) {
+      const int id = tid + t * NT, n = id / (BR / 8), s = id % (BR / 8);
+      const int unit = min((k0 >> 5) + ((s >> 2) ^ (n & 3)), U - 1);
+      copy_to_lds(b, uint32_t(min(n, N - 1 - nb)) * uint32_t(2 * K) + 64 * unit + 32 * ((s >> 1) & 1) +
+                         16 * ((s & 1) ^ ((n >> 2) & 1)), 0, A + t * NT + wave * 64);
     }
   };
-  auto stage = [&](const Set& s, int step, int buf) {
-    const bool up = step >= half;
-    const int nb = 64 * (up ? step - half : step);
+  // Tokens: LDS slot tid + t * NT of a tile is row (tid + t * NT) / 4.  Pieces past
+  // the row, and all pieces of a stage past the split's end, get an offset past
+  // the buffer, which reads as zero.
+  const uint8_t* gx = reinterpret_cast<const uint8_t*>(p.dg + int64_t(m0) * ld);
+  const uint8_t* ux = reinterpret_cast<const uint8_t*>(p.du + int64_t(m0) * ld);
+  const int xc = (tid & 3) ^ ((tid >> 4) & 3);
+  uint32_t xo[XPT];
 #pragma unroll
-    for (int j = 0; j < XPT; ++j) {
-      const int id = j * NT + tid, r = id >> 3, c = id & 7;
-      Xs[buf][tile_at(r, c)] = s.x[j];
-    }
+  for (int t = 0; t < XPT; ++t)
+    xo[t] = uint32_t(min(m0 + t * (NT / 4) + (tid >> 2), p.M - 1) - m0) * uint32_t(2 * ld) + 16 * xc;
+  auto copy_x = [&](int st, u32x4* X) {
+    const bool up = st >= NS;
+    const int nb = 32 * (up ? st - NS : st);
+    const bool in = st < end && nb + 8 * xc < ld;
+    const Buf b = buffer_of(scalar_base((up ? ux : gx) + 2 * nb), 0x7FFFFFFF);
 #pragma unroll
-    for (int j = 0; j < BPT; ++j) {
-      if (SOME && tid >= BR) break;
-      const int id = (j * NT + tid) % BR, kg = id % KG, ng = id / KG;
-      const int kw = min((k0 >> 3) + kg, (K >> 3) - 1);
-      u32x4 o[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float a[8], b[8];
-        word_values<FMT>(s.w[j][2 * e], kw >> 2, kw & 3, a);
-        word_values<FMT>(s.w[j][2 * e + 1], kw >> 2, kw & 3, b);
-        const bool ina = nb + 8 * ng + 2 * e < N, inb = nb + 8 * ng + 2 * e + 1 < N;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k][e] = pack16<F16>(ina ? a[k] : 0.0f, inb ? b[k] : 0.0f);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) As[buf][tile_at_t(8 * kg + k, ng)] = o[k];
-    }
+    for (int t = 0; t < XPT; ++t) copy_to_lds(b, in ? xo[t] : 0x80000000u, 0, X + t * NT + wave * 64);
   };
 
   f32x16 acc[RB][TB];
@@ -101,73 +140,143 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
       for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.0f;
 
   const int fr = lane & 31, fh = lane >> 5;
-  auto products = [&](int buf) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u32x4 a[RB], b[TB];
-#pragma unroll
-      for (int i = 0; i < RB; ++i) a[i] = As[buf][tile_at_t((wr * RB + i) * 32 + fr, 2 * s + fh)];
-#pragma unroll
-      for (int i = 0; i < TB; ++i) b[i] = Xs[buf][tile_at((wt * TB + i) * 32 + fr, 2 * s + fh)];
-#pragma unroll
-      for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int j = 0; j < TB; ++j) acc[i][j] = mfma32<F16>(a[i], b[j], acc[i][j]);
-    }
+  const int bj = (lane >> 2) & 3, bh = (lane >> 4) & 1, bc = lane & 3;  // transposing reads
+  struct Frag {
+    u32x4 a[RB], b[TB];
   };
-
-  Set s0, s1;
-  const int last = first + ns - 1;
-  load(s0, first);
-  load(s1, min(first + 1, last));
-  stage(s0, first, 0);
-  lds_barrier16();
-  int st = first;
-  for (; st < last; st += 2) {
-    load(s0, min(st + 2, last));
-    stage(s1, st + 1, 1);
-    products(0);
-    lds_barrier16();
-    load(s1, min(st + 3, last));
-    stage(s0, min(st + 2, last), 0);
-    products(1);
-    lds_barrier16();
-  }
-  if (st == last) products(0);
-
+  auto read = [&](Frag& f, const u32x4* A, const u32x4* X, int s) {
 #pragma unroll
-  for (int j = 0; j < TB; ++j) {
-    const int m = m0 + (wt * TB + j) * 32 + fr;
-    if (m >= p.M) continue;
+    for (int i = 0; i < RB; ++i) {
+      const int n = 16 * s + 8 * fh + bj;
+      const u32x2 lo = read_tr(A, 2 * rows_at<BR>(n, wr * RB + i, bh, bc >> 1) + (bc & 1));
+      const u32x2 hi = read_tr(A, 2 * rows_at<BR>(n + 4, wr * RB + i, bh, bc >> 1) + (bc & 1));
+      f.a[i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+#pragma unroll
+    for (int i = 0; i < TB; ++i) f.b[i] = X[tile32_at((wt * TB + i) * 32 + fr, 2 * s + fh)];
+  };
+  auto mul = [&](const Frag& f) {
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int k = k0 + (wr * RB + i) * 32 + 8 * q + 4 * fh;
-        if (k >= K) continue;  // K is a multiple of 32: all four or none
-        f32x4 v;
+      for (int j = 0; j < TB; ++j) acc[i][j] = mfma32<F16>(f.a[i], f.b[j], acc[i][j]);
+  };
+  auto fence = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  HalfRaw<FMT> c[4];
+  if constexpr (DIRECT) {
+    copy_a(first, A0);
+    copy_a(first + 1, A1);
+    copy_a(first + 2, A2);
+  } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
-        const int64_t at = int64_t(m) * K + k;
-        if (p.part)
-          *reinterpret_cast<f32x4*>(p.part + int64_t(blockIdx.z) * p.M * K + at) = v;
-        else
-          *reinterpret_cast<u32x2*>(p.dx + at) = u32x2{pack16<F16>(v[0], v[1]), pack16<F16>(v[2], v[3])};
-      }
+    for (int i = 0; i < 4; ++i) c[i] = load(first + i);
   }
+  copy_x(first, X0);
+  copy_x(first + 1, X1);
+  copy_x(first + 2, X2);
+  if constexpr (!DIRECT) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      decode(c[0], i, A0);
+      decode(c[1], i, A1);
+    }
+    c[0] = load(first + 4);
+    c[1] = load(first + 5);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  lds_barrier16();
+  Frag f0, f1;
+  read(f0, A0, X0, 0);
+#pragma unroll 1
+  for (int st = first; st < end; st += 4) {
+    [&]<int... H>(std::integer_sequence<int, H...>) {
+      (([&] {
+         const u32x4 *A = At.template operator()<H>(), *X = Xt.template operator()<H>();
+         const u32x4 *A1n = At.template operator()<H + 1>(), *X1n = Xt.template operator()<H + 1>();
+         u32x4* A2n = At.template operator()<H + 2>();
+         copy_x(st + H + 3, Xt.template operator()<H + 3>());
+         if constexpr (DIRECT) copy_a(st + H + 3, At.template operator()<H + 3>());
+         fence();
+         read(f1, A, X, 1);
+         if constexpr (!DIRECT) decode(c[(H + 2) & 3], 0, A2n);
+         mul(f0);
+         fence();
+         read(f0, A1n, X1n, 0);
+         if constexpr (!DIRECT) {
+           decode(c[(H + 2) & 3], 1, A2n);
+           c[(H + 2) & 3] = load(st + H + 6);
+         }
+         mul(f1);
+         fence();
+         // Stage H + 2 is whole once the copies of the stage before this one have
+         // landed; certainly issued after those: two stages' loads and this stage's copies.
+         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(DIRECT ? XPT + APT : XPT + 2 * kHalfLoads<FMT>) : "memory");
+         lds_barrier16();
+       }()),
+       ...);
+    }(std::make_integer_sequence<int, 4>{});
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the copies past the end
+  lds_barrier16();
+
+  // C fragment: lane holds columns k = 8 q + 4 fh + e (q, e in 0..3) of token lane % 32
+  if (p.part) {
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      const int m = m0 + (wt * TB + j) * 32 + fr;
+      if (m >= p.M) continue;
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int k = k0 + (wr * RB + i) * 32 + 8 * q + 4 * fh;
+          if (k >= K) continue;  // K is a multiple of 32: all four or none
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+          *reinterpret_cast<f32x4*>(p.part + (int64_t(blockIdx.y) * p.M + m) * K + k) = v;
+        }
+    }
+    return;
+  }
+  // through the wave's own part of LDS, 32 tokens x 64 columns at a time: rows leave whole
+  u32x4* mine = (wave & 1 ? A1 : A0) + (wave >> 1) * (32 * 8);
+#pragma unroll
+  for (int j = 0; j < TB; ++j)
+#pragma unroll
+    for (int g = 0; g < RB; g += 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& v = acc[g + i][j];
+          reinterpret_cast<u32x2*>(mine + tile_at(fr, 4 * i + q))[fh] =
+              u32x2{pack16<F16>(v[4 * q], v[4 * q + 1]), pack16<F16>(v[4 * q + 2], v[4 * q + 3])};
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // written and read by this wave only
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += 8) {
+        const int r = r0 + (lane >> 3), pc = lane & 7;
+        const int m = m0 + (wt * TB + j) * 32 + r, k = k0 + (wr * RB + g) * 32 + 8 * pc;
+        if (m < p.M && k < K) *reinterpret_cast<u32x4*>(p.dx + int64_t(m) * K + k) = mine[tile_at(r, pc)];
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
 }
 
 template <int FMT, bool F16>
-hipError_t glu_bwd_go(const GluBwdArgs& p, int splits, hipStream_t s) {
-  const dim3 grid((p.K + 127) / 128, (p.M + 127) / 128, splits);
-  const int64_t big = int64_t((p.K + 255) / 256) * ((p.M + 255) / 256);
-  if (p.M <= 32)
-    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, 1, 1, 4, 1>), dim3(grid.x, (p.M + 31) / 32, splits), dim3(256), 0, s, p);
-  else if (big >= 256)
-    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, 4, 2, 2, 4>), dim3((p.K + 255) / 256, (p.M + 255) / 256, splits),
-                       dim3(512), 0, s, p);
-  else
+hipError_t glu_bwd_go(const GluBwdArgs& p, const GluBwdPlan& plan, hipStream_t s) {
+  const dim3 grid(unsigned(plan.tiles), unsigned(plan.splits));
+  if (plan.tile == 2)
+    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, 4, 2, 2, 4>), grid, dim3(512), 0, s, p);
+  else if (plan.tile == 1)
     hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, 2, 2, 2, 2>), grid, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, 2, 1, 2, 2>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

@@ -233,7 +233,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   for (int u = runs * SR; u < U; ++u) {
 #pragma unroll
     for (int t = 0; t < XPT; ++t) X0[tid + t * NT] = load_at<u32x4>(xb, xo[t] + 64 * u);
-    const HalfRaw<FMT> r = load_half<FMT>(w, wrow, u, half, K);
+    const HalfRaw<FMT> r = load_half<FMT, false>(w, wrow, u, half, K);
 #pragma unroll
     for (int i = 0; i < 2; ++i) A0[tile32_at(arow, 2 * half + i)] = half_piece<FMT, F16>(r, u, half, i);
     lds_barrier16();
