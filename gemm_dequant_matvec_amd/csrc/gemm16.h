@@ -159,11 +159,16 @@ __device__ __forceinline__ uint32_t lane_offset(uint32_t v) {
   return v;
 }
 
-// A T at byte `row` (a lane's) + `u` of a plane.  LANE: u differs between lanes
-// too and joins the 32-bit offset; else it joins the scalar base.
-template <class T, bool LANE = true>
+// How the addresses of a load differ between the lanes of a wave: only in the
+// row; in the row and in u, which then joins the 32-bit offset instead of the
+// scalar base; or in the matrix too.
+enum By { kByRow, kByUnit, kByMatrix };
+
+// A T at byte `row` (a lane's) + `u` of a plane.
+template <class T, By BY = kByUnit>
 __device__ __forceinline__ T load_at(const uint8_t* plane, uint32_t row, int64_t u = 0) {
-  if constexpr (LANE) return *(const QMV_GLOBAL T*)(scalar_base(plane) + lane_offset(row + uint32_t(u)));
+  if constexpr (BY == kByMatrix) return *reinterpret_cast<const T*>(plane + (row + uint32_t(u)));
+  else if constexpr (BY == kByUnit) return *(const QMV_GLOBAL T*)(scalar_base(plane) + lane_offset(row + uint32_t(u)));
   else return *(const QMV_GLOBAL T*)(scalar_base(plane + u) + lane_offset(row));
 }
 
@@ -182,22 +187,22 @@ struct MetaRaw {
 };
 
 // The scales of unit u of row r.
-template <int FMT, bool LANE>
+template <int FMT, By BY>
 __device__ __forceinline__ MetaRaw<FMT> load_meta(const Mat& w, uint32_t r, int u, int K) {
   MetaRaw<FMT> m;
   constexpr int P = kPlanes<FMT> - 1;  // the plane of the scales (Q6K: of d)
   const uint32_t at = r * row_bytes<FMT>(P, K);
   if constexpr (FMT == QMV_Q8_0 || FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
-    m.v[0] = load_at<uint16_t, LANE>(w.p[P], at, 2 * u);
+    m.v[0] = load_at<uint16_t, BY>(w.p[P], at, 2 * u);
   } else if constexpr (FMT == QMV_W4A16_G64) {
-    m.v[0] = load_at<uint32_t, LANE>(w.p[P], at, 4 * (u >> 1));
+    m.v[0] = load_at<uint32_t, BY>(w.p[P], at, 4 * (u >> 1));
   } else if constexpr (is_super(FMT)) {
-    m.v = load_at<u32x4, LANE>(w.p[P], at, 16 * (u >> 3));
+    m.v = load_at<u32x4, BY>(w.p[P], at, 16 * (u >> 3));
   } else if constexpr (FMT == QMV_Q6K) {
-    m.v[0] = load_at<uint16_t, LANE>(w.p[2], r * row_bytes<FMT>(2, K), 2 * u);
-    m.v[1] = load_at<uint16_t, LANE>(w.p[3], at, 2 * (u >> 3));
+    m.v[0] = load_at<uint16_t, BY>(w.p[2], r * row_bytes<FMT>(2, K), 2 * u);
+    m.v[1] = load_at<uint16_t, BY>(w.p[3], at, 2 * (u >> 3));
   } else if constexpr (FMT == QMV_I8_ROW) {
-    m.v[0] = load_at<uint32_t>(w.p[1], at);
+    m.v[0] = load_at<uint32_t, BY>(w.p[1], at);
   }
   return m;
 }
@@ -278,16 +283,16 @@ struct UnitRaw {
 };
 
 // Unit u of row r.
-template <int FMT, bool LANE>
+template <int FMT, By BY>
 __device__ __forceinline__ UnitRaw<FMT> load_unit(const Mat& w, uint32_t r, int u, int K) {
   UnitRaw<FMT> x;
   constexpr int NQ = UnitRaw<FMT>::NQ;
   const uint32_t at = r * row_bytes<FMT>(0, K);
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) x.q[i] = load_at<u32x4, LANE>(w.p[0], at, int64_t(u) * (16 * NQ) + 16 * i);
-  if constexpr (is_fifth(FMT)) x.qh[0] = load_at<uint32_t, LANE>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
-  if constexpr (FMT == QMV_Q6K) x.qh = load_at<u32x2, LANE>(w.p[1], r * row_bytes<FMT>(1, K), 8 * u);
-  x.m = load_meta<FMT, LANE>(w, r, u, K);
+  for (int i = 0; i < NQ; ++i) x.q[i] = load_at<u32x4, BY>(w.p[0], at, int64_t(u) * (16 * NQ) + 16 * i);
+  if constexpr (is_fifth(FMT)) x.qh[0] = load_at<uint32_t, BY>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
+  if constexpr (FMT == QMV_Q6K) x.qh = load_at<u32x2, BY>(w.p[1], r * row_bytes<FMT>(1, K), 8 * u);
+  x.m = load_meta<FMT, BY>(w, r, u, K);
   return x;
 }
 
@@ -352,24 +357,24 @@ __device__ __forceinline__ void read_codes(u32x4 (&q)[2], const u32x4* R, int r,
   }
 }
 
-// Half h (a lane's) of unit u (LANE: a lane's too), from global memory.
-template <int FMT, bool LANE>
+// Half h (a lane's) of unit u (a lane's too if BY is kByUnit), from global memory.
+template <int FMT, By BY>
 __device__ __forceinline__ HalfRaw<FMT> load_half(const Mat& w, uint32_t r, int u, int h, int K) {
   HalfRaw<FMT> x;
   constexpr int B = 32 / kChunk<FMT>;  // bytes of half a unit's codes
   const uint32_t at = r * row_bytes<FMT>(0, K) + B * h;
   const int64_t ub = int64_t(u) * (2 * B);
   if constexpr (B == 8) {
-    const u32x2 v = load_at<u32x2, LANE>(w.p[0], at, ub);
+    const u32x2 v = load_at<u32x2, BY>(w.p[0], at, ub);
     x.q[0][0] = v[0];
     x.q[0][1] = v[1];
   } else {
-    x.q[0] = load_at<u32x4, LANE>(w.p[0], at, ub);
-    if constexpr (B == 32) x.q[1] = load_at<u32x4, LANE>(w.p[0], at, ub + 16);
+    x.q[0] = load_at<u32x4, BY>(w.p[0], at, ub);
+    if constexpr (B == 32) x.q[1] = load_at<u32x4, BY>(w.p[0], at, ub + 16);
   }
-  if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t, LANE>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
-  if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t, LANE>(w.p[1], r * row_bytes<FMT>(1, K) + 4 * h, 8 * u);
-  x.m = load_meta<FMT, LANE>(w, r, u, K);
+  if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t, BY>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
+  if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t, BY>(w.p[1], r * row_bytes<FMT>(1, K) + 4 * h, 8 * u);
+  x.m = load_meta<FMT, BY>(w, r, u, K);
   return x;
 }
 
@@ -425,7 +430,7 @@ __device__ __forceinline__ RunMeta<FMT> load_run_meta(const Mat& w, uint32_t r, 
   constexpr int S = kRun, P = kPlanes<FMT> - 1;
   const uint32_t mt = r * row_bytes<FMT>(P, K), ht = r * row_bytes<FMT>(1, K);
   if constexpr (is_fifth(FMT)) {
-    const u32x4 a = load_at<u32x4_a4, false>(w.p[1], ht, 4 * u), b = load_at<u32x4_a4, false>(w.p[1], ht, 4 * u + 16);
+    const u32x4 a = load_at<u32x4_a4, kByRow>(w.p[1], ht, 4 * u), b = load_at<u32x4_a4, kByRow>(w.p[1], ht, 4 * u + 16);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       x.qh[s] = a[s];
@@ -433,18 +438,18 @@ __device__ __forceinline__ RunMeta<FMT> load_run_meta(const Mat& w, uint32_t r, 
     }
   }
   if constexpr (FMT == QMV_Q8_0 || FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
-    x.m = load_at<u32x4_a2, false>(w.p[P], mt, 2 * u);
+    x.m = load_at<u32x4_a2, kByRow>(w.p[P], mt, 2 * u);
   } else if constexpr (FMT == QMV_W4A16_G64) {
-    x.m = load_at<u32x4_a4, false>(w.p[P], mt, 2 * u);
+    x.m = load_at<u32x4_a4, kByRow>(w.p[P], mt, 2 * u);
   } else if constexpr (is_super(FMT)) {
-    x.m = load_at<u32x4, false>(w.p[P], mt, 16 * (u >> 3));
+    x.m = load_at<u32x4, kByRow>(w.p[P], mt, 16 * (u >> 3));
   } else if constexpr (FMT == QMV_Q6K) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) x.qh[s] = load_at<uint32_t, false>(w.p[1], ht + 4 * h, 8 * (u + s));
-    x.m = load_at<u32x4, false>(w.p[2], r * row_bytes<FMT>(2, K), 2 * u);
-    x.d = load_at<uint16_t, false>(w.p[3], mt, 2 * (u >> 3));
+    for (int s = 0; s < S; ++s) x.qh[s] = load_at<uint32_t, kByRow>(w.p[1], ht + 4 * h, 8 * (u + s));
+    x.m = load_at<u32x4, kByRow>(w.p[2], r * row_bytes<FMT>(2, K), 2 * u);
+    x.d = load_at<uint16_t, kByRow>(w.p[3], mt, 2 * (u >> 3));
   } else if constexpr (FMT == QMV_I8_ROW) {
-    x.m[0] = load_at<uint32_t>(w.p[1], mt);
+    x.m[0] = load_at<uint32_t, kByRow>(w.p[1], mt);
   }
   return x;
 }

@@ -94,7 +94,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
   auto load = [&](int t) {
     int nb;
     const Mat w = at_row(t, nb);
-    return load_half<FMT, true>(w, min(nl, N - 1 - nb), u, half, K);
+    return load_half<FMT, kByUnit>(w, min(nl, N - 1 - nb), u, half, K);
   };
   auto decode = [&](const HalfRaw<FMT>& c, int i, u32x4* A) {
     A[rows_at<BR>(nl, ul, half, i)] = half_piece<FMT, F16>(c, u, half, i);

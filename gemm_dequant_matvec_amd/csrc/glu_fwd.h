@@ -233,7 +233,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   for (int u = runs * SR; u < U; ++u) {
 #pragma unroll
     for (int t = 0; t < XPT; ++t) X0[tid + t * NT] = load_at<u32x4>(xb, xo[t] + 64 * u);
-    const HalfRaw<FMT> r = load_half<FMT, false>(w, wrow, u, half, K);
+    const HalfRaw<FMT> r = load_half<FMT, kByRow>(w, wrow, u, half, K);
 #pragma unroll
     for (int i = 0; i < 2; ++i) A0[tile32_at(arow, 2 * half + i)] = half_piece<FMT, F16>(r, u, half, i);
     lds_barrier16();
@@ -300,57 +300,67 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   else out.template operator()<QMV_ACT_GELU>();
 }
 
-// Few tokens: a weight stream.  A workgroup owns 16 gate and the same 16 up
-// rows; its W waves split K in steps of 128 (wave w takes steps w, w + W, ...).
-// Lane group g (16 lanes) of a fragment holds one 32-k unit, word s of it being
-// k = 32 g + 8 s .. + 7 of MFMA s; the token operand follows the same order
-// straight from global memory (no two waves share a step, so LDS would only be
-// a detour).  The partial tiles meet in LDS and are added in wave order.
-template <int FMT, bool F16, int FM, int W>
+// Few tokens: a weight stream.  A workgroup owns 16 FN gate and the same up
+// rows; its W waves split K in steps of 128 (wave w takes steps w, w + W, ...,
+// two of them in flight).  Lane group g (16 lanes) of a fragment holds one 32-k
+// unit, word s of it being k = 32 g + 8 s .. + 7 of MFMA s; the token operand
+// follows the same order straight from global memory (no two waves share a
+// step, so LDS would only be a detour).  The partial tiles meet in LDS and are
+// added in wave order.
+template <int FMT, bool F16, int FM, int FN, int W>
 __global__ __launch_bounds__(64 * W) void glu_fwd_few_kernel(const GluFwdArgs p) {
-  __shared__ f32x4 red[W][2 * FM][64];
+  constexpr int T = 2 * FN * FM;  // partial 16 x 16 tiles per wave
+  __shared__ f32x4 red[W][T][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 15, g4 = lane >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * FM;
+  const int n0 = blockIdx.x * 16 * FN, m0 = blockIdx.y * 16 * FM;
   const int K = p.K, U = K >> 5, nk = (K + 127) >> 7;
-  const uint32_t row = min(n0 + fr, p.N - 1) - n0;
   const Mat wg = from_row<FMT>(p.wg, n0, K), wu = from_row<FMT>(p.wu, n0, K);
+  const uint8_t* xb = reinterpret_cast<const uint8_t*>(p.x + int64_t(m0) * K);
 
   struct Set {
-    UnitRaw<FMT> g, u;
+    UnitRaw<FMT> w[2][FN];
     u32x4 x[FM][4];
   };
   auto load = [&](Set& s, int step) {
     const int u = min(4 * step + g4, U - 1);
-    s.g = load_unit<FMT, true>(wg, row, u, K);
-    s.u = load_unit<FMT, true>(wu, row, u, K);
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      const uint32_t row = min(n0 + 16 * i + fr, p.N - 1) - n0;
+      s.w[0][i] = load_unit<FMT, kByUnit>(wg, row, u, K);
+      s.w[1][i] = load_unit<FMT, kByUnit>(wu, row, u, K);
+    }
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      const int m = min(m0 + 16 * j + fr, p.M - 1);
+      const uint32_t m = min(m0 + 16 * j + fr, p.M - 1) - m0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        s.x[j][i] = *reinterpret_cast<const u32x4*>(p.x + int64_t(m) * K + 32 * u + 8 * i);
+      for (int i = 0; i < 4; ++i) s.x[j][i] = load_at<u32x4>(xb, m * uint32_t(2 * K) + 64 * u + 16 * i);
     }
   };
-  f32x4 acc[2][FM];
+  f32x4 acc[2][FN][FM];
 #pragma unroll
-  for (int j = 0; j < FM; ++j) acc[0][j] = acc[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[0][i][j] = acc[1][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto use = [&](const Set& s, int step) {
     const int u = 4 * step + g4;
     const bool in = u < U;
     const u32x4 zero = {0, 0, 0, 0};
-    const Affine fg = affine_of<FMT>(s.g.m, min(u, U - 1)), fu = affine_of<FMT>(s.u.m, min(u, U - 1));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const u32x4 vg = unit_piece<FMT, F16>(s.g, fg, i), vu = unit_piece<FMT, F16>(s.u, fu, i);
-      const u32x4 ag = in ? vg : zero, au = in ? vu : zero;
+      u32x4 b[FM];
 #pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        const u32x4 b = in ? s.x[j][i] : zero;
-        acc[0][j] = mfma16<F16>(ag, b, acc[0][j]);
-        acc[1][j] = mfma16<F16>(au, b, acc[1][j]);
-      }
+      for (int j = 0; j < FM; ++j) b[j] = in ? s.x[j][i] : zero;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+          const u32x4 v = unit_piece<FMT, F16>(s.w[t][n], affine_of<FMT>(s.w[t][n].m, min(u, U - 1)), i);
+          const u32x4 a = in ? v : zero;
+#pragma unroll
+          for (int j = 0; j < FM; ++j) acc[t][n][j] = mfma16<F16>(a, b[j], acc[t][n][j]);
+        }
     }
   };
   Set s0, s1;
@@ -358,29 +368,30 @@ __global__ __launch_bounds__(64 * W) void glu_fwd_few_kernel(const GluFwdArgs p)
   load(s1, wave + W);
   for (int st = wave; st < nk; st += 2 * W) {
     use(s0, st);
-    load(s0, st + 2 * W);
-    use(s1, st + W);  // all zeros past the last step
-    load(s1, st + 3 * W);
+    if (st + 2 * W < nk) load(s0, st + 2 * W);
+    if (st + W < nk) use(s1, st + W);
+    if (st + 3 * W < nk) load(s1, st + 3 * W);
   }
 #pragma unroll
-  for (int j = 0; j < FM; ++j) {
-    red[wave][2 * j][lane] = acc[0][j];
-    red[wave][2 * j + 1][lane] = acc[1][j];
-  }
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) red[wave][(i * FM + j) * 2 + t][lane] = acc[t][i][j];
   lds_barrier16();
-  // C fragment: lane holds rows n0 + 4 g4 + e of token fr
-  for (int j = wave; j < FM; j += W) {
-    f32x4 g = red[0][2 * j][lane], u = red[0][2 * j + 1][lane];
+  // C fragment: lane holds rows n0 + 16 i + 4 g4 + e of token fr
+  for (int ij = wave; ij < FN * FM; ij += W) {
+    f32x4 g = red[0][2 * ij][lane], u = red[0][2 * ij + 1][lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) {
-      g += red[w][2 * j][lane];
-      u += red[w][2 * j + 1][lane];
+      g += red[w][2 * ij][lane];
+      u += red[w][2 * ij + 1][lane];
     }
-    const int m = m0 + 16 * j + fr;
+    const int m = m0 + 16 * (ij % FM) + fr;
     if (m < p.M) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int nn = n0 + 4 * g4 + e;
+        const int nn = n0 + 16 * (ij / FM) + 4 * g4 + e;
         if (nn < p.N) {
           const int64_t at = int64_t(m) * p.N + nn;
           p.h[at] = uint16_t(pack16<F16>(act_of(p.act, g[e]) * u[e], 0.f));
@@ -394,16 +405,103 @@ __global__ __launch_bounds__(64 * W) void glu_fwd_few_kernel(const GluFwdArgs p)
   }
 }
 
+// The fewest tokens: as above with 8 gate and the same 8 up rows in one fragment,
+// which halves what a wave has to decode one after the other and gives twice the
+// workgroups; every workgroup reads all tokens, so it pays for few of them only.
+template <int FMT, bool F16, int W>
+__global__ __launch_bounds__(64 * W) void glu_fwd_fewest_kernel(const GluFwdArgs p) {
+  __shared__ f32x4 red[W][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int fr = lane & 15, g4 = lane >> 4;
+  const int n0 = blockIdx.x * 8;
+  const int K = p.K, U = K >> 5, nk = (K + 127) >> 7;
+  const uint32_t row = min(n0 + (fr & 7), p.N - 1) - n0;
+  Mat w = from_row<FMT>(p.wg, n0, K);
+  const Mat wu = from_row<FMT>(p.wu, n0, K);
+#pragma unroll
+  for (int i = 0; i < kPlanes<FMT>; ++i) w.p[i] = fr < 8 ? w.p[i] : wu.p[i];
+  const uint32_t xrow = uint32_t(min(fr, p.M - 1)) * uint32_t(2 * K);
+  const uint8_t* xb = reinterpret_cast<const uint8_t*>(p.x);
+  struct Set {
+    UnitRaw<FMT> w;
+    u32x4 x[4];
+  };
+  auto load = [&](Set& s, int step) {
+    const int u = min(4 * step + g4, U - 1);
+    s.w = load_unit<FMT, kByMatrix>(w, row, u, K);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.x[i] = load_at<u32x4>(xb, xrow + 64 * u + 16 * i);
+  };
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const Set& s, int step) {
+    const int u = 4 * step + g4;
+    const bool in = u < U;
+    const u32x4 zero = {0, 0, 0, 0};
+    const Affine f = affine_of<FMT>(s.w.m, min(u, U - 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4 v = unit_piece<FMT, F16>(s.w, f, i);
+      acc = mfma16<F16>(in ? v : zero, in ? s.x[i] : zero, acc);
+    }
+  };
+  Set s0, s1;
+  load(s0, wave);
+  load(s1, wave + W);
+  for (int st = wave; st < nk; st += 2 * W) {
+    use(s0, st);
+    if (st + 2 * W < nk) load(s0, st + 2 * W);
+    if (st + W < nk) use(s1, st + W);
+    if (st + 3 * W < nk) load(s1, st + 3 * W);
+  }
+  red[wave][lane] = acc;
+  lds_barrier16();
+  if (wave) return;
+  f32x4 v = red[0][lane];
+#pragma unroll
+  for (int w = 1; w < W; ++w) v += red[w][lane];
+  // lanes 0 .. 31 hold gate rows n0 + 4 g4 + e of token fr, lanes 32 .. 63 the same up rows
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float u = __shfl_xor(v[e], 32);
+    const int n = n0 + 4 * g4 + e;
+    if (lane < 32 && fr < p.M && n < p.N) {
+      const int64_t at = int64_t(fr) * p.N + n;
+      p.h[at] = uint16_t(pack16<F16>(act_of(p.act, v[e]) * u, 0.f));
+      if (p.g) {
+        p.g[at] = uint16_t(pack16<F16>(v[e], 0.f));
+        p.u[at] = uint16_t(pack16<F16>(u, 0.f));
+      }
+    }
+  }
+}
+
 template <int FMT, bool F16>
 hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
+  // W4A16, K = 2048, us (N = 5632 / 1024): one token 7.7 / 4.4 with 8 + 8 rows per
+  // workgroup against 8.6 / 5.8 with 16 + 16 and 9.2 / 8.8 with 32 + 32; 16 tokens
+  // 11.2 / 5.6, 10.7 / 6.9 and 9.9 / 9.7; 64 tokens 18.7 with 32 + 32, 24 with
+  // 16 + 16.  More rows per workgroup read the tokens fewer times, fewer rows
+  // keep more workgroups at work.
+  if (p.M <= 16 && int64_t(p.M) * p.N <= 24576) {
+    hipLaunchKernelGGL((glu_fwd_fewest_kernel<FMT, F16, 8>), dim3((p.N + 7) / 8), dim3(512), 0, s, p);
+    return hipGetLastError();
+  }
   if (p.M <= 64) {
-    const dim3 grid((p.N + 15) / 16);
-    if (p.M <= 16)
-      hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 1, 4>), grid, dim3(256), 0, s, p);
+    const bool wide = p.N >= 4096;
+    const dim3 grid(wide ? (p.N + 31) / 32 : (p.N + 15) / 16);
+    if (p.M <= 16 && wide)
+      hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 1, 2, 8>), grid, dim3(512), 0, s, p);
+    else if (p.M <= 16)
+      hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 1, 1, 8>), grid, dim3(512), 0, s, p);
+    else if (p.M <= 32 && wide)
+      hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 2, 2, 8>), grid, dim3(512), 0, s, p);
     else if (p.M <= 32)
-      hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 2, 4>), grid, dim3(256), 0, s, p);
+      hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 2, 1, 8>), grid, dim3(512), 0, s, p);
+    else if (wide)
+      hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 4, 2, 4>), grid, dim3(256), 0, s, p);
     else
-      hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 4, 4>), grid, dim3(256), 0, s, p);
+      hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 4, 1, 4>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
   }
   // Tiles of 64 outputs x 128 tokens go two to a compute unit: up to 512 of them
