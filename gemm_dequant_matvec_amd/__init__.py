@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -397,7 +398,7 @@ ROPE_KINDS = {"linear": 1, "ntk": 2, "parts": 3}
 # The many-token operators below are called once or twice per layer, for single
 # tokens too: their checks are kept to attribute reads (sizes are cached, the
 # stream comes as a raw handle), a few microseconds per call.
-_packed_bytes_cached = functools.lru_cache(maxsize=None)(packed_bytes)
+_packed_bytes_cached = functools.lru_cache(maxsize=4096)(packed_bytes)
 
 
 def _act(act) -> int:
@@ -437,7 +438,7 @@ def _weight(W: torch.Tensor, nbytes: int, device: int, what: str) -> int:
 def _like(t: torch.Tensor | None, like: torch.Tensor, shape: tuple, what: str) -> torch.Tensor:
     """t, or a new tensor in its place: of this shape, contiguous, of like's dtype and device."""
     if t is None:
-        return like.new_empty(shape)
+        return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
     if t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {shape}")
     if t.dtype != like.dtype:
@@ -486,6 +487,9 @@ def gemm_glu_backward_bytes(fmt, N: int, K: int, M: int) -> int:
     return out.value
 
 
+_backward_bytes_cached = functools.lru_cache(maxsize=4096)(gemm_glu_backward_bytes)
+
+
 def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
                       dH: torch.Tensor, N: int, K: int, act="silu", dG: torch.Tensor | None = None,
                       dU: torch.Tensor | None = None, dX: torch.Tensor | None = None,
@@ -505,15 +509,15 @@ def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Te
     nbytes = _packed_bytes_cached(f, N, K)
     wg, wu = _weight(W_gate, nbytes, device, "W_gate"), _weight(W_up, nbytes, device, "W_up")
     dG, dU, dX = _like(dG, G, shape, "dG"), _like(dU, G, shape, "dU"), _like(dX, G, (M, K), "dX")
-    nbytes = gemm_glu_backward_bytes(f, N, K, M)
+    nbytes = _backward_bytes_cached(f, N, K, M)
     ws = None
     if nbytes:
         if workspace is None:
             if stream is None:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=G.device)
+                workspace = G.new_empty(nbytes, dtype=torch.uint8)
             else:  # memory of the stream that the call runs on
                 with torch.cuda.stream(stream):
-                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=G.device)
+                    workspace = G.new_empty(nbytes, dtype=torch.uint8)
         ws = _weight(workspace, nbytes, device, "workspace")
     _check(_lib.qmv_gemm_glu_backward(f, N, K, M, wg, wu, G.data_ptr(), U.data_ptr(), dH.data_ptr(),
                                       _DTYPES[G.dtype], a, dG.data_ptr(), dU.data_ptr(), dX.data_ptr(), ws, nbytes, s))
@@ -536,12 +540,12 @@ def rope_freqs(R: int, base: float = 10000.0, scaling: str | None = None, factor
     return host.to(device)
 
 
-_RopeFields = ctypes.c_int64 * 14  # two qmv_rope_tensor, all of whose fields are 8 bytes
+_RopeFields = {7: struct.Struct("7q"), 14: struct.Struct("14q")}  # qmv_rope_tensor: seven 8-byte fields
 
 
 def _rope_out(x: torch.Tensor, y: torch.Tensor | None, what: str) -> torch.Tensor:
     if y is None:
-        return x.new_empty(x.shape)
+        return torch.empty_like(x)
     if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != x.get_device():
         raise ValueError(f"{what}_out must have {what}'s shape, dtype and device")
     return y
@@ -592,7 +596,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torc
     if k is not None:
         k_out = _rope_out(k, k_out, "k")
         fields += _rope_fields(k, k_out, "k")
-    _check(_lib.qmv_rope(T, D, 2 * freqs.numel(), layout, 1 if k is None else 2, _RopeFields(*fields), _DTYPES[q.dtype],
+    _check(_lib.qmv_rope(T, D, 2 * freqs.numel(), layout, len(fields) // 7, _RopeFields[len(fields)].pack(*fields),
+                         _DTYPES[q.dtype],
                          pos.data_ptr(), freqs.data_ptr(), amplitude, inverse, s))
     return q_out, None if k is None else k_out
 

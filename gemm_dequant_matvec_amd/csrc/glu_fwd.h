@@ -487,9 +487,10 @@ hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
     hipLaunchKernelGGL((glu_fwd_fewest_kernel<FMT, F16, 8>), dim3((p.N + 7) / 8), dim3(512), 0, s, p);
     return hipGetLastError();
   }
-  if (p.M <= 64) {
-    const bool wide = p.N >= 4096;
-    const dim3 grid(wide ? (p.N + 31) / 32 : (p.N + 15) / 16);
+  const int64_t blocks = (p.M + 63) / 64, few = int64_t((p.N + 15) / 16) * blocks;
+  if (p.M <= 64 || few <= 256) {
+    const bool wide = p.M <= 64 && p.N >= 4096;
+    const dim3 grid(unsigned(wide ? (p.N + 31) / 32 : (p.N + 15) / 16), unsigned(blocks));
     if (p.M <= 16 && wide)
       hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 1, 2, 8>), grid, dim3(512), 0, s, p);
     else if (p.M <= 16)
@@ -504,17 +505,22 @@ hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
       hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 4, 1, 4>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
   }
-  // Tiles of 64 outputs x 128 tokens go two to a compute unit: up to 512 of them
-  // are one round of the chip.  Past that the tile of 128 x 256 is faster, which
-  // decodes a weight once for twice the tokens.  W4A16, K = 2048, N = 5632: 352
-  // small tiles (M = 512) 42 us against 48, 528 (M = 768) 65 against 51.
+  // A stage of 32 of K takes about 0.34 us with tiles of 64 outputs x 64 tokens
+  // alone on their units, 0.40 with 64 x 128, 0.75 with two of these to a unit and
+  // with one of 128 x 256, which decodes a weight once for twice the tokens.  So the
+  // smallest tile whose count still is one round of the chip is taken.  Q4K, N = 1024,
+  // K = 1024, 128 tokens: 8.4 us few-token kernel, 13.1 / 15.9 tiles of 64 x 64 / 64 x 128;
+  // W4A16, N = 5632, K = 2048: 512 tokens 42 with 64 x 128 against 48 with 128 x 256, 768
+  // tokens 65 against 51.
+  const int64_t tiny = int64_t((p.N + 63) / 64) * ((p.M + 63) / 64);
   const int64_t small = int64_t((p.N + 63) / 64) * ((p.M + 127) / 128);
-  if (small <= 512) {
+  if (tiny <= 256)
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 2>), dim3(unsigned(tiny)), dim3(256), 0, s, p);
+  else if (small <= 512)
     hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 2, 2, 2>), dim3(unsigned(small)), dim3(256), 0, s, p);
-  } else {
+  else
     hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 4, 2, 2, 4>),
                        dim3(unsigned(int64_t((p.N + 127) / 128) * ((p.M + 255) / 256))), dim3(512), 0, s, p);
-  }
   return hipGetLastError();
 }
 
