@@ -342,18 +342,30 @@ struct HalfRaw {
   MetaRaw<FMT> m;
 };
 
-// A tile of 64-byte rows of codes: the half h of unit s of row r (0 <= s < kChunk).
-template <int FMT>
-__device__ __forceinline__ void read_codes(u32x4 (&q)[2], const u32x4* R, int r, int s, int h) {
+// A tile of 64-byte rows of codes: WPT words (2: half w / 2; 1: word w) of unit s
+// of row r, 0 <= s < kChunk.
+template <int FMT, int WPT>
+__device__ __forceinline__ void read_codes(u32x4 (&q)[2], const u32x4* R, int r, int s, int w) {
   if constexpr (FMT == QMV_DENSE_BF16) {
-    q[0] = R[tile32_at(r, 2 * h)];
-    q[1] = R[tile32_at(r, 2 * h + 1)];
+    q[0] = R[tile32_at(r, w)];
+    if constexpr (WPT == 2) q[1] = R[tile32_at(r, w + 1)];
   } else if constexpr (is_byte(FMT)) {
-    q[0] = R[tile32_at(r, 2 * s + h)];
+    if constexpr (WPT == 2) {
+      q[0] = R[tile32_at(r, 2 * s + (w >> 1))];
+    } else {
+      const u32x2 v = reinterpret_cast<const u32x2*>(R + tile32_at(r, 2 * s + (w >> 1)))[w & 1];
+      q[0][0] = v[0];
+      q[0][1] = v[1];
+    }
   } else {
-    const u32x2 v = reinterpret_cast<const u32x2*>(R + tile32_at(r, s))[h];
-    q[0][0] = v[0];
-    q[0][1] = v[1];
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(R + tile32_at(r, s)) + w;
+    if constexpr (WPT == 2) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+      q[0][0] = v[0];
+      q[0][1] = v[1];
+    } else {
+      q[0][0] = *p;
+    }
   }
 }
 
@@ -378,9 +390,9 @@ __device__ __forceinline__ HalfRaw<FMT> load_half(const Mat& w, uint32_t r, int 
   return x;
 }
 
-// Word i (0, 1) of half h of unit u as one 16-byte piece.
+// Word w of unit u as one 16-byte piece; its codes are the i-th of r.
 template <int FMT, bool F16>
-__device__ __forceinline__ u32x4 half_piece(const HalfRaw<FMT>& r, int u, int h, int i) {
+__device__ __forceinline__ u32x4 word_piece(const HalfRaw<FMT>& r, int u, int w, int i) {
   if constexpr (FMT == QMV_DENSE_BF16) {
     if constexpr (!F16) return r.q[i];
     u32x4 o;
@@ -400,10 +412,10 @@ __device__ __forceinline__ u32x4 half_piece(const HalfRaw<FMT>& r, int u, int h,
     }
     c.qh = r.qh;
     const Affine f = affine_of<FMT>(r.m, u);
-    float w[8];
-    // Q6K: h selects the sub-block; word 2 h + i's high bits are those of word i
-    decode8<FMT>(c, FMT == QMV_Q6K && h ? f.a1 : f.a0, FMT == QMV_Q6K && h ? f.b1 : f.b0, FMT == QMV_Q6K ? i : 2 * h + i, w);
-    return u32x4{pack16<F16>(w[0], w[1]), pack16<F16>(w[2], w[3]), pack16<F16>(w[4], w[5]), pack16<F16>(w[6], w[7])};
+    float v[8];
+    const bool second = FMT == QMV_Q6K && w >= 2;  // the second sub-block
+    decode8<FMT>(c, second ? f.a1 : f.a0, second ? f.b1 : f.b0, w, v);
+    return u32x4{pack16<F16>(v[0], v[1]), pack16<F16>(v[2], v[3]), pack16<F16>(v[4], v[5]), pack16<F16>(v[6], v[7])};
   }
 }
 

@@ -97,7 +97,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
     return load_half<FMT, kByUnit>(w, min(nl, N - 1 - nb), u, half, K);
   };
   auto decode = [&](const HalfRaw<FMT>& c, int i, u32x4* A) {
-    A[rows_at<BR>(nl, ul, half, i)] = half_piece<FMT, F16>(c, u, half, i);
+    A[rows_at<BR>(nl, ul, half, i)] = word_piece<FMT, F16>(c, u, 2 * half + i, i);
   };
   // dense rows: LDS slot tid + t * NT is row (tid + t * NT) / (BR / 8)
   auto copy_a = [&](int st, u32x4* A) {
@@ -244,6 +244,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
     return;
   }
   // through the wave's own part of LDS, 32 tokens x 64 columns at a time: rows leave whole
+  static_assert(WR * WT * 32 * 8 <= 2 * BR * 4);
   u32x4* mine = (wave & 1 ? A1 : A0) + (wave >> 1) * (32 * 8);
 #pragma unroll
   for (int j = 0; j < TB; ++j)

@@ -19,15 +19,15 @@ namespace {
 // How many vector memory operations a wave has certainly issued by the end of
 // stage `now` after the copy of the tokens (or of the codes) in stage `from`.  A
 // stage issues the XPT copies of its tokens, then, where it starts to decode a
-// tile of codes, the two copies of the tile after the next, then, once per run,
+// tile of codes, the CPT copies of the tile after the next, then, once per run,
 // the loads of the next run's scales.
-template <int FMT, int XPT>
+template <int FMT, int XPT, int CPT>
 constexpr int issued_after(int from, bool codes, int now) {
   int n = 0;
   for (int s = from; s <= now; ++s) {
     const int h = (s + 4 * kRun) % kRun;
     if (s > from) n += XPT;
-    if ((s > from || !codes) && (h + 2) % kChunk<FMT> == 0) n += 2;
+    if ((s > from || !codes) && (h + 2) % kChunk<FMT> == 0) n += CPT;
     if (h == 0) n += kMetaLoads<FMT>;
   }
   return n;
@@ -51,7 +51,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   constexpr int BR = 32 * RB * WR, BN = BR / 2, BM = 32 * TB * WT;
   constexpr int XPT = BM * 4 / NT;      // 16-byte token pieces per thread and stage
   constexpr int SR = kRun, SC = kChunk<FMT>;  // stages per run and per tile of codes
-  static_assert(2 * BR == NT && XPT * NT == BM * 4 && RB % 2 == 0);
+  constexpr int CPT = BR * 4 / NT;      // ... of codes, per thread and tile
+  constexpr int WPT = CPT;              // words of 8 weights that a thread decodes per stage
+  static_assert((WPT == 1 || WPT == 2) && CPT * NT == BR * 4 && XPT * NT == BM * 4 && RB % 2 == 0);
   constexpr int XD = 3;                 // stages that the tokens' copies run ahead
 
   // variables of their own: the compiler then knows that a copy into one does
@@ -73,19 +75,21 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   const int n0 = id0.x * BN, m0 = id0.y * BM;
   const int K = p.K, U = K >> 5;
 
-  // Threads 2 i and 2 i + 1 decode the halves of weight row i: gate or up goes
-  // by wave, so that the addresses are scalar bases and one lane offset per
-  // plane.
-  const int half = tid & 1, ri = tid >> 1;
+  // 4 / WPT neighbouring threads decode a unit of a weight row, each the words
+  // word .. word + WPT - 1: gate or up goes by wave, so that the addresses are
+  // scalar bases and one lane offset per plane.
+  const int word = tid % (4 / WPT) * WPT, half = word >> 1, ri = tid / (4 / WPT);
   const bool up = wave >= WR * WT / 2;
   const uint32_t wrow = min(n0 + ri % BN, p.N - 1) - n0;
   const Mat wg = from_row<FMT>(p.wg, n0, K), wu = from_row<FMT>(p.wu, n0, K), w = up ? wu : wg;
-  // Codes: thread tid copies piece tid % 4 (by the tile's order) of gate and of up row tid / 4.
-  const uint32_t co = uint32_t(min(n0 + (tid >> 2), p.N - 1) - n0) * row_bytes<FMT>(0, K) + 16 * ((tid & 3) ^ ((tid >> 4) & 3));
+  // Codes: thread tid copies piece tid % 4 (by the tile's order) of gate and of up
+  // row tid / 4, or of one of them where the threads cover both.
+  const uint32_t co = uint32_t(min(n0 + (tid >> 2) % BN, p.N - 1) - n0) * row_bytes<FMT>(0, K) + 16 * ((tid & 3) ^ ((tid >> 4) & 3));
   const int arow = ((ri % BN) / (16 * RB)) * 32 * RB + (ri % BN) % (16 * RB) + (up ? 16 * RB : 0);
   // Token pieces: LDS slot tid + t * NT of a tile is row (tid + t * NT) / 4.
   const uint8_t* xb = reinterpret_cast<const uint8_t*>(p.x + int64_t(m0) * K);
   const Buf xbuf = buffer_of(xb), gbuf = buffer_of(wg.p[0]), ubuf = buffer_of(wu.p[0]);
+  const Buf cbuf = buffer_of(scalar_base(w.p[0]));
   uint32_t xo[XPT];
 #pragma unroll
   for (int t = 0; t < XPT; ++t)
@@ -126,8 +130,12 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   };
 
   auto copy_codes = [&](int u, u32x4* R) {  // units u .. u + SC - 1
-    copy_to_lds(gbuf, co, u * (64 / SC), R + wave * 64);
-    copy_to_lds(ubuf, co, u * (64 / SC), R + BN * 4 + wave * 64);
+    if constexpr (CPT == 2) {
+      copy_to_lds(gbuf, co, u * (64 / SC), R + wave * 64);
+      copy_to_lds(ubuf, co, u * (64 / SC), R + BN * 4 + wave * 64);
+    } else {
+      copy_to_lds(cbuf, co, u * (64 / SC), R + wave * 64);
+    }
   };
 
   // ---- whole runs
@@ -143,7 +151,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
       r.q[0] = codes[0];
       r.q[1] = codes[1];
       meta_of<FMT>(r, x, s);
-      A[tile32_at(arow, 2 * half + i)] = half_piece<FMT, F16>(r, u + s, half, i);
+      A[tile32_at(arow, word + i)] = word_piece<FMT, F16>(r, u + s, word + i, i);
     };
     // Tile of codes of stage s (of this run or, past SR, the next).
     auto Rt = [&]<int S>() { return (S / SC) & 1 ? R1 : R0; };
@@ -158,9 +166,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
     [&]<int... S>(std::integer_sequence<int, S...>) {
       (([&] {
          u32x4 c[2];
-         read_codes<FMT>(c, Rt.template operator()<S>(), ri, S % SC, half);
+         read_codes<FMT, WPT>(c, Rt.template operator()<S>(), ri, S % SC, word);
 #pragma unroll
-         for (int i = 0; i < 2; ++i) decode(c, cur, ua, S, S ? A1 : A0, i);
+         for (int i = 0; i < WPT; ++i) decode(c, cur, ua, S, S ? A1 : A0, i);
        }()),
        ...);
     }(std::make_integer_sequence<int, 2>{});
@@ -173,7 +181,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
     Frag f0, f1;
     u32x4 c[2][2];
     read(f0, A0, X0, 0);
-    if constexpr (SC == 4) read_codes<FMT>(c[0], R0, ri, 2, half);
+    if constexpr (SC == 4) read_codes<FMT, WPT>(c[0], R0, ri, 2, word);
 #pragma unroll 1
     for (int run = 0; run < runs; ++run) {
       const int then = ua + SR < runs * SR ? ua + SR : 0;
@@ -195,7 +203,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
            if constexpr (H == 0) next = load_run_meta<FMT>(w, wrow, then, half, K);
            // Where a tile of codes lasts four stages, a stage's codes are read in the
            // stage before.
-           if constexpr (SC < 4) read_codes<FMT>(c[H & 1], Rt.template operator()<D>(), ri, D % SC, half);
+           if constexpr (SC < 4) read_codes<FMT, WPT>(c[H & 1], Rt.template operator()<D>(), ri, D % SC, word);
            read(f1, A, X, 1);
            auto dec = [&](int i) {
              if constexpr (D >= SR) decode(c[H & 1], next, then, D - SR, A2n, i);
@@ -205,16 +213,16 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
            mul(f0);
            fence();
            read(f0, A1n, X1n, 0);
-           if constexpr (SC == 4) read_codes<FMT>(c[(H + 1) & 1], Rt.template operator()<D + 1>(), ri, (D + 1) % SC, half);
-           dec(1);
+           if constexpr (SC == 4) read_codes<FMT, WPT>(c[(H + 1) & 1], Rt.template operator()<D + 1>(), ri, (D + 1) % SC, word);
+           if constexpr (WPT == 2) dec(1);
            mul(f1);
            fence();
            // The next stage reads the tokens of stage H + 2, and the codes of the stage
            // `code`, if they start a tile.  Everything issued after their copies may
            // still be under way.
            constexpr int code = SC == 4 ? H + 4 : H + 3;
-           constexpr int left_x = issued_after<FMT, XPT>(H + 2 - XD, false, H);
-           constexpr int left_c = code % SC ? 63 : issued_after<FMT, XPT>(code - SC - 2, true, H);
+           constexpr int left_x = issued_after<FMT, XPT, CPT>(H + 2 - XD, false, H);
+           constexpr int left_c = code % SC ? 63 : issued_after<FMT, XPT, CPT>(code - SC - 2, true, H);
            constexpr int left = left_x < left_c ? left_x : left_c;
            static_assert(left >= 0 && left <= 63);
            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(left) : "memory");
@@ -235,7 +243,8 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
     for (int t = 0; t < XPT; ++t) X0[tid + t * NT] = load_at<u32x4>(xb, xo[t] + 64 * u);
     const HalfRaw<FMT> r = load_half<FMT, kByRow>(w, wrow, u, half, K);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) A0[tile32_at(arow, 2 * half + i)] = half_piece<FMT, F16>(r, u, half, i);
+    for (int i = 0; i < 2; ++i)
+      if (WPT == 2 || i == (word & 1)) A0[tile32_at(arow, 2 * half + i)] = word_piece<FMT, F16>(r, u, 2 * half + i, i);
     lds_barrier16();
     Frag f;
 #pragma unroll
@@ -251,7 +260,10 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   // are done with), so that rows of up to 128 bytes leave whole.
   lds_barrier16();
   constexpr int HB = RB / 2;                       // 32-row blocks of outputs
-  u32x4* mine = (wave & 1 ? A1 : A0) + (wave >> 1) * (32 * 8);  // 32 tokens x 64 values
+  constexpr int WPA = BR * 4 / (32 * 8);           // waves per weight tile, 32 tokens x 64 values each
+  static_assert(NT / 64 <= 4 * WPA);
+  const int wa = wave / WPA;
+  u32x4* mine = (wa == 0 ? A0 : wa == 1 ? A1 : wa == 2 ? A2 : A3) + wave % WPA * (32 * 8);
   const int nw = n0 + wr * HB * 32;
   auto put = [&](uint16_t* y, int j, auto value) {
 #pragma unroll
@@ -505,22 +517,24 @@ hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
       hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 4, 1, 4>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
   }
-  // A stage of 32 of K takes about 0.34 us with tiles of 64 outputs x 64 tokens
-  // alone on their units, 0.40 with 64 x 128, 0.75 with two of these to a unit and
-  // with one of 128 x 256, which decodes a weight once for twice the tokens.  So the
-  // smallest tile whose count still is one round of the chip is taken.  Q4K, N = 1024,
-  // K = 1024, 128 tokens: 8.4 us few-token kernel, 13.1 / 15.9 tiles of 64 x 64 / 64 x 128;
-  // W4A16, N = 5632, K = 2048: 512 tokens 42 with 64 x 128 against 48 with 128 x 256, 768
-  // tokens 65 against 51.
-  const int64_t tiny = int64_t((p.N + 63) / 64) * ((p.M + 63) / 64);
-  const int64_t small = int64_t((p.N + 63) / 64) * ((p.M + 127) / 128);
-  if (tiny <= 256)
-    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 2>), dim3(unsigned(tiny)), dim3(256), 0, s, p);
-  else if (small <= 512)
-    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 2, 2, 2>), dim3(unsigned(small)), dim3(256), 0, s, p);
+  // A launch takes rounds of the chip: the smallest tile is taken whose count is
+  // one round (256 units, two 64 x 128 tiles to a unit), else the largest, which
+  // decodes a weight once for the most tokens.  Us on W4A16, K = 2048, for tiles of
+  // outputs x tokens:        64 x 64   64 x 128   64 x 256   128 x 256
+  //   N 5632,  128 tokens       22        26         33         46
+  //            256 tokens       32        27         34         46
+  //            512 tokens       50        40         36         49
+  //           1024 tokens       90        65         69         54
+  // and Q4K, N 1024, K 1024, 128 tokens: 8.4 few-token kernel, 13.1 and 15.9 the first two.
+  auto tiles = [&](int bn, int bm) { return int64_t((p.N + bn - 1) / bn) * ((p.M + bm - 1) / bm); };
+  if (tiles(64, 64) <= 256)
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 2>), dim3(unsigned(tiles(64, 64))), dim3(256), 0, s, p);
+  else if (tiles(64, 128) <= 256 || (tiles(64, 256) > 256 && tiles(64, 128) <= 512))
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 4>), dim3(unsigned(tiles(64, 128))), dim3(512), 0, s, p);
+  else if (tiles(64, 256) <= 256)
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 2, 2, 4>), dim3(unsigned(tiles(64, 256))), dim3(512), 0, s, p);
   else
-    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 4, 2, 2, 4>),
-                       dim3(unsigned(int64_t((p.N + 127) / 128) * ((p.M + 255) / 256))), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 4, 2, 2, 4>), dim3(unsigned(tiles(128, 256))), dim3(512), 0, s, p);
   return hipGetLastError();
 }
 

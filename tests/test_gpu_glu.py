@@ -107,6 +107,10 @@ def test_forward(qmv, fmt, dtype, M, N, mult):
 @pytest.mark.parametrize("fmt,dtype,act,M,N,K", [
     ("w4a16_g64", "bf16", "silu", 1, 5632, 2048), ("q4k", "f16", "gelu", 16, 5632, 2048),
     ("q6k", "bf16", "silu", 512, 1408, 2048), ("bf16", "bf16", "silu", 1030, 700, 1056),
+    # one round of 64 x 128 and of 64 x 256 tiles, and two to a unit, ragged in every direction
+    ("w4a16_g64", "bf16", "silu", 250, 5000, 320), ("q5_0", "f16", "gelu", 250, 5000, 352),
+    ("bf16", "f16", "silu", 500, 5000, 288), ("q6k", "bf16", "gelu_tanh", 500, 5000, 256),
+    ("q8_0", "bf16", "silu", 600, 5600, 544), ("q4k", "f16", "silu", 600, 5600, 512),
     # enough 256-token tiles for the large kernel, ragged in every direction
     ("w4a16_g64", "bf16", "silu", 4100, 2050, 192), ("q8_0", "f16", "gelu_tanh", 4100, 2050, 96),
     ("q5k", "bf16", "gelu", 4100, 2050, 256), ("bf16", "f16", "silu", 4100, 2050, 64)])
