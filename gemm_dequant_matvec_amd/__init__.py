@@ -409,19 +409,15 @@ def _act(act) -> int:
     return int(act)
 
 
-def _on_current_device(t: torch.Tensor, stream) -> int:
-    """The raw stream for a call whose tensors are on t's device, which has to be
-    the current one: kernels are launched there."""
+def _on_current_device(t: torch.Tensor) -> int:
+    """The raw current stream, for a call whose tensors are on t's device, which
+    has to be the current one: kernels are launched there."""
     if not t.is_cuda:
         raise ValueError("tensors passed to libqmv must live on the GPU")
     device = t.get_device()
     if device != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on device {device}, the current device is {torch._C._cuda_getDevice()}")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    if stream.device.index != device:
-        raise ValueError(f"the stream is on device {stream.device.index}, the tensors on {device}")
-    return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _weight(W: torch.Tensor, nbytes: int, device: int, what: str) -> int:
@@ -458,6 +454,9 @@ def gemm_glu(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, X: torch.Tensor, N: 
     act: "silu", "gelu_tanh" or "gelu".  With save=True (or G and U given) the
     two products are kept for gemm_glu_backward and (H, G, U) is returned.
     """
+    if stream is not None:  # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return gemm_glu(fmt, W_gate, W_up, X, N, K, act, H, G, U, save)
     if X.dim() != 2 or X.shape[1] != K:
         raise ValueError(f"X has shape {tuple(X.shape)}, expected [M][{K}]")
     if X.dtype not in _DTYPES:
@@ -465,7 +464,7 @@ def gemm_glu(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, X: torch.Tensor, N: 
     if (G is None) != (U is None):
         raise ValueError("G and U go together")
     shape, dt, f, a = (X.shape[0], N), _DTYPES[X.dtype], _fmt(fmt), _act(act)
-    s, device = _on_current_device(X, stream), X.get_device()
+    s, device = _on_current_device(X), X.get_device()
     nbytes = _packed_bytes_cached(f, N, K)
     wg, wu = _weight(W_gate, nbytes, device, "W_gate"), _weight(W_up, nbytes, device, "W_up")
     if not X.is_contiguous():
@@ -498,6 +497,9 @@ def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Te
     from its saved G and U; all of one dtype.  dG and dU may be given as two of
     the buffers G, U and dH.  workspace: scratch memory of
     gemm_glu_backward_bytes bytes, allocated when absent."""
+    if stream is not None:  # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return gemm_glu_backward(fmt, W_gate, W_up, G, U, dH, N, K, act, dG, dU, dX, workspace)
     if G.dtype not in _DTYPES:
         raise ValueError("G dtype must be float32, float16 or bfloat16")
     shape, f, a = (G.shape[0], N), _fmt(fmt), _act(act)
@@ -505,7 +507,7 @@ def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Te
     _like(G, G, shape, "G")
     _like(U, G, shape, "U")
     _like(dH, G, shape, "dH")
-    s, device = _on_current_device(G, stream), G.get_device()
+    s, device = _on_current_device(G), G.get_device()
     nbytes = _packed_bytes_cached(f, N, K)
     wg, wu = _weight(W_gate, nbytes, device, "W_gate"), _weight(W_up, nbytes, device, "W_up")
     dG, dU, dX = _like(dG, G, shape, "dG"), _like(dU, G, shape, "dU"), _like(dX, G, (M, K), "dX")
@@ -513,11 +515,7 @@ def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Te
     ws = None
     if nbytes:
         if workspace is None:
-            if stream is None:
-                workspace = G.new_empty(nbytes, dtype=torch.uint8)
-            else:  # memory of the stream that the call runs on
-                with torch.cuda.stream(stream):
-                    workspace = G.new_empty(nbytes, dtype=torch.uint8)
+            workspace = G.new_empty(nbytes, dtype=torch.uint8)
         ws = _weight(workspace, nbytes, device, "workspace")
     _check(_lib.qmv_gemm_glu_backward(f, N, K, M, wg, wu, G.data_ptr(), U.data_ptr(), dH.data_ptr(),
                                       _DTYPES[G.dtype], a, dG.data_ptr(), dU.data_ptr(), dX.data_ptr(), ws, nbytes, s))
@@ -548,6 +546,8 @@ def _rope_out(x: torch.Tensor, y: torch.Tensor | None, what: str) -> torch.Tenso
         return torch.empty_like(x)
     if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != x.get_device():
         raise ValueError(f"{what}_out must have {what}'s shape, dtype and device")
+    if any(n > 1 and st == 0 for n, st in zip(y.shape, y.stride())):
+        raise ValueError(f"{what}_out holds some values more than once")
     return y
 
 
@@ -571,6 +571,9 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torc
     strided (slices of one fused product) as long as a head's values are
     adjacent; q_out=q, k_out=k works in place.
     """
+    if stream is not None:  # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return rope(q, k, pos, freqs, layout, amplitude, inverse, q_out, k_out)
     if layout in ROPE_LAYOUTS:
         layout = ROPE_LAYOUTS[layout]
     elif isinstance(layout, str):
@@ -586,7 +589,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torc
         raise ValueError(f"pos holds {pos.numel()} positions, q {T} tokens")
     if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype != q.dtype):
         raise ValueError(f"k has shape {tuple(k.shape)} and {k.dtype}, expected [{T}][heads][{D}] and {q.dtype}")
-    s, device = _on_current_device(q, stream), q.get_device()
+    s, device = _on_current_device(q), q.get_device()
     if pos.get_device() != device or freqs.get_device() != device or (k is not None and k.get_device() != device):
         raise ValueError("q, k, pos and freqs must be on one device")
     if not (pos.is_contiguous() and freqs.is_contiguous()):

@@ -321,6 +321,15 @@ int qmv_quantize_x(int64_t K, int64_t batch, const float* x, void* xq, void* str
                   "quantize_x");
 }
 
+// 256 rows of N or K 16-bit values (and 256 packed rows) are reached by 31-bit byte offsets from
+// their first; rows are counted in 31 bits with room for a tile, a launch's threads in 32.
+static int check_glu_sizes(int64_t N, int64_t K, int64_t M) {
+  if (N > (int64_t(1) << 21) || K > (int64_t(1) << 21)) return fail(QMV_ERR_OVERFLOW, "N or K is past 2^21");
+  if (M > (int64_t(1) << 30) || M * N > (int64_t(1) << 34) || M * K > (int64_t(1) << 34))
+    return fail(QMV_ERR_OVERFLOW, "M is past 2^30, or M * N or M * K past 2^34");
+  return QMV_OK;
+}
+
 // Arguments that qmv_gemm_glu and its backward pass share.
 static int check_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up, int dtype,
                      const char* dtype_name, int act) {
@@ -336,12 +345,7 @@ static int check_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gat
   if (act < QMV_ACT_SILU || act > QMV_ACT_GELU) return fail(QMV_ERR_UNSUPPORTED, "act=%d is not a qmv_act", act);
   if (!aligned(W_gate, 16)) return fail(QMV_ERR_ALIGN, "W_gate is not 16-byte aligned");
   if (!aligned(W_up, 16)) return fail(QMV_ERR_ALIGN, "W_up is not 16-byte aligned");
-  // 256 rows of N or K 16-bit values (and 256 packed rows) are reached by 31-bit byte offsets from
-  // their first; tiles, and eighths of M * N, are counted in 32 bits
-  if (N > (int64_t(1) << 21) || K > (int64_t(1) << 21)) return fail(QMV_ERR_OVERFLOW, "N or K is past 2^21");
-  if (M >= (int64_t(1) << 31) || M * N >= (int64_t(1) << 38) || M * K >= (int64_t(1) << 38))
-    return fail(QMV_ERR_OVERFLOW, "M * N or M * K is past 2^38");
-  return QMV_OK;
+  return check_glu_sizes(N, K, M);
 }
 
 static int check_buffer(const void* p, const char* name) {
@@ -361,6 +365,8 @@ int qmv_gemm_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, c
   if ((st = check_buffer(H, "H"))) return st;
   if ((G != nullptr) != (U != nullptr)) return fail(QMV_ERR_NULL, "%s is NULL and %s is not", G ? "U" : "G", G ? "G" : "U");
   if (G && ((st = check_buffer(G, "G")) || (st = check_buffer(U, "U")))) return st;
+  if (H == X || G == X || U == X) return fail(QMV_ERR_UNSUPPORTED, "an output is the buffer of X");
+  if (G && (G == H || U == H || G == U)) return fail(QMV_ERR_UNSUPPORTED, "two of H, G and U are one buffer");
   if ((st = check_device())) return st;
   return launched(qmv::launch_glu_fwd(fmt, N, K, M, static_cast<const uint8_t*>(W_gate),
                                       static_cast<const uint8_t*>(W_up), static_cast<const uint16_t*>(X),
@@ -379,9 +385,7 @@ int qmv_gemm_glu_backward_bytes(int fmt, int64_t N, int64_t K, int64_t M, size_t
   if ((st = check_fmt(fmt))) return st;
   if ((st = check_shape(fmt, N, K, M, "M"))) return st;
   if (!out_bytes) return fail(QMV_ERR_NULL, "out_bytes is NULL");
-  if (N > (int64_t(1) << 21) || K > (int64_t(1) << 21)) return fail(QMV_ERR_OVERFLOW, "N or K is past 2^21");
-  if (M >= (int64_t(1) << 31) || M * N >= (int64_t(1) << 38) || M * K >= (int64_t(1) << 38))
-    return fail(QMV_ERR_OVERFLOW, "M * N or M * K is past 2^38");
+  if ((st = check_glu_sizes(N, K, M))) return st;
   *out_bytes = glu_backward_bytes(N, K, M);
   return ok();
 }
@@ -448,7 +452,8 @@ int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_r
     heads += t.heads;
   }
   // a block of tokens is indexed with 32-bit ints, the grid counts tokens
-  if (D >= lim || heads > (lim - 1) / D || T >= lim) return fail(QMV_ERR_OVERFLOW, "T or heads * D too large");
+  if (D > (lim >> 3) || heads > (lim >> 3) / D || T >= lim)
+    return fail(QMV_ERR_OVERFLOW, "T is past 2^31 or heads * D past 2^28");
   if ((st = check_device())) return st;
   return launched(qmv::launch_rope(T, int(D), int(R), layout, count, tensors, dtype, pos, freqs, amplitude, inverse,
                                    as_stream(stream)),

@@ -186,12 +186,26 @@ struct MetaRaw {
   u32x4 v;  // super-block record, or v[0], v[1]
 };
 
-// The scales of unit u of row r.
+// Byte offsets of a row in each plane.
+template <int FMT>
+struct RowAt {
+  uint32_t o[kPlanes<FMT>];
+};
+
+template <int FMT>
+__device__ __forceinline__ RowAt<FMT> row_at(uint32_t r, int K) {
+  RowAt<FMT> x;
+#pragma unroll
+  for (int i = 0; i < kPlanes<FMT>; ++i) x.o[i] = r * row_bytes<FMT>(i, K);
+  return x;
+}
+
+// The scales of unit u of a row.
 template <int FMT, By BY>
-__device__ __forceinline__ MetaRaw<FMT> load_meta(const Mat& w, uint32_t r, int u, int K) {
+__device__ __forceinline__ MetaRaw<FMT> load_meta(const Mat& w, const RowAt<FMT>& r, int u) {
   MetaRaw<FMT> m;
   constexpr int P = kPlanes<FMT> - 1;  // the plane of the scales (Q6K: of d)
-  const uint32_t at = r * row_bytes<FMT>(P, K);
+  const uint32_t at = r.o[P];
   if constexpr (FMT == QMV_Q8_0 || FMT == QMV_Q4_0 || FMT == QMV_Q5_0) {
     m.v[0] = load_at<uint16_t, BY>(w.p[P], at, 2 * u);
   } else if constexpr (FMT == QMV_W4A16_G64) {
@@ -199,7 +213,7 @@ __device__ __forceinline__ MetaRaw<FMT> load_meta(const Mat& w, uint32_t r, int 
   } else if constexpr (is_super(FMT)) {
     m.v = load_at<u32x4, BY>(w.p[P], at, 16 * (u >> 3));
   } else if constexpr (FMT == QMV_Q6K) {
-    m.v[0] = load_at<uint16_t, BY>(w.p[2], r * row_bytes<FMT>(2, K), 2 * u);
+    m.v[0] = load_at<uint16_t, BY>(w.p[2], r.o[2], 2 * u);
     m.v[1] = load_at<uint16_t, BY>(w.p[3], at, 2 * (u >> 3));
   } else if constexpr (FMT == QMV_I8_ROW) {
     m.v[0] = load_at<uint32_t, BY>(w.p[1], at);
@@ -284,15 +298,15 @@ struct UnitRaw {
 
 // Unit u of row r.
 template <int FMT, By BY>
-__device__ __forceinline__ UnitRaw<FMT> load_unit(const Mat& w, uint32_t r, int u, int K) {
+__device__ __forceinline__ UnitRaw<FMT> load_unit(const Mat& w, uint32_t row, int u, int K) {
   UnitRaw<FMT> x;
   constexpr int NQ = UnitRaw<FMT>::NQ;
-  const uint32_t at = r * row_bytes<FMT>(0, K);
+  const RowAt<FMT> r = row_at<FMT>(row, K);
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) x.q[i] = load_at<u32x4, BY>(w.p[0], at, int64_t(u) * (16 * NQ) + 16 * i);
-  if constexpr (is_fifth(FMT)) x.qh[0] = load_at<uint32_t, BY>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
-  if constexpr (FMT == QMV_Q6K) x.qh = load_at<u32x2, BY>(w.p[1], r * row_bytes<FMT>(1, K), 8 * u);
-  x.m = load_meta<FMT, BY>(w, r, u, K);
+  for (int i = 0; i < NQ; ++i) x.q[i] = load_at<u32x4, BY>(w.p[0], r.o[0], int64_t(u) * (16 * NQ) + 16 * i);
+  if constexpr (is_fifth(FMT)) x.qh[0] = load_at<uint32_t, BY>(w.p[1], r.o[1], 4 * u);
+  if constexpr (FMT == QMV_Q6K) x.qh = load_at<u32x2, BY>(w.p[1], r.o[1], 8 * u);
+  x.m = load_meta<FMT, BY>(w, r, u);
   return x;
 }
 
@@ -369,12 +383,12 @@ __device__ __forceinline__ void read_codes(u32x4 (&q)[2], const u32x4* R, int r,
   }
 }
 
-// Half h (a lane's) of unit u (a lane's too if BY is kByUnit), from global memory.
+// Half h (a lane's) of unit u (a lane's too if BY is kByUnit) of a row, from global memory.
 template <int FMT, By BY>
-__device__ __forceinline__ HalfRaw<FMT> load_half(const Mat& w, uint32_t r, int u, int h, int K) {
+__device__ __forceinline__ HalfRaw<FMT> load_half(const Mat& w, const RowAt<FMT>& r, int u, int h) {
   HalfRaw<FMT> x;
   constexpr int B = 32 / kChunk<FMT>;  // bytes of half a unit's codes
-  const uint32_t at = r * row_bytes<FMT>(0, K) + B * h;
+  const uint32_t at = r.o[0] + B * h;
   const int64_t ub = int64_t(u) * (2 * B);
   if constexpr (B == 8) {
     const u32x2 v = load_at<u32x2, BY>(w.p[0], at, ub);
@@ -384,9 +398,9 @@ __device__ __forceinline__ HalfRaw<FMT> load_half(const Mat& w, uint32_t r, int 
     x.q[0] = load_at<u32x4, BY>(w.p[0], at, ub);
     if constexpr (B == 32) x.q[1] = load_at<u32x4, BY>(w.p[0], at, ub + 16);
   }
-  if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t, BY>(w.p[1], r * row_bytes<FMT>(1, K), 4 * u);
-  if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t, BY>(w.p[1], r * row_bytes<FMT>(1, K) + 4 * h, 8 * u);
-  x.m = load_meta<FMT, BY>(w, r, u, K);
+  if constexpr (is_fifth(FMT)) x.qh = load_at<uint32_t, BY>(w.p[1], r.o[1], 4 * u);
+  if constexpr (FMT == QMV_Q6K) x.qh = load_at<uint32_t, BY>(w.p[1], r.o[1] + 4 * h, 8 * u);
+  x.m = load_meta<FMT, BY>(w, r, u);
   return x;
 }
 

@@ -68,23 +68,24 @@ __global__ __launch_bounds__(kThreads) void glu_dgates_kernel(const uint16_t* g,
 template <bool F16, int ACT>
 __global__ __launch_bounds__(kThreads) void glu_dgates_ragged_kernel(const uint16_t* g, const uint16_t* u,
                                                                      const uint16_t* dh, uint16_t* dg, uint16_t* du,
-                                                                     uint16_t* cg, uint16_t* cu, int N, int ld) {
-  const int64_t m = blockIdx.x;
+                                                                     uint16_t* cg, uint16_t* cu, int64_t M, int N, int ld) {
   const int n = (blockIdx.y * kThreads + threadIdx.x) * 8, left = min(8, N - n);
   if (n >= ld) return;
-  const int64_t at = m * N + n;
   const bool whole = left == 8;
-  u32x4 og, ou;
-  dgates8<F16, ACT>(whole ? load8(g + at) : load_part(g + at, left), whole ? load8(u + at) : load_part(u + at, left),
-                    whole ? load8(dh + at) : load_part(dh + at, left), og, ou);
-  *reinterpret_cast<u32x4*>(cg + m * ld + n) = og;  // dh is zero behind the row, so og and ou are
-  *reinterpret_cast<u32x4*>(cu + m * ld + n) = ou;
-  if (whole) {
-    __builtin_memcpy(dg + at, &og, 16);
-    __builtin_memcpy(du + at, &ou, 16);
-  } else {
-    store_part(dg + at, og, left);
-    store_part(du + at, ou, left);
+  for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+    const int64_t at = m * N + n;
+    u32x4 og, ou;
+    dgates8<F16, ACT>(whole ? load8(g + at) : load_part(g + at, left), whole ? load8(u + at) : load_part(u + at, left),
+                      whole ? load8(dh + at) : load_part(dh + at, left), og, ou);
+    *reinterpret_cast<u32x4*>(cg + m * ld + n) = og;  // dh is zero behind the row, so og and ou are
+    *reinterpret_cast<u32x4*>(cu + m * ld + n) = ou;
+    if (whole) {
+      __builtin_memcpy(dg + at, &og, 16);
+      __builtin_memcpy(du + at, &ou, 16);
+    } else {
+      store_part(dg + at, og, left);
+      store_part(du + at, ou, left);
+    }
   }
 }
 
@@ -168,9 +169,9 @@ hipError_t launch_glu_bwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_
   }
   auto gates = [&]<bool F16, int ACT>() {
     if (plan.copy_bytes) {
-      const dim3 grid(unsigned(M), unsigned((plan.ld / 8 + kThreads - 1) / kThreads));
+      const dim3 grid(unsigned(std::min<int64_t>(M, 1 << 20)), unsigned((plan.ld / 8 + kThreads - 1) / kThreads));
       hipLaunchKernelGGL((glu_dgates_ragged_kernel<F16, ACT>), grid, dim3(kThreads), 0, s, G, U, dH, dG, dU, cg, cu,
-                         int(N), plan.ld);
+                         M, int(N), plan.ld);
     } else {
       const dim3 grid(unsigned((mn + 8 * kThreads - 1) / (8 * kThreads)));
       hipLaunchKernelGGL((glu_dgates_kernel<F16, ACT>), grid, dim3(kThreads), 0, s, G, U, dH, dG, dU, mn);

@@ -82,35 +82,57 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
   const int ul = ((tid >> 1) & 3) | (UB ? ((tid >> 4) & 1) * 4 : 0);
   const int nl = (nr & 3) | ((tid >> 3) & 1) * 4 | (nr >> 2) * 8;
   const int u = min((k0 >> 5) + ul, U - 1);
-  auto at_row = [&](int t, int& nb) {  // matrix and first row of stage t (clamped to the last stage)
+  // The weights of one stage after the other: first rows of the stage in every
+  // plane, scalars that advance by 32 rows; the last stage again past the end.
+  struct Walk {
+    Mat m;
+    int nb, t;
+  };
+  auto walk_from = [&](int t) {
     t = min(t, 2 * NS - 1);
     const bool up = t >= NS;
-    nb = 32 * (up ? t - NS : t);
-    Mat m;
+    Walk w;
+    w.t = t;
+    w.nb = 32 * (up ? t - NS : t);
 #pragma unroll
-    for (int i = 0; i < kPlanes<FMT>; ++i) m.p[i] = (up ? p.wu.p[i] : p.wg.p[i]) + int64_t(nb) * row_bytes<FMT>(i, K);
-    return m;
+    for (int i = 0; i < kPlanes<FMT>; ++i)
+      w.m.p[i] = (up ? p.wu.p[i] : p.wg.p[i]) + int64_t(w.nb) * row_bytes<FMT>(i, K);
+    return w;
   };
-  auto load = [&](int t) {
-    int nb;
-    const Mat w = at_row(t, nb);
-    return load_half<FMT, kByUnit>(w, min(nl, N - 1 - nb), u, half, K);
+  auto advance = [&](Walk& w) {
+    const bool stay = w.t + 1 >= 2 * NS, turn = w.t + 1 == NS;
+    w.t += stay ? 0 : 1;
+    w.nb = turn ? 0 : w.nb + (stay ? 0 : 32);
+#pragma unroll
+    for (int i = 0; i < kPlanes<FMT>; ++i)
+      w.m.p[i] = turn ? p.wu.p[i] : w.m.p[i] + (stay ? 0 : 32 * row_bytes<FMT>(i, K));
+  };
+  const RowAt<FMT> nl_at = row_at<FMT>(nl, K);
+  auto load = [&](const Walk& w) {
+    RowAt<FMT> r;  // rows past N: the last one
+    const uint32_t lastrow = N - 1 - w.nb;
+#pragma unroll
+    for (int i = 0; i < kPlanes<FMT>; ++i) r.o[i] = nl <= int(lastrow) ? nl_at.o[i] : lastrow * row_bytes<FMT>(i, K);
+    return load_half<FMT, kByUnit>(w.m, r, u, half);
   };
   auto decode = [&](const HalfRaw<FMT>& c, int i, u32x4* A) {
     A[rows_at<BR>(nl, ul, half, i)] = word_piece<FMT, F16>(c, u, 2 * half + i, i);
   };
   // dense rows: LDS slot tid + t * NT is row (tid + t * NT) / (BR / 8)
-  auto copy_a = [&](int st, u32x4* A) {
-    int nb;
-    const Mat w = at_row(st, nb);
-    const Buf b = buffer_of(scalar_base(w.p[0]));
+  uint32_t ao[APT];
+  int an[APT];
 #pragma unroll
-    for (int t = 0; t < APT; ++t) {
-      const int id = tid + t * NT, n = id / (BR / 8), s = id % (BR / 8);
-      const int unit = min((k0 >> 5) + ((s >> 2) ^ (n & 3)), U - 1);
-      copy_to_lds(b, uint32_t(min(n, N - 1 - nb)) * uint32_t(2 * K) + 64 * unit + 32 * ((s >> 1) & 1) +
-                         16 * ((s & 1) ^ ((n >> 2) & 1)), 0, A + t * NT + wave * 64);
-    }
+  for (int t = 0; t < APT; ++t) {
+    const int id = tid + t * NT, n = id / (BR / 8), s = id % (BR / 8);
+    const int unit = min((k0 >> 5) + ((s >> 2) ^ (n & 3)), U - 1);
+    ao[t] = 64 * unit + 32 * ((s >> 1) & 1) + 16 * ((s & 1) ^ ((n >> 2) & 1));
+    an[t] = n;
+  }
+  auto copy_a = [&](const Walk& w, u32x4* A) {
+    const Buf b = buffer_of(scalar_base(w.m.p[0]));
+#pragma unroll
+    for (int t = 0; t < APT; ++t)
+      copy_to_lds(b, uint32_t(min(an[t], N - 1 - w.nb)) * uint32_t(2 * K) + ao[t], 0, A + t * NT + wave * 64);
   };
   // Tokens: LDS slot tid + t * NT of a tile is row (tid + t * NT) / 4.  Pieces past
   // the row, and all pieces of a stage past the split's end, get an offset past
@@ -122,13 +144,19 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
 #pragma unroll
   for (int t = 0; t < XPT; ++t)
     xo[t] = uint32_t(min(m0 + t * (NT / 4) + (tid >> 2), p.M - 1) - m0) * uint32_t(2 * ld) + 16 * xc;
-  auto copy_x = [&](int st, u32x4* X) {
-    const bool up = st >= NS;
-    const int nb = 32 * (up ? st - NS : st);
-    const bool in = st < end && nb + 8 * xc < ld;
-    const Buf b = buffer_of(scalar_base((up ? ux : gx) + 2 * nb), 0x7FFFFFFF);
+  struct XWalk {
+    const uint8_t* p;
+    int nb, t;
+  };
+  auto copy_x = [&](XWalk& w, u32x4* X) {  // and on to the next stage
+    const bool in = w.t < end && w.nb + 8 * xc < ld;
+    const Buf b = buffer_of(scalar_base(w.p), 0x7FFFFFFF);
 #pragma unroll
     for (int t = 0; t < XPT; ++t) copy_to_lds(b, in ? xo[t] : 0x80000000u, 0, X + t * NT + wave * 64);
+    w.t += 1;
+    const bool turn = w.t == NS;
+    w.nb = turn ? 0 : w.nb + 32;
+    w.p = turn ? ux : w.p + 64;
   };
 
   f32x16 acc[RB][TB];
@@ -167,25 +195,36 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
   };
 
   HalfRaw<FMT> c[4];
+  Walk walk = walk_from(first);
+  XWalk xwalk{first < NS ? gx + 64 * int64_t(first) : ux + 64 * int64_t(first - NS), 32 * (first < NS ? first : first - NS), first};
+  auto copy_a_next = [&](u32x4* A) {
+    copy_a(walk, A);
+    advance(walk);
+  };
+  auto load_next = [&] {
+    const HalfRaw<FMT> r = load(walk);
+    advance(walk);
+    return r;
+  };
   if constexpr (DIRECT) {
-    copy_a(first, A0);
-    copy_a(first + 1, A1);
-    copy_a(first + 2, A2);
+    copy_a_next(A0);
+    copy_a_next(A1);
+    copy_a_next(A2);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = load(first + i);
+    for (int i = 0; i < 4; ++i) c[i] = load_next();
   }
-  copy_x(first, X0);
-  copy_x(first + 1, X1);
-  copy_x(first + 2, X2);
+  copy_x(xwalk, X0);
+  copy_x(xwalk, X1);
+  copy_x(xwalk, X2);
   if constexpr (!DIRECT) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       decode(c[0], i, A0);
       decode(c[1], i, A1);
     }
-    c[0] = load(first + 4);
-    c[1] = load(first + 5);
+    c[0] = load_next();
+    c[1] = load_next();
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   lds_barrier16();
@@ -198,8 +237,8 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
          const u32x4 *A = At.template operator()<H>(), *X = Xt.template operator()<H>();
          const u32x4 *A1n = At.template operator()<H + 1>(), *X1n = Xt.template operator()<H + 1>();
          u32x4* A2n = At.template operator()<H + 2>();
-         copy_x(st + H + 3, Xt.template operator()<H + 3>());
-         if constexpr (DIRECT) copy_a(st + H + 3, At.template operator()<H + 3>());
+         copy_x(xwalk, Xt.template operator()<H + 3>());
+         if constexpr (DIRECT) copy_a_next(At.template operator()<H + 3>());
          fence();
          read(f1, A, X, 1);
          if constexpr (!DIRECT) decode(c[(H + 2) & 3], 0, A2n);
@@ -208,7 +247,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
          read(f0, A1n, X1n, 0);
          if constexpr (!DIRECT) {
            decode(c[(H + 2) & 3], 1, A2n);
-           c[(H + 2) & 3] = load(st + H + 6);
+           c[(H + 2) & 3] = load_next();
          }
          mul(f1);
          fence();

@@ -27,7 +27,8 @@ constexpr int issued_after(int from, bool codes, int now) {
   for (int s = from; s <= now; ++s) {
     const int h = (s + 4 * kRun) % kRun;
     if (s > from) n += XPT;
-    if ((s > from || !codes) && (h + 2) % kChunk<FMT> == 0) n += CPT;
+    if (s == from && codes) continue;  // the order of the scales' loads and the codes' copies is open
+    if ((h + 2) % kChunk<FMT> == 0) n += CPT;
     if (h == 0) n += kMetaLoads<FMT>;
   }
   return n;
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   for (int u = runs * SR; u < U; ++u) {
 #pragma unroll
     for (int t = 0; t < XPT; ++t) X0[tid + t * NT] = load_at<u32x4>(xb, xo[t] + 64 * u);
-    const HalfRaw<FMT> r = load_half<FMT, kByRow>(w, wrow, u, half, K);
+    const HalfRaw<FMT> r = load_half<FMT, kByRow>(w, row_at<FMT>(wrow, K), u, half);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (WPT == 2 || i == (word & 1)) A0[tile32_at(arow, 2 * half + i)] = word_piece<FMT, F16>(r, u, 2 * half + i, i);

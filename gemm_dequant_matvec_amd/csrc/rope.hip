@@ -110,61 +110,63 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs p) {
   __shared__ float2 cs[kMaxPairs];
   const int tid = threadIdx.x;
   const int P = p.R >> 1;
-  const int64_t t0 = int64_t(blockIdx.x) * p.tb;
-  const int nt = int(min(int64_t(p.tb), p.T - t0));
-  for (int i = tid; i < nt * P; i += kThreads) {
-    const int t = i / P, f = i - t * P;
-    float c, s;
-    turn(p.pos[t0 + t], p.freqs[f], c, s);
-    cs[i] = make_float2(p.amplitude * c, p.sign * p.amplitude * s);
-  }
-  __syncthreads();
-
   // pieces of a head: the rotated ones, then the passing ones
   const int nr = HALF ? (P + V - 1) / V : (p.R + V - 1) / V;
+  for (int64_t t0 = int64_t(blockIdx.x) * p.tb; t0 < p.T; t0 += int64_t(gridDim.x) * p.tb) {
+    const int nt = int(min(int64_t(p.tb), p.T - t0));
+    for (int i = tid; i < nt * P; i += kThreads) {
+      const int t = i / P, f = i - t * P;
+      float c, s;
+      turn(p.pos[t0 + t], p.freqs[f], c, s);
+      cs[i] = make_float2(p.amplitude * c, p.sign * p.amplitude * s);
+    }
+    __syncthreads();
+
 #pragma unroll 1
-  for (int k = 0; k < p.count; ++k) {
-    const RopeTensor& q = p.t[k];
-    const int np = nr + (q.copy ? (p.D - p.R + V - 1) / V : 0);
-    const int items = nt * q.heads * np;
-    for (int it = tid; it < items; it += kThreads) {
-      const int th = it / np, c = it - th * np;
-      const int t = th / q.heads, h = th - t * q.heads;
-      const T* x = static_cast<const T*>(q.x) + (t0 + t) * q.xt + h * q.xh;
-      T* y = static_cast<T*>(q.y) + (t0 + t) * q.yt + h * q.yh;
-      if (c >= nr) {
-        const int at = p.R + (c - nr) * V, n = min(V, p.D - at);
-        float v[V];
-        El::load(x + at, n, v);
-        El::store(y + at, n, v);
-      } else if constexpr (HALF) {
-        const int i0 = c * V, n = min(V, P - i0);
-        float a[V], b[V];
-        El::load(x + i0, n, a);
-        El::load(x + P + i0, n, b);
+    for (int k = 0; k < p.count; ++k) {
+      const RopeTensor& q = p.t[k];
+      const int np = nr + (q.copy ? (p.D - p.R + V - 1) / V : 0);
+      const int items = nt * q.heads * np;
+      for (int it = tid; it < items; it += kThreads) {
+        const int th = it / np, c = it - th * np;
+        const int t = th / q.heads, h = th - t * q.heads;
+        const T* x = static_cast<const T*>(q.x) + (t0 + t) * q.xt + h * q.xh;
+        T* y = static_cast<T*>(q.y) + (t0 + t) * q.yt + h * q.yh;
+        if (c >= nr) {
+          const int at = p.R + (c - nr) * V, n = min(V, p.D - at);
+          float v[V];
+          El::load(x + at, n, v);
+          El::store(y + at, n, v);
+        } else if constexpr (HALF) {
+          const int i0 = c * V, n = min(V, P - i0);
+          float a[V], b[V];
+          El::load(x + i0, n, a);
+          El::load(x + P + i0, n, b);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 w = cs[t * P + min(i0 + i, P - 1)];
-          const float u = a[i];
-          a[i] = fmaf(-b[i], w.y, u * w.x);
-          b[i] = fmaf(u, w.y, b[i] * w.x);
-        }
-        El::store(y + i0, n, a);
-        El::store(y + P + i0, n, b);
-      } else {
-        const int i0 = c * V, n = min(V, p.R - i0);
-        float a[V];
-        El::load(x + i0, n, a);
+          for (int i = 0; i < V; ++i) {
+            const float2 w = cs[t * P + min(i0 + i, P - 1)];
+            const float u = a[i];
+            a[i] = fmaf(-b[i], w.y, u * w.x);
+            b[i] = fmaf(u, w.y, b[i] * w.x);
+          }
+          El::store(y + i0, n, a);
+          El::store(y + P + i0, n, b);
+        } else {
+          const int i0 = c * V, n = min(V, p.R - i0);
+          float a[V];
+          El::load(x + i0, n, a);
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          const float2 w = cs[t * P + min((i0 + i) >> 1, P - 1)];
-          const float u = a[i];
-          a[i] = fmaf(-a[i + 1], w.y, u * w.x);
-          a[i + 1] = fmaf(u, w.y, a[i + 1] * w.x);
+          for (int i = 0; i < V; i += 2) {
+            const float2 w = cs[t * P + min((i0 + i) >> 1, P - 1)];
+            const float u = a[i];
+            a[i] = fmaf(-a[i + 1], w.y, u * w.x);
+            a[i + 1] = fmaf(u, w.y, a[i + 1] * w.x);
+          }
+          El::store(y + i0, n, a);
         }
-        El::store(y + i0, n, a);
       }
     }
+    __syncthreads();  // the sines of these tokens are done with
   }
 }
 
@@ -191,7 +193,7 @@ hipError_t launch_rope(int64_t T, int D, int R, int layout, int count, const qmv
   int64_t tb = std::max(1, 16384 / per);
   tb = std::min<int64_t>({tb, std::max<int64_t>(1, kMaxPairs / (R / 2)), std::max<int64_t>(1, T / 512)});
   p.tb = int(tb);
-  const dim3 grid(static_cast<unsigned>((T + tb - 1) / tb));
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((T + tb - 1) / tb, 1 << 20)));
   const bool half = layout == QMV_ROPE_HALF;
 #define QMV_ROPE_GO(E)                                                                   \
   if (half) hipLaunchKernelGGL((rope_kernel<E, true>), grid, dim3(kThreads), 0, s, p);   \

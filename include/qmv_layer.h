@@ -49,11 +49,12 @@ enum qmv_rope_kind {
  *   H        [M][N] of h_dtype == x_dtype, device, 16-byte aligned
  *   G, U     [M][N] of h_dtype, 16-byte aligned: receive g and u, which
  *            qmv_gemm_glu_backward needs; both or neither (NULL)
- * N >= 1, any M >= 1 (from single tokens to training batches).  No output may
- * overlap another buffer of the call.  Within a row the result does not depend
+ * N >= 1, any M >= 1 (from single tokens to training batches); N, K <= 2^21,
+ * M <= 2^30, M * N and M * K <= 2^34.  No output may overlap another buffer of
+ * the call.  Within a row the result does not depend
  * on the other rows' values, and calls repeat bit for bit.
  * Errors: FORMAT, SHAPE, NULL, ALIGN, DTYPE, UNSUPPORTED (x_dtype f32 / Q8X, h_dtype other than
- * x_dtype, unknown act), OVERFLOW, DEVICE, LAUNCH.
+ * x_dtype, unknown act, one buffer given twice), OVERFLOW, DEVICE, LAUNCH.
  */
 int qmv_gemm_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up, const void* X,
                  int x_dtype, int act, void* H, int h_dtype, void* G, void* U, void* stream);
@@ -102,7 +103,8 @@ typedef struct qmv_rope_tensor {
  * same amplitude that is the gradient of the forward call.  The angle is
  * reduced in f64, so far positions (|pos| < 2^31) keep f32 accuracy; the
  * rotation is f32 and each output is rounded once to dtype.
- *   D >= 1, R even, 2 <= R <= D, R <= 4096; 1 <= count <= QMV_ROPE_MAX
+ *   D >= 1, R even, 2 <= R <= D, R <= 4096; 1 <= count <= QMV_ROPE_MAX;
+ *   T < 2^31, the tensors' heads together times D <= 2^28
  *   dtype     QMV_F32, QMV_F16 or QMV_BF16, of every x and y, aligned to its element
  *   pos       int64 [T], freqs f32 [R/2] (device)
  * Errors: SHAPE, NULL, ALIGN, DTYPE, UNSUPPORTED (Q8X), OVERFLOW, DEVICE, LAUNCH.

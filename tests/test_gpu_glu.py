@@ -118,11 +118,11 @@ def test_forward_sizes(qmv, fmt, dtype, act, M, N, K):
     run_forward(qmv, fmt, dtype, act, M, N, K)
 
 
-def run_backward(qmv, fmt, dtype, act, M, N, K, alias=False):
+def run_backward(qmv, fmt, dtype, act, M, N, K, alias=False, scale=0.25):
     dt = DT[dtype]
     say("glu_bwd", fmt, dtype, act, M, N, K)
     (wg, Wg), (wu, Wu) = weights(fmt, N, K, (33, N, K), dt), weights(fmt, N, K, (34, N, K), dt)
-    G, U, dH = inputs((M, N), dt, 1), inputs((M, N), dt, 2), inputs((M, N), dt, 3, 0.25)
+    G, U, dH = inputs((M, N), dt, 1), inputs((M, N), dt, 2), inputs((M, N), dt, 3, scale)
     Gd, Ud, Hd = G.cuda(), U.cuda(), dH.cuda()
     kw = dict(dG=Gd, dU=Hd) if alias else {}
     dX, dG, dU = qmv.gemm_glu_backward(fmt, pack_dev(qmv, fmt, wg), pack_dev(qmv, fmt, wu), Gd, Ud, Hd, N, K, act=act, **kw)
@@ -278,3 +278,48 @@ def test_repeats_streams_and_graphs(qmv):
             for a, b, c in zip(out, base, eager):
                 assert torch.equal(a, b) and torch.equal(c, b)
                 a.zero_()
+
+
+def test_small_gradients_keep_their_subnormals(qmv):
+    """f16 gradients far below 2^-14: the matrix cores take subnormal operands as
+    they are (dX from the returned dG, dU within its bound)."""
+    run_backward(qmv, "w4a16_g64", "f16", "silu", 70, 128, 128, scale=2.0 ** -17)
+    run_backward(qmv, "bf16", "f16", "gelu", 300, 200, 256, scale=2.0 ** -19)
+
+
+def test_rounds_of_the_chip(qmv):
+    """Backward tiles and cuts at sizes around one round of the chip, against the
+    forward's weights: every row of dX equals the row of a one-row call's up to
+    the order of its sum."""
+    fmt, N, K, dt = "q8_0", 192, 512, torch.bfloat16
+    (wg, Wg), (wu, Wu) = weights(fmt, N, K, (43, 0, 0), dt), weights(fmt, N, K, (44, 0, 0), dt)
+    Pg, Pu = pack_dev(qmv, fmt, wg), pack_dev(qmv, fmt, wu)
+    e, _ = half_step(dt)
+    for M in (2, 64, 65, 128, 129, 1000, 9000):
+        G, U, dH = (inputs((M, N), dt, i) for i in (11, 12, 13))
+        dX, dG, dU = (t.cpu() for t in qmv.gemm_glu_backward(fmt, Pg, Pu, G.cuda(), U.cuda(), dH.cuda(), N, K))
+        ref = dG.double() @ Wg + dU.double() @ Wu
+        d = 4 * N * T * (dG.double().abs() @ Wg.abs() + dU.double().abs() @ Wu.abs())
+        say("M", M)
+        check("dX", dX, ref, d + e * (ref.abs() + d))
+
+
+def test_stream_argument_and_devices(qmv):
+    """stream= runs there and allocates there; a CPU tensor among them is refused."""
+    fmt, M, N, K, dt = "w4a16_g64", 20, 96, 128, torch.bfloat16
+    (wg, _), (wu, _) = weights(fmt, N, K, (45, 0, 0), dt), weights(fmt, N, K, (46, 0, 0), dt)
+    Pg, Pu = pack_dev(qmv, fmt, wg), pack_dev(qmv, fmt, wu)
+    X = inputs((M, K), dt, 1).cuda()
+    H, G, U = qmv.gemm_glu(fmt, Pg, Pu, X, N, K, save=True)
+    base = qmv.gemm_glu_backward(fmt, Pg, Pu, G, U, H, N, K)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = qmv.gemm_glu(fmt, Pg, Pu, X, N, K, save=True, stream=s)
+    back = qmv.gemm_glu_backward(fmt, Pg, Pu, *got[1:], got[0], N, K, stream=s)
+    s.synchronize()
+    for a, b in zip((*got, *back), (H, G, U, *base)):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        qmv.gemm_glu(fmt, Pg.cpu(), Pu, X, N, K)
+    with pytest.raises(ValueError):
+        qmv.gemm_glu_backward(fmt, Pg, Pu, G, U.cpu(), H, N, K)

@@ -32,7 +32,7 @@ P = 0x10000  # an aligned address that no refused call touches
 
 
 def glu(q, **kw):
-    a = dict(fmt=2, N=64, K=64, M=4, wg=P, wu=P, x=P, xd=3, act=1, h=P, hd=3, g=0, u=0)
+    a = dict(fmt=2, N=64, K=64, M=4, wg=P, wu=P, x=P, xd=3, act=1, h=3 * P, hd=3, g=0, u=0)
     a.update(kw)
     return q.raw_call("qmv_gemm_glu", a["fmt"], a["N"], a["K"], a["M"], a["wg"], a["wu"], a["x"], a["xd"], a["act"],
                       a["h"], a["hd"], a["g"], a["u"], None)
@@ -46,10 +46,17 @@ def glu(q, **kw):
     (dict(act=0), UNSUP, "act"), (dict(act=4), UNSUP, "act"), (dict(wg=P + 4), ALIGN, "W_gate"),
     (dict(wu=P + 8), ALIGN, "W_up"), (dict(x=P + 2), ALIGN, "X"), (dict(h=P + 8), ALIGN, "H"),
     (dict(g=P + 2, u=P), ALIGN, "G"), (dict(g=P, u=P + 2), ALIGN, "U"), (dict(M=1 << 33), OVER, "M"),
-    (dict(N=1 << 31), OVER, "N"), (dict(M=1 << 24, N=1 << 20), OVER, "M * N")])
+    (dict(N=1 << 31), OVER, "N"), (dict(M=1 << 24, N=1 << 20), OVER, "M * N"),
+    (dict(M=(1 << 30) + 1, N=1), OVER, "M is past"), (dict(N=1 << 22), OVER, "2^21")])
 def test_glu_refusals(q, kw, status, text):
     assert glu(q, **kw) == status, q.last_error()
     assert text in q.last_error()
+
+
+@pytest.mark.parametrize("kw,text", [(dict(h=P), "X"), (dict(g=P, u=4 * P), "X"), (dict(g=3 * P, u=4 * P), "one buffer"),
+                                     (dict(g=4 * P, u=4 * P), "one buffer")])
+def test_glu_buffers_given_twice(q, kw, text):
+    assert glu(q, **{"h": 3 * P, **kw}) == UNSUP and text in q.last_error()
 
 
 def bwd(q, **kw):
