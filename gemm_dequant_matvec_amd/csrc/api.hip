@@ -12,7 +12,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "qmv_internal.h"
+#include "layer_internal.h"
 
 namespace {
 

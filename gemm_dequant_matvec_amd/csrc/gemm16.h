@@ -10,7 +10,7 @@
 // rounded once, to nearest even, to the operand type.
 #pragma once
 
-#include "qmv_internal.h"
+#include "layer_internal.h"
 
 namespace qmv {
 
