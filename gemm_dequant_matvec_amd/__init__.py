@@ -10,6 +10,9 @@ Importing this package fails loudly when the library has not been built
     W = qmv.pack("q4k", {"q": q, "sc": sc, "m": m, "d": d, "dmin": dmin})
     y = qmv.matvec("q4k", W, x, N, K)          # x [b][K] f32 -> y [b][N] f32
     Y = qmv.gemm("w4a16_g64", W, X, N, K)      # X [M][K] bf16 -> Y [M][N] bf16
+    H, G, U = qmv.gemm_glu("q4k", Wg, Wu, X, N, K, act="silu", save=True)   # act(X Wg^T) * (X Wu^T)
+    dX, dG, dU = qmv.gemm_glu_backward("q4k", Wg, Wu, G, U, dH, N, K, act="silu")
+    q, k = qmv.rope(q, k, pos, qmv.rope_freqs(R))   # q [T][heads][D], k [T][kv_heads][D]
 """
 from __future__ import annotations
 

@@ -42,6 +42,14 @@ __device__ __forceinline__ u32x2 read_tr(const u32x4* A, int pos8) {  // pos8: i
 template <int FMT>
 constexpr int kHalfLoads = FMT == QMV_Q6K ? 4 : is_fifth(FMT) ? 3 : 2;
 
+// dX[m][k] = sum_n dG[m][n] W~g[n][k] + dU[m][n] W~u[n][k], one f32 accumulator
+// over both sums.  Its operands are dG and dU as they leave the call, rounded
+// once to the 16-bit type: the matrix cores take no wider ones, and two passes
+// over a high and a low part would double the MFMAs that bound the kernel.  The
+// relative error of dX is therefore about sqrt(2) of what rounding dX alone
+// gives (more where the terms of a sum cancel), as in a model that trains in
+// this type.
+//
 // RB, TB: 32-column blocks of dX and 32-token blocks per wave; WR x WT waves.
 //
 // The depth is n: first the gate rows, then the up rows, 32 to a stage.  Tokens
@@ -51,6 +59,12 @@ constexpr int kHalfLoads = FMT == QMV_Q6K ? 4 : is_fifth(FMT) ? 3 : 2;
 // stages ahead (dense bf16 rows need no decoding and are copied like the
 // tokens).  As in the forward kernel the first fragments of a stage are read
 // before the barrier that ends the stage before it.
+//
+// Bound by the matrix cores and the decoding beside them: W4A16, 5632 x 2048,
+// 8192 tokens take ~360 us, 1.05 PFLOP/s (a dense library product of the two
+// matrices 290), MFMAs busy ~50 % of the SIMDs' cycles at 1.95 GHz.  The wider
+// tile decodes a weight for 256 tokens; few tokens split the depth over
+// workgroups instead (glu_backward_plan), as a stage's latency is then what counts.
 template <int FMT, bool F16, int RB, int TB, int WR, int WT>
 __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs p) {
   constexpr int NT = 64 * WR * WT;
@@ -61,7 +75,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
 
   __shared__ u32x4 A0[BR * 4], A1[BR * 4], A2[BR * 4], A3[BR * 4];
   __shared__ u32x4 X0[BM * 4], X1[BM * 4], X2[BM * 4], X3[BM * 4];
-  asm volatile("" ::"v"(A0), "v"(A1), "v"(A2), "v"(A3) : "memory");  // see the forward kernel
+  asm volatile("" ::"v"(A0), "v"(A1), "v"(A2), "v"(A3) : "memory");  // escape, as in the forward kernel
   asm volatile("" ::"v"(X0), "v"(X1), "v"(X2), "v"(X3) : "memory");
   auto At = [&]<int S>() { return (S & 3) == 0 ? A0 : (S & 3) == 1 ? A1 : (S & 3) == 2 ? A2 : A3; };
   auto Xt = [&]<int S>() { return (S & 3) == 0 ? X0 : (S & 3) == 1 ? X1 : (S & 3) == 2 ? X2 : X3; };

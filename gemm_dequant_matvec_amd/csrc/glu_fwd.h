@@ -34,18 +34,32 @@ constexpr int issued_after(int from, bool codes, int now) {
   return n;
 }
 
+// Many tokens.  g = sum_k W~g[n][k] x[m][k] and u likewise in f32 accumulators,
+// H = act(g) u rounded once; gate and up row n meet in one wave, so the product
+// needs no second pass over G and U (which leave only if the caller keeps them
+// for the backward pass).
+//
 // RB, TB: 32-row blocks of weights (half gate, half up) and of tokens per wave;
 // WR x WT waves.
 //
 // K goes by in stages of 32: one unit of every weight row and 64 bytes of every
 // token, in a ring of four LDS tiles each.  Tokens go straight from global
-// memory to LDS, three stages ahead (seven were no faster).  So do the weights' codes, 64 bytes of
-// every row at a time into two more tiles; from there a pair of threads decodes
-// one unit of a row into the operand type, once per workgroup, two stages ahead.
-// The first fragments of a stage are
-// read before the barrier that ends the stage before it, so no wave waits for
-// LDS behind a barrier (with 64-deep steps in two buffers, all read after the
-// barrier, a step took 1.85 us for 0.92 us of MFMA).
+// memory to LDS, three stages ahead (seven were no faster).  So do the weights'
+// codes, 64 bytes of every row at a time into two more tiles; from there
+// neighbouring threads decode one unit of a row into the operand type, once per
+// workgroup, two stages ahead.  The first fragments of a stage are read before
+// the barrier that ends the stage before it, so no wave waits for LDS behind a
+// barrier (with 64-deep steps in two buffers, all read after the barrier, a step
+// took 1.85 us for 0.92 us of MFMA).
+//
+// Bound by the matrix cores and what shares their issue slots.  W4A16, 5632 x
+// 2048: 8192 tokens with G and U kept take 365 - 370 us, 1.02 - 1.04 PFLOP/s (414
+// where call follows call for long and the clock falls; a dense bf16 library
+// product of the two matrices alone takes 393).  The MFMAs are busy 52 % of the
+// SIMDs' cycles at the 1.86 GHz that the card holds under this load, LDS 30 %; the
+// rest is the decoding (~20 VALU instructions per 8 weights), the barriers and
+// ~26 us of stores.  512 tokens take 32 - 36 us, 0.65 - 0.74 PFLOP/s: one round of
+// the chip, of which ~10 us is launch, first loads and epilogue.
 template <int FMT, bool F16, int RB, int TB, int WR, int WT>
 __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs p) {
   constexpr int NT = 64 * WR * WT;
@@ -320,6 +334,10 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
 // follows the same order straight from global memory (no two waves share a
 // step, so LDS would only be a detour).  The partial tiles meet in LDS and are
 // added in wave order.
+//
+// Bound by the latency of a chain that is only K / (128 W) steps long: Q4K,
+// 5632 x 2048, 16 tokens take 9.7 us for 13.2 MB (1.36 TB/s; a copy of that size
+// at the card's 5.1 TB/s would take 2.6), of which ~3 us is the launch.
 template <int FMT, bool F16, int FM, int FN, int W>
 __global__ __launch_bounds__(64 * W) void glu_fwd_few_kernel(const GluFwdArgs p) {
   constexpr int T = 2 * FN * FM;  // partial 16 x 16 tiles per wave
@@ -421,6 +439,7 @@ __global__ __launch_bounds__(64 * W) void glu_fwd_few_kernel(const GluFwdArgs p)
 // The fewest tokens: as above with 8 gate and the same 8 up rows in one fragment,
 // which halves what a wave has to decode one after the other and gives twice the
 // workgroups; every workgroup reads all tokens, so it pays for few of them only.
+// W4A16, 5632 x 2048, one token: 7.4 us for 13 MB (1.76 TB/s).
 template <int FMT, bool F16, int W>
 __global__ __launch_bounds__(64 * W) void glu_fwd_fewest_kernel(const GluFwdArgs p) {
   __shared__ f32x4 red[W][64];
@@ -526,7 +545,9 @@ hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
   //            256 tokens       32        27         34         46
   //            512 tokens       50        40         36         49
   //           1024 tokens       90        65         69         54
-  // and Q4K, N 1024, K 1024, 128 tokens: 8.4 few-token kernel, 13.1 and 15.9 the first two.
+  // The few-token kernel up to 256 groups, the 64 x 64 tile past them: Q4K, 1024 x
+  // 1024, 128 tokens (128 groups) 8.4 against 13.1; W4A16, 1333 x 768, 197 tokens
+  // (336) 12.8 against 10.8; 5632 x 2048, 128 tokens (704) 38 against 22.
   auto tiles = [&](int bn, int bm) { return int64_t((p.N + bn - 1) / bn) * ((p.M + bm - 1) / bm); };
   if (tiles(64, 64) <= 256)
     hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 2>), dim3(unsigned(tiles(64, 64))), dim3(256), 0, s, p);

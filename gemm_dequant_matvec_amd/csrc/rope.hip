@@ -6,7 +6,11 @@
 // first R values of every head; the other D - R values pass.  The inverse
 // (t -> -t) is the gradient.  Bound by memory: each value is read and written
 // once, so a block computes the R/2 sines and cosines of its tokens once, into
-// LDS, for all heads of all tensors.
+// LDS, for all heads of all tensors.  A block takes tokens up to about 16 KB of
+// heads, so that its threads have several 16-byte pieces each and the sines are
+// not the longer part, but no more than leave 512 blocks.  f16, 24 heads of 128,
+// 32768 tokens: 81 us, 4.95 TB/s (a copy of 1 GiB runs at 5.1); bf16, 36 heads of
+// 64, 4096 tokens: 8.7 us, 4.3 TB/s; one token 2.8 us, the launch.
 //
 // The angle of a far position needs more than f32: pos * freq is formed in f64,
 // turned into revolutions, reduced to an eighth of a turn there and only then
