@@ -64,13 +64,16 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* p) {
   return v;
 }
 
-// The first n (0..7) of eight 16-bit values at p, zeros behind them; nothing
-// past p[n - 1] is read.
+// The first n (1..7) of eight 16-bit values at p, zeros behind them; nothing
+// past p[n - 1] is read (the last value again instead: eight loads that are
+// under way together, where a branch per value waits for each).
 __device__ __forceinline__ u32x4 load_part(const uint16_t* p, int n) {
   uint32_t o[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < n) o[e >> 1] |= uint32_t(p[e]) << (16 * (e & 1));
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t v = p[min(e, n - 1)];
+    o[e >> 1] |= e < n ? v << (16 * (e & 1)) : 0u;
+  }
   return u32x4{o[0], o[1], o[2], o[3]};
 }
 
