@@ -40,7 +40,9 @@ constexpr int issued_after(int from, bool codes, int now) {
 // for the backward pass).
 //
 // RB, TB: 32-row blocks of weights (half gate, half up) and of tokens per wave;
-// WR x WT waves.
+// KG groups of WR x WT waves.  Two groups halve K between them, each with tiles of
+// its own, and the second's sums join the first's in LDS: where a unit has one
+// small workgroup anyway, a second wave per SIMD works while the first waits.
 //
 // K goes by in stages of 32: one unit of every weight row and 64 bytes of every
 // token, in a ring of four LDS tiles each.  Tokens go straight from global
@@ -60,9 +62,9 @@ constexpr int issued_after(int from, bool codes, int now) {
 // rest is the decoding (~20 VALU instructions per 8 weights), the barriers and
 // ~26 us of stores.  512 tokens take 32 - 36 us, 0.65 - 0.74 PFLOP/s: one round of
 // the chip, of which ~10 us is launch, first loads and epilogue.
-template <int FMT, bool F16, int RB, int TB, int WR, int WT>
-__global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs p) {
-  constexpr int NT = 64 * WR * WT;
+template <int FMT, bool F16, int RB, int TB, int WR, int WT, int KG>
+__global__ __launch_bounds__(64 * WR * WT * KG) void glu_fwd_kernel(const GluFwdArgs p) {
+  constexpr int NT = 64 * WR * WT;      // threads of a group
   constexpr int BR = 32 * RB * WR, BN = BR / 2, BM = 32 * TB * WT;
   constexpr int XPT = BM * 4 / NT;      // 16-byte token pieces per thread and stage
   constexpr int SR = kRun, SC = kChunk<FMT>;  // stages per run and per tile of codes
@@ -73,17 +75,21 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
 
   // variables of their own: the compiler then knows that a copy into one does
   // not concern the reads of the others
-  __shared__ u32x4 A0[BR * 4], A1[BR * 4], A2[BR * 4], A3[BR * 4];
-  __shared__ u32x4 X0[BM * 4], X1[BM * 4], X2[BM * 4], X3[BM * 4];
-  __shared__ u32x4 R0[BR * 4], R1[BR * 4];  // rows of codes: gate 0 .. BN - 1, then up
+  __shared__ u32x4 SA0[KG][BR * 4], SA1[KG][BR * 4], SA2[KG][BR * 4], SA3[KG][BR * 4];
+  __shared__ u32x4 SX0[KG][BM * 4], SX1[KG][BM * 4], SX2[KG][BM * 4], SX3[KG][BM * 4];
+  __shared__ u32x4 SR0[KG][BR * 4], SR1[KG][BR * 4];  // rows of codes: gate 0 .. BN - 1, then up
   // let their addresses escape: otherwise the compiler knows that no asm
   // statement can touch them and moves LDS reads across the fences below
-  asm volatile("" ::"v"(A0), "v"(A1), "v"(A2), "v"(A3) : "memory");
-  asm volatile("" ::"v"(X0), "v"(X1), "v"(X2), "v"(X3), "v"(R0), "v"(R1) : "memory");
+  asm volatile("" ::"v"(SA0), "v"(SA1), "v"(SA2), "v"(SA3) : "memory");
+  asm volatile("" ::"v"(SX0), "v"(SX1), "v"(SX2), "v"(SX3), "v"(SR0), "v"(SR1) : "memory");
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+  u32x4 *const A0 = SA0[kg], *const A1 = SA1[kg], *const A2 = SA2[kg], *const A3 = SA3[kg];
+  u32x4 *const X0 = SX0[kg], *const X1 = SX1[kg], *const X2 = SX2[kg], *const X3 = SX3[kg];
+  u32x4 *const R0 = SR0[kg], *const R1 = SR1[kg];
   auto At = [&]<int S>() { return (S & 3) == 0 ? A0 : (S & 3) == 1 ? A1 : (S & 3) == 2 ? A2 : A3; };
   auto Xt = [&]<int S>() { return (S & 3) == 0 ? X0 : (S & 3) == 1 ? X1 : (S & 3) == 2 ? X2 : X3; };
 
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x - kg * NT, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / WT, wt = wave % WT;
   const TileId id0 = tile_of_block(p.N, BN, p.M, BM);
@@ -154,11 +160,13 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   };
 
   // ---- whole runs
-  const int runs = U / SR;
+  const int all = U / SR, per = (all + KG - 1) / KG;
+  const int r0 = kg * per, runs = min(per, all - r0);  // this group's, from r0 on
+  const int idle = per - runs;
   if (runs > 0) {
     // Workgroups start at different runs: in step they would all read the same
     // columns of rows a power of two apart, which lie on few L2 channels.
-    int ua = id0.y % runs * SR;  // first unit of the current run
+    int ua = (r0 + id0.y % runs) * SR;  // first unit of the current run
     RunMeta<FMT> cur, next;
     // words i of the unit of stage s of a run (first unit u, scales x) from codes R
     auto decode = [&](const u32x4 (&codes)[2], const RunMeta<FMT>& x, int u, int s, u32x4* A, int i) {
@@ -199,7 +207,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
     if constexpr (SC == 4) read_codes<FMT, WPT>(c[0], R0, ri, 2, word);
 #pragma unroll 1
     for (int run = 0; run < runs; ++run) {
-      const int then = ua + SR < runs * SR ? ua + SR : 0;
+      const int then = ua + SR < (r0 + runs) * SR ? ua + SR : r0 * SR;
       [&]<int... H>(std::integer_sequence<int, H...>) {
         (([&] {
            const u32x4 *A = At.template operator()<H>(), *X = Xt.template operator()<H>();
@@ -250,10 +258,19 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the copies past the end
     lds_barrier16();
+  } else if (per > 0) {  // a single run is the first group's: the barriers outside its stages
+    lds_barrier16();
+    lds_barrier16();
+    if constexpr (SC == 1) lds_barrier16();
+    lds_barrier16();
   }
+  // the barriers of the stages that the other group has more
+  if constexpr (KG > 1)
+    for (int i = 0; i < idle * SR; ++i) lds_barrier16();
 
   // ---- the rest of K, one unit at a time
-  for (int u = runs * SR; u < U; ++u) {
+  for (int u0 = all * SR; u0 < U; u0 += KG) {
+    const int u = min(u0 + kg, U - 1);
 #pragma unroll
     for (int t = 0; t < XPT; ++t) X0[tid + t * NT] = load_at<u32x4>(xb, xo[t] + 64 * u);
     const HalfRaw<FMT> r = load_half<FMT, kByRow>(w, row_at<FMT>(wrow, K), u, half);
@@ -261,11 +278,13 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
     for (int i = 0; i < 2; ++i)
       if (WPT == 2 || i == (word & 1)) A0[tile32_at(arow, 2 * half + i)] = word_piece<FMT, F16>(r, u, 2 * half + i, i);
     lds_barrier16();
-    Frag f;
+    if (u0 + kg < U) {
+      Frag f;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      read(f, A0, X0, s);
-      mul(f);
+      for (int s = 0; s < 2; ++s) {
+        read(f, A0, X0, s);
+        mul(f);
+      }
     }
     lds_barrier16();
   }
@@ -274,6 +293,26 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_fwd_kernel(const GluFwdArgs 
   // lane % 32.  Each output goes through the wave's own part of LDS (the tiles
   // are done with), so that rows of up to 128 bytes leave whole.
   lds_barrier16();
+  if constexpr (KG == 2) {  // the second group's sums join the first's, through the second's tiles
+    static_assert(RB * TB == 2 && NT * 2 == BR * 4);
+    f32x4* const at[4] = {reinterpret_cast<f32x4*>(SA0[1]), reinterpret_cast<f32x4*>(SA1[1]),
+                          reinterpret_cast<f32x4*>(SA2[1]), reinterpret_cast<f32x4*>(SA3[1])};
+    if (kg == 1) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const f32x16& v = acc[c >> 2][0];
+        at[c >> 1][(c & 1) * NT + tid] = f32x4{v[4 * (c & 3)], v[4 * (c & 3) + 1], v[4 * (c & 3) + 2], v[4 * (c & 3) + 3]};
+      }
+    }
+    lds_barrier16();
+    if (kg == 1) return;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const f32x4 v = at[c >> 1][(c & 1) * NT + tid];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[c >> 2][0][4 * (c & 3) + e] += v[e];
+    }
+  }
   constexpr int HB = RB / 2;                       // 32-row blocks of outputs
   constexpr int WPA = BR * 4 / (32 * 8);           // waves per weight tile, 32 tokens x 64 values each
   static_assert(NT / 64 <= 4 * WPA);
@@ -541,22 +580,28 @@ hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
   // one round (256 units, two 64 x 128 tiles to a unit), else the largest, which
   // decodes a weight once for the most tokens.  Us on W4A16, K = 2048, for tiles of
   // outputs x tokens:        64 x 64   64 x 128   64 x 256   128 x 256
-  //   N 5632,  128 tokens       22        26         33         46
+  //   N 5632,  128 tokens       21        26         33         46
   //            256 tokens       32        27         34         46
   //            512 tokens       50        40         36         49
   //           1024 tokens       90        65         69         54
   // The few-token kernel up to 256 groups, the 64 x 64 tile past them: Q4K, 1024 x
   // 1024, 128 tokens (128 groups) 8.4 against 13.1; W4A16, 1333 x 768, 197 tokens
-  // (336) 12.8 against 10.8; 5632 x 2048, 128 tokens (704) 38 against 22.
+  // (336) 12.8 against 10.8; 5632 x 2048, 128 tokens (704) 38 against 21.
+  // Two groups of waves from K = 1024 on (four runs): W4A16, 2048 wide, 256 tokens
+  // 19.3 against 21.8 at K = 2048, 15.7 against 17.3 at 1536; 1333 wide, 197 tokens
+  // 11.4 against 12.6 at 1024, 10.4 both at 768 (Q6K 14.1 against 13.3); 1300 wide,
+  // 300 tokens 6.5 against 6.1 at 256.
   auto tiles = [&](int bn, int bm) { return int64_t((p.N + bn - 1) / bn) * ((p.M + bm - 1) / bm); };
-  if (tiles(64, 64) <= 256)
-    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 2>), dim3(unsigned(tiles(64, 64))), dim3(256), 0, s, p);
+  if (tiles(64, 64) <= 256 && p.K >= 1024)
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 2, 2>), dim3(unsigned(tiles(64, 64))), dim3(512), 0, s, p);
+  else if (tiles(64, 64) <= 256)
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 2, 1>), dim3(unsigned(tiles(64, 64))), dim3(256), 0, s, p);
   else if (tiles(64, 128) <= 256 || (tiles(64, 256) > 256 && tiles(64, 128) <= 512))
-    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 4>), dim3(unsigned(tiles(64, 128))), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 1, 2, 4, 1>), dim3(unsigned(tiles(64, 128))), dim3(512), 0, s, p);
   else if (tiles(64, 256) <= 256)
-    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 2, 2, 4>), dim3(unsigned(tiles(64, 256))), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 2, 2, 2, 4, 1>), dim3(unsigned(tiles(64, 256))), dim3(512), 0, s, p);
   else
-    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 4, 2, 2, 4>), dim3(unsigned(tiles(128, 256))), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((glu_fwd_kernel<FMT, F16, 4, 2, 2, 4, 1>), dim3(unsigned(tiles(128, 256))), dim3(512), 0, s, p);
   return hipGetLastError();
 }
 
