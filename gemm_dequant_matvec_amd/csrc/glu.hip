@@ -114,34 +114,38 @@ __global__ __launch_bounds__(kThreads) void glu_join_kernel(const float* part, u
 
 }  // namespace
 
-// Measured on W4A16 (us): a stage of 32 rows takes 0.75 with the 256 x 256 tile
-// (one workgroup per compute unit), 0.45 with 128 x 128 alone on its unit and
-// 0.75 for two of them; a split's partial sums cost their write and read at
-// 4 TB/s and a launch.  The cut with the smallest estimate is taken.
+// Which tile and how many splits of the depth: the cut with the smallest
+// estimate.  Us per stage of 32 rows, by tile and by the workgroups on a compute
+// unit (as many as their LDS allows), what a round of the chip adds, and what the
+// join costs, fitted to 3364 timings (W4A16, Q4K, Q8_0 and dense; 1 to 4096 tokens
+// of 1333 x 768 to 5632 x 2048): on average 1.3 % and at most 12 % over the best
+// cut of each size.  W4A16, 5632 x 2048: 512 tokens 57.9 with 128 x 128 and 8
+// splits against 63.5 with 256 x 256 and 16, 2048 tokens 140 with 256 x 256 and 4
+// against 177 with 128 x 128 and 2.
 GluBwdPlan glu_backward_plan(int64_t N, int64_t K, int64_t M) {
+  struct Tile {
+    int k, m, units;  // columns, tokens; workgroups that share a unit
+    double stage[3], round;
+  };
+  constexpr Tile kTiles[3] = {
+      {128, 64, 3, {0.25, 0.37, 0.69}, 0.6}, {128, 128, 2, {0.33, 0.52}, 1.5}, {256, 256, 1, {0.68}, 5.4}};
   GluBwdPlan best{};
   const int64_t stages = 2 * ((N + 31) / 32);
   double best_us = 0;
-  auto consider = [&](int tile, int64_t tiles, int splits) {
-    const int64_t steps = ((stages + splits - 1) / splits + 3) / 4 * 4;
-    splits = int((stages + steps - 1) / steps);  // no empty split
-    const int64_t groups = tiles * splits;
-    double rounds = 0;
-    if (tile == 2) rounds = double((groups + 255) / 256) * 0.75;
-    else if (tile == 1) rounds = groups <= 256 ? 0.45 : double((groups + 511) / 512) * 0.75;
-    else rounds = groups <= 256 ? 0.35 : groups <= 512 ? 0.45 : double((groups + 767) / 768) * 0.6;
-    double us = 8.0 + rounds * double(steps);
-    if (splits > 1) us += 3.0 + double(splits) * double(M) * double(K) * 8e-6 / 4.0;
-    if (best.tiles && us >= best_us) return;
-    best_us = us;
-    best = GluBwdPlan{tile, splits, int(steps), 0, tiles, splits > 1 ? splits * M * K * 4 : 0, 0};
-  };
-  for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
-    if (splits > 1 && stages / splits < 8) break;
-    if (M <= 128) consider(0, (K + 127) / 128 * ((M + 63) / 64), splits);
-    if (M > 64) {
-      consider(1, ((K + 127) / 128) * ((M + 127) / 128), splits);
-      consider(2, ((K + 255) / 256) * ((M + 255) / 256), splits);
+  for (int64_t cut : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+    if (cut > 1 && stages / cut < 4) break;
+    const int64_t steps = ((stages + cut - 1) / cut + 3) / 4 * 4;
+    const int64_t splits = (stages + steps - 1) / steps;  // no empty split
+    for (int t = 0; t < 3; ++t) {
+      const Tile& c = kTiles[t];
+      const int64_t tiles = ((K + c.k - 1) / c.k) * ((M + c.m - 1) / c.m), groups = tiles * splits;
+      const int64_t full = groups / (256 * c.units), rest = (groups - full * 256 * c.units + 255) / 256;
+      double us = double(full) * (c.stage[c.units - 1] * double(steps) + c.round);
+      if (rest) us += c.stage[rest - 1] * double(steps) + c.round;
+      if (splits > 1) us += 0.6 + double(splits) * double(M) * double(K) * 8e-6 * 0.13;
+      if (best.tiles && us >= best_us) continue;
+      best_us = us;
+      best = GluBwdPlan{t, int(splits), int(steps), 0, tiles, splits > 1 ? splits * M * K * 4 : 0, 0};
     }
   }
   best.ld = int((N + 7) / 8 * 8);

@@ -118,6 +118,18 @@ def test_forward_sizes(qmv, fmt, dtype, act, M, N, K):
     run_forward(qmv, fmt, dtype, act, M, N, K)
 
 
+# the 64 x 64 tile, ragged in both directions: from K = 1024 on two groups of
+# waves share its depth (here of unequal halves, with and without units past the
+# last whole run), below one does all of it
+@pytest.mark.parametrize("least", [1280, 1024, 512, 64])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt", wl.FORMATS)
+def test_forward_small_tiles(qmv, fmt, dtype, least):
+    K = least if wl.BLOCK[fmt] == 256 else least + (96 if wl.BLOCK[fmt] == 32 else 64)
+    act = ("silu", "gelu_tanh", "gelu")[wl.FORMATS.index(fmt) % 3]
+    run_forward(qmv, fmt, dtype, act, 200, 1333, max(K, wl.BLOCK[fmt]), save=least == 1280)
+
+
 def run_backward(qmv, fmt, dtype, act, M, N, K, alias=False, scale=0.25):
     dt = DT[dtype]
     say("glu_bwd", fmt, dtype, act, M, N, K)
@@ -158,6 +170,15 @@ def test_backward(qmv, fmt, dtype, M, N, mult):
     ("i8row", "bf16", "silu", 4100, 136, 4128)])
 def test_backward_sizes(qmv, fmt, dtype, act, M, N, K):
     run_backward(qmv, fmt, dtype, act, M, N, K)
+
+
+# the 256 x 256 tile, ragged in every direction, with one cut of the depth and with several
+@pytest.mark.parametrize("M,N,K", [(2050, 500, 4160), (2050, 1333, 2112)])
+@pytest.mark.parametrize("fmt", wl.FORMATS)
+def test_backward_large_tiles(qmv, fmt, M, N, K):
+    if wl.BLOCK[fmt] == 256:
+        K = -(-K // 256) * 256
+    run_backward(qmv, fmt, "f16" if wl.FORMATS.index(fmt) % 2 else "bf16", "silu", M, N, K)
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu"])
