@@ -117,11 +117,11 @@ __global__ __launch_bounds__(kThreads) void glu_join_kernel(const float* part, u
 // Which tile and how many splits of the depth: the cut with the smallest
 // estimate.  Us per stage of 32 rows, by tile and by the workgroups on a compute
 // unit (as many as their LDS allows), what a round of the chip adds, and what the
-// join costs, fitted to 3364 timings (W4A16, Q4K, Q8_0 and dense; 1 to 4096 tokens
-// of 1333 x 768 to 5632 x 2048): on average 1.3 % and at most 12 % over the best
-// cut of each size.  W4A16, 5632 x 2048: 512 tokens 57.9 with 128 x 128 and 8
-// splits against 63.5 with 256 x 256 and 16, 2048 tokens 140 with 256 x 256 and 4
-// against 177 with 128 x 128 and 2.
+// join costs (its launch and its bytes), fitted to 5191 timings (W4A16, Q4K, Q8_0
+// and dense; 1 to 4096 tokens of 64 x 256 to 5632 x 2048): on average 1 % and at
+// most 12 % over the best cut of each size.  W4A16, 5632 x 2048: 512 tokens 57.9
+// with 128 x 128 and 8 splits against 63.5 with 256 x 256 and 16, 2048 tokens 140
+// with 256 x 256 and 4 against 177 with 128 x 128 and 2.
 GluBwdPlan glu_backward_plan(int64_t N, int64_t K, int64_t M) {
   struct Tile {
     int k, m, units;  // columns, tokens; workgroups that share a unit
@@ -142,7 +142,7 @@ GluBwdPlan glu_backward_plan(int64_t N, int64_t K, int64_t M) {
       const int64_t full = groups / (256 * c.units), rest = (groups - full * 256 * c.units + 255) / 256;
       double us = double(full) * (c.stage[c.units - 1] * double(steps) + c.round);
       if (rest) us += c.stage[rest - 1] * double(steps) + c.round;
-      if (splits > 1) us += 0.6 + double(splits) * double(M) * double(K) * 8e-6 * 0.13;
+      if (splits > 1) us += 2.0 + double(splits) * double(M) * double(K) * 8e-6 * 0.13;
       if (best.tiles && us >= best_us) continue;
       best_us = us;
       best = GluBwdPlan{t, int(splits), int(steps), 0, tiles, splits > 1 ? splits * M * K * 4 : 0, 0};
