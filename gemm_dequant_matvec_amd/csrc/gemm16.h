@@ -282,6 +282,10 @@ __device__ __forceinline__ void decode8(const Word8& c, float a, float b, int i,
       ev |= ((c.qh >> (4 * (i & 1))) & 0x03030303u) << 4;
       od |= ((c.qh >> (4 * (i & 1) + 2)) & 0x03030303u) << 4;
     }
+    // whole bytes, as the conversion takes them: seeing the mask, the compiler
+    // extracts four bits at a time instead (6 more instructions per 8 weights;
+    // W4A16, 5632 x 2048, 512 tokens 36.5 against 34.0 us)
+    asm("" : "+v"(ev), "+v"(od));
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       w[2 * k] = fmaf(a, static_cast<float>((ev >> (8 * k)) & 0xFFu), b);

@@ -413,9 +413,9 @@ __global__ __launch_bounds__(64 * W) void glu_fwd_few_kernel(const GluFwdArgs p)
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[0][i][j] = acc[1][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto use = [&](const Set& s, int step) {
+  auto use_as = [&]<bool WHOLE>(const Set& s, int step) {
     const int u = 4 * step + g4;
-    const bool in = u < U;
+    const bool in = WHOLE || u < U;
     const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -426,16 +426,21 @@ __global__ __launch_bounds__(64 * W) void glu_fwd_few_kernel(const GluFwdArgs p)
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int n = 0; n < FN; ++n) {
-          const u32x4 v = unit_piece<FMT, F16>(s.w[t][n], affine_of<FMT>(s.w[t][n].m, min(u, U - 1)), i);
+          const u32x4 v = unit_piece<FMT, F16>(s.w[t][n], affine_of<FMT>(s.w[t][n].m, WHOLE ? u : min(u, U - 1)), i);
           const u32x4 a = in ? v : zero;
 #pragma unroll
           for (int j = 0; j < FM; ++j) acc[t][n][j] = mfma16<F16>(a, b[j], acc[t][n][j]);
         }
     }
   };
+  // only the last step can end inside
+  auto use = [&](const Set& s, int step) {
+    if (4 * step + 4 <= U) use_as.template operator()<true>(s, step);
+    else use_as.template operator()<false>(s, step);
+  };
   Set s0, s1;
   load(s0, wave);
-  load(s1, wave + W);
+  if (wave + W < nk) load(s1, wave + W);
   for (int st = wave; st < nk; st += 2 * W) {
     use(s0, st);
     if (st + 2 * W < nk) load(s0, st + 2 * W);
@@ -505,20 +510,25 @@ __global__ __launch_bounds__(64 * W) void glu_fwd_fewest_kernel(const GluFwdArgs
     for (int i = 0; i < 4; ++i) s.x[i] = load_at<u32x4>(xb, xrow + 64 * u + 16 * i);
   };
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  auto use = [&](const Set& s, int step) {
+  auto use_as = [&]<bool WHOLE>(const Set& s, int step) {
     const int u = 4 * step + g4;
-    const bool in = u < U;
+    const bool in = WHOLE || u < U;
     const u32x4 zero = {0, 0, 0, 0};
-    const Affine f = affine_of<FMT>(s.w.m, min(u, U - 1));
+    const Affine f = affine_of<FMT>(s.w.m, WHOLE ? u : min(u, U - 1));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const u32x4 v = unit_piece<FMT, F16>(s.w, f, i);
       acc = mfma16<F16>(in ? v : zero, in ? s.x[i] : zero, acc);
     }
   };
+  // only the last step can end inside
+  auto use = [&](const Set& s, int step) {
+    if (4 * step + 4 <= U) use_as.template operator()<true>(s, step);
+    else use_as.template operator()<false>(s, step);
+  };
   Set s0, s1;
   load(s0, wave);
-  load(s1, wave + W);
+  if (wave + W < nk) load(s1, wave + W);
   for (int st = wave; st < nk; st += 2 * W) {
     use(s0, st);
     if (st + 2 * W < nk) load(s0, st + 2 * W);
