@@ -55,11 +55,11 @@ constexpr int issued_after(int from, bool codes, int now) {
 // took 1.85 us for 0.92 us of MFMA).
 //
 // Bound by the matrix cores and what shares their issue slots.  W4A16, 5632 x
-// 2048: 8192 tokens with G and U kept take 365 - 370 us, 1.02 - 1.04 PFLOP/s (414
+// 2048: 8192 tokens with G and U kept take 365 - 394 us, 0.96 - 1.04 PFLOP/s (414
 // where call follows call for long and the clock falls; a dense bf16 library
 // product of the two matrices alone takes 393).  The MFMAs are busy 52 % of the
 // SIMDs' cycles at the 1.86 GHz that the card holds under this load, LDS 30 %; the
-// rest is the decoding (~20 VALU instructions per 8 weights), the barriers and
+// rest is the decoding (~24 VALU instructions per 8 weights), the barriers and
 // ~26 us of stores.  512 tokens take 32 - 36 us, 0.65 - 0.74 PFLOP/s: one round of
 // the chip, of which ~10 us is launch, first loads and epilogue.
 template <int FMT, bool F16, int RB, int TB, int WR, int WT, int KG>
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(64 * WR * WT * KG) void glu_fwd_kernel(const GluFwd
 // added in wave order.
 //
 // Bound by the latency of a chain that is only K / (128 W) steps long: Q4K,
-// 5632 x 2048, 16 tokens take 9.7 us for 13.2 MB (1.36 TB/s; a copy of that size
+// 5632 x 2048, 16 tokens take 9.7 us for 13.2 MB (1.37 TB/s; a copy of that size
 // at the card's 5.1 TB/s would take 2.6), of which ~3 us is the launch.
 template <int FMT, bool F16, int FM, int FN, int W>
 __global__ __launch_bounds__(64 * W) void glu_fwd_few_kernel(const GluFwdArgs p) {
@@ -559,11 +559,11 @@ __global__ __launch_bounds__(64 * W) void glu_fwd_fewest_kernel(const GluFwdArgs
 
 template <int FMT, bool F16>
 hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
-  // W4A16, K = 2048, us (N = 5632 / 1024): one token 7.7 / 4.4 with 8 + 8 rows per
-  // workgroup against 8.6 / 5.8 with 16 + 16 and 9.2 / 8.8 with 32 + 32; 16 tokens
-  // 11.2 / 5.6, 10.7 / 6.9 and 9.9 / 9.7; 64 tokens 18.7 with 32 + 32, 24 with
-  // 16 + 16.  More rows per workgroup read the tokens fewer times, fewer rows
-  // keep more workgroups at work.
+  // W4A16, K = 2048, us (N = 5632 / 1024): one token 7.6 / 4.3 with 8 + 8 rows per
+  // workgroup against 8.1 / 5.5 with 16 + 16 and 8.9 / 8.4 with 32 + 32; 16 tokens
+  // 11.3 / 5.5, 10.6 / 6.7 and 9.6 / 9.2; 64 tokens 18.5 / 17.6 with 32 + 32,
+  // 24.9 / 12.8 with 16 + 16.  More rows per workgroup read the tokens fewer times,
+  // fewer rows keep more workgroups at work.
   if (p.M <= 16 && int64_t(p.M) * p.N <= 24576) {
     hipLaunchKernelGGL((glu_fwd_fewest_kernel<FMT, F16, 8>), dim3((p.N + 7) / 8), dim3(512), 0, s, p);
     return hipGetLastError();
@@ -590,13 +590,13 @@ hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
   // one round (256 units, two 64 x 128 tiles to a unit), else the largest, which
   // decodes a weight once for the most tokens.  Us on W4A16, K = 2048, for tiles of
   // outputs x tokens:        64 x 64   64 x 128   64 x 256   128 x 256
-  //   N 5632,  128 tokens       21        26         33         46
-  //            256 tokens       32        27         34         46
-  //            512 tokens       50        40         36         49
-  //           1024 tokens       90        65         69         54
+  //   N 5632,  128 tokens       20        24         31         47
+  //            256 tokens       38        26         31         47
+  //            512 tokens       59        41         34         50
+  //           1024 tokens      113        73         68         56
   // The few-token kernel up to 256 groups, the 64 x 64 tile past them: Q4K, 1024 x
-  // 1024, 128 tokens (128 groups) 8.4 against 13.1; W4A16, 1333 x 768, 197 tokens
-  // (336) 12.8 against 10.8; 5632 x 2048, 128 tokens (704) 38 against 21.
+  // 1024, 128 tokens (128 groups) 7.9 against 11.0; W4A16, 1333 x 768, 197 tokens
+  // (336) 12.8 against 10.8; 5632 x 2048, 128 tokens (704) 38 against 20.
   // Two groups of waves from K = 1024 on (four runs): W4A16, 2048 wide, 256 tokens
   // 19.3 against 21.8 at K = 2048, 15.7 against 17.3 at 1536; 1333 wide, 197 tokens
   // 11.4 against 12.6 at 1024, 10.4 both at 768 (Q6K 14.1 against 13.3); 1300 wide,
