@@ -111,6 +111,11 @@ _lib.qmv_gemm_glu_backward.argtypes = [_int, _i64, _i64, _i64, _vp, _vp, _vp, _v
 _lib.qmv_gemm_glu_backward.restype = _int
 _lib.qmv_gemm_glu_backward_bytes.argtypes = [_int, _i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)]
 _lib.qmv_gemm_glu_backward_bytes.restype = _int
+_lib.qmv_gemm_glu_backward_ex.argtypes = [_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _vp, _vp,
+                                          _vp, _vp, ctypes.c_size_t, _vp]
+_lib.qmv_gemm_glu_backward_ex.restype = _int
+_lib.qmv_gemm_glu_backward_ex_bytes.argtypes = [_int, _i64, _i64, _i64, _int, ctypes.POINTER(ctypes.c_size_t)]
+_lib.qmv_gemm_glu_backward_ex_bytes.restype = _int
 
 
 class QmvRopeTensor(ctypes.Structure):
@@ -135,7 +140,8 @@ _lib.qmv_dequant.restype = _int
 EXPORTS = ("qmv_abi_version", "qmv_status_string", "qmv_last_error", "qmv_packed_bytes",
            "qmv_pack", "qmv_matvec", "qmv_matvec_ex", "qmv_matvec_swiglu", "qmv_matvec_grouped", "qmv_gemm",
            "qmv_dequant", "qmv_quantize_x", "qmv_q8x_bytes")
-LAYER_EXPORTS = ("qmv_gemm_glu", "qmv_gemm_glu_backward", "qmv_gemm_glu_backward_bytes", "qmv_rope", "qmv_rope_freqs")
+LAYER_EXPORTS = ("qmv_gemm_glu", "qmv_gemm_glu_backward", "qmv_gemm_glu_backward_bytes", "qmv_gemm_glu_backward_ex",
+                 "qmv_gemm_glu_backward_ex_bytes", "qmv_rope", "qmv_rope_freqs")
 
 
 class QmvError(RuntimeError):
@@ -394,6 +400,7 @@ def gemm(fmt, W: torch.Tensor, X: torch.Tensor, N: int, K: int, Y: torch.Tensor 
     return Y
 
 
+GLU_UNROUNDED = 1  # qmv_glu_flags
 ACTS = {"silu": 1, "gelu_tanh": 2, "gelu": 3}
 ROPE_LAYOUTS = {"half": 1, "interleaved": 2}
 ROPE_KINDS = {"linear": 1, "ntk": 2, "parts": 3}
@@ -482,10 +489,10 @@ def gemm_glu(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, X: torch.Tensor, N: 
     return H, G, U
 
 
-def gemm_glu_backward_bytes(fmt, N: int, K: int, M: int) -> int:
+def gemm_glu_backward_bytes(fmt, N: int, K: int, M: int, unrounded: bool = False) -> int:
     """Bytes of scratch memory that gemm_glu_backward needs for these sizes."""
     out = ctypes.c_size_t(0)
-    _check(_lib.qmv_gemm_glu_backward_bytes(_fmt(fmt), N, K, M, ctypes.byref(out)))
+    _check(_lib.qmv_gemm_glu_backward_ex_bytes(_fmt(fmt), N, K, M, GLU_UNROUNDED if unrounded else 0, ctypes.byref(out)))
     return out.value
 
 
@@ -495,14 +502,17 @@ _backward_bytes_cached = functools.lru_cache(maxsize=4096)(gemm_glu_backward_byt
 def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
                       dH: torch.Tensor, N: int, K: int, act="silu", dG: torch.Tensor | None = None,
                       dU: torch.Tensor | None = None, dX: torch.Tensor | None = None,
-                      workspace: torch.Tensor | None = None, stream=None):
+                      workspace: torch.Tensor | None = None, stream=None, unrounded: bool = False):
     """(dX [M][K], dG [M][N], dU [M][N]) of gemm_glu for the gradient dH [M][N] of H,
-    from its saved G and U; all of one dtype.  dG and dU may be given as two of
-    the buffers G, U and dH.  workspace: scratch memory of
-    gemm_glu_backward_bytes bytes, allocated when absent."""
+    from its saved G and U; all of one dtype.  dX is the sum over the returned
+    dG and dU, which are rounded to that type; with unrounded=True over their
+    values before that rounding, at twice the matrix operations and without its
+    error.  dG and dU may be given as two of the buffers G, U and dH.  workspace:
+    scratch memory of gemm_glu_backward_bytes bytes (of the same unrounded),
+    allocated when absent."""
     if stream is not None:  # what is allocated here belongs to that stream too
         with torch.cuda.stream(stream):
-            return gemm_glu_backward(fmt, W_gate, W_up, G, U, dH, N, K, act, dG, dU, dX, workspace)
+            return gemm_glu_backward(fmt, W_gate, W_up, G, U, dH, N, K, act, dG, dU, dX, workspace, None, unrounded)
     if G.dtype not in _DTYPES:
         raise ValueError("G dtype must be float32, float16 or bfloat16")
     shape, f, a = (G.shape[0], N), _fmt(fmt), _act(act)
@@ -514,14 +524,16 @@ def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Te
     nbytes = _packed_bytes_cached(f, N, K)
     wg, wu = _weight(W_gate, nbytes, device, "W_gate"), _weight(W_up, nbytes, device, "W_up")
     dG, dU, dX = _like(dG, G, shape, "dG"), _like(dU, G, shape, "dU"), _like(dX, G, (M, K), "dX")
-    nbytes = _backward_bytes_cached(f, N, K, M)
+    unrounded = bool(unrounded)
+    nbytes = _backward_bytes_cached(f, N, K, M, unrounded)
     ws = None
     if nbytes:
         if workspace is None:
             workspace = G.new_empty(nbytes, dtype=torch.uint8)
         ws = _weight(workspace, nbytes, device, "workspace")
-    _check(_lib.qmv_gemm_glu_backward(f, N, K, M, wg, wu, G.data_ptr(), U.data_ptr(), dH.data_ptr(),
-                                      _DTYPES[G.dtype], a, dG.data_ptr(), dU.data_ptr(), dX.data_ptr(), ws, nbytes, s))
+    _check(_lib.qmv_gemm_glu_backward_ex(f, N, K, M, wg, wu, G.data_ptr(), U.data_ptr(), dH.data_ptr(),
+                                         _DTYPES[G.dtype], a, GLU_UNROUNDED if unrounded else 0, dG.data_ptr(),
+                                         dU.data_ptr(), dX.data_ptr(), ws, nbytes, s))
     return dX, dG, dU
 
 

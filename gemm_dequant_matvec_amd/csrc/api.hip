@@ -375,26 +375,40 @@ int qmv_gemm_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, c
                   "gemm_glu");
 }
 
-static size_t glu_backward_bytes(int64_t N, int64_t K, int64_t M) {
-  const qmv::GluBwdPlan p = qmv::glu_backward_plan(N, K, M);
-  return size_t(p.part_bytes + 2 * p.copy_bytes);
+static size_t bytes_of(const qmv::GluBwdPlan& p) { return size_t(p.part_bytes + 2 * p.copy_bytes + 2 * p.low_bytes); }
+
+static int check_glu_flags(int flags) {
+  if (flags & ~QMV_GLU_UNROUNDED) return fail(QMV_ERR_UNSUPPORTED, "flags=%d holds an unknown flag", flags);
+  return QMV_OK;
 }
 
 int qmv_gemm_glu_backward_bytes(int fmt, int64_t N, int64_t K, int64_t M, size_t* out_bytes) {
+  return qmv_gemm_glu_backward_ex_bytes(fmt, N, K, M, 0, out_bytes);
+}
+
+int qmv_gemm_glu_backward_ex_bytes(int fmt, int64_t N, int64_t K, int64_t M, int flags, size_t* out_bytes) {
   int st;
   if ((st = check_fmt(fmt))) return st;
   if ((st = check_shape(fmt, N, K, M, "M"))) return st;
   if (!out_bytes) return fail(QMV_ERR_NULL, "out_bytes is NULL");
+  if ((st = check_glu_flags(flags))) return st;
   if ((st = check_glu_sizes(N, K, M))) return st;
-  *out_bytes = glu_backward_bytes(N, K, M);
+  *out_bytes = bytes_of(qmv::glu_backward_plan(N, K, M, flags & QMV_GLU_UNROUNDED));
   return ok();
 }
 
 int qmv_gemm_glu_backward(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up,
                           const void* G, const void* U, const void* dH, int dtype, int act, void* dG, void* dU,
                           void* dX, void* ws, size_t ws_bytes, void* stream) {
+  return qmv_gemm_glu_backward_ex(fmt, N, K, M, W_gate, W_up, G, U, dH, dtype, act, 0, dG, dU, dX, ws, ws_bytes, stream);
+}
+
+int qmv_gemm_glu_backward_ex(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up,
+                             const void* G, const void* U, const void* dH, int dtype, int act, int flags, void* dG,
+                             void* dU, void* dX, void* ws, size_t ws_bytes, void* stream) {
   int st;
   if ((st = check_glu(fmt, N, K, M, W_gate, W_up, dtype, "dtype", act))) return st;
+  if ((st = check_glu_flags(flags))) return st;
   const void* bufs[] = {G, U, dH, dG, dU, dX};
   const char* names[] = {"G", "U", "dH", "dG", "dU", "dX"};
   for (int i = 0; i < 6; ++i)
@@ -402,7 +416,8 @@ int qmv_gemm_glu_backward(int fmt, int64_t N, int64_t K, int64_t M, const void* 
   if (dG == dU) return fail(QMV_ERR_UNSUPPORTED, "dG and dU are the same buffer");
   for (int i = 0; i < 5; ++i)
     if (dX == bufs[i]) return fail(QMV_ERR_UNSUPPORTED, "dX is the buffer of %s", names[i]);
-  const size_t need = glu_backward_bytes(N, K, M);
+  const qmv::GluBwdPlan plan = qmv::glu_backward_plan(N, K, M, flags & QMV_GLU_UNROUNDED);
+  const size_t need = bytes_of(plan);
   if (need) {
     if ((st = check_buffer(ws, "ws"))) return st;
     if (ws_bytes < need)
@@ -413,8 +428,9 @@ int qmv_gemm_glu_backward(int fmt, int64_t N, int64_t K, int64_t M, const void* 
   return launched(qmv::launch_glu_bwd(fmt, N, K, M, static_cast<const uint8_t*>(W_gate),
                                       static_cast<const uint8_t*>(W_up), static_cast<const uint16_t*>(G),
                                       static_cast<const uint16_t*>(U), static_cast<const uint16_t*>(dH),
-                                      dtype == QMV_F16, act, static_cast<uint16_t*>(dG), static_cast<uint16_t*>(dU),
-                                      static_cast<uint16_t*>(dX), static_cast<uint8_t*>(ws), as_stream(stream)),
+                                      dtype == QMV_F16, act, plan, static_cast<uint16_t*>(dG),
+                                      static_cast<uint16_t*>(dU), static_cast<uint16_t*>(dX), static_cast<uint8_t*>(ws),
+                                      as_stream(stream)),
                   "gemm_glu_backward");
 }
 

@@ -18,9 +18,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight values: dG = dH U act'(G), dU = dH act(G).
-template <bool F16, int ACT>
-__device__ __forceinline__ void dgates8(u32x4 gv, u32x4 uv, u32x4 hv, u32x4& og, u32x4& ou) {
+// What rounding v (f32) to the 16-bit value `bits` left over, to be rounded to the
+// same type: with it, v is kept to 16 (bf16) or 22 (f16) bits, and where f16 ends, to
+// multiples of 2^-24.  Zero behind a value that is no longer finite: dX follows it.
+template <bool F16>
+__device__ __forceinline__ float left_over(float v, uint32_t bits) {
+  const float r = v - unpack16<F16>(bits & 0xFFFFu);
+  return fabsf(r) < __builtin_inff() ? r : 0.0f;
+}
+
+// Eight values: dG = dH U act'(G), dU = dH act(G); LOW: also the low parts of both.
+template <bool F16, int ACT, bool LOW>
+__device__ __forceinline__ void dgates8(u32x4 gv, u32x4 uv, u32x4 hv, u32x4& og, u32x4& ou, u32x4& lg, u32x4& lu) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float a[2], b[2];
@@ -35,6 +44,10 @@ __device__ __forceinline__ void dgates8(u32x4 gv, u32x4 uv, u32x4 hv, u32x4& og,
     }
     og[i] = pack16<F16>(a[0], a[1]);
     ou[i] = pack16<F16>(b[0], b[1]);
+    if constexpr (LOW) {
+      lg[i] = pack16<F16>(left_over<F16>(a[0], og[i]), left_over<F16>(a[1], og[i] >> 16));
+      lu[i] = pack16<F16>(left_over<F16>(b[0], ou[i]), left_over<F16>(b[1], ou[i] >> 16));
+    }
   }
 }
 
@@ -50,38 +63,50 @@ __device__ __forceinline__ void store_part(uint16_t* p, u32x4 v, int n) {
 // The elementwise half, n = M N values in all (a multiple of 8).  Each thread
 // reads its values before it writes them, so dG and dU may be any of the
 // inputs' buffers.  dG and dU are rounded to the 16-bit type here, once: they are
-// outputs of that type, and what the product takes.  Bound by memory, 5 x 2
-// bytes per value: 8192 x 5632 values take 68 us (6.8 TB/s; what was written last
-// is partly still in the 256 MB cache).
-template <bool F16, int ACT>
+// outputs of that type, and what the product takes; LOW: what the rounding left
+// over goes to clg and clu.  Bound by memory, 5 x 2 (LOW: 7 x 2) bytes per value:
+// 8192 x 5632 values take 68 us (6.8 TB/s; what was written last is partly still in
+// the 256 MB cache).
+template <bool F16, int ACT, bool LOW>
 __global__ __launch_bounds__(kThreads) void glu_dgates_kernel(const uint16_t* g, const uint16_t* u, const uint16_t* dh,
-                                                              uint16_t* dg, uint16_t* du, int64_t n) {
+                                                              uint16_t* dg, uint16_t* du, uint16_t* clg, uint16_t* clu,
+                                                              int64_t n) {
   const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8;
   if (at >= n) return;
-  u32x4 og, ou;
-  dgates8<F16, ACT>(*reinterpret_cast<const u32x4*>(g + at), *reinterpret_cast<const u32x4*>(u + at),
-                    *reinterpret_cast<const u32x4*>(dh + at), og, ou);
+  u32x4 og, ou, lg, lu;
+  dgates8<F16, ACT, LOW>(*reinterpret_cast<const u32x4*>(g + at), *reinterpret_cast<const u32x4*>(u + at),
+                         *reinterpret_cast<const u32x4*>(dh + at), og, ou, lg, lu);
   *reinterpret_cast<u32x4*>(dg + at) = og;
   *reinterpret_cast<u32x4*>(du + at) = ou;
+  if constexpr (LOW) {
+    *reinterpret_cast<u32x4*>(clg + at) = lg;
+    *reinterpret_cast<u32x4*>(clu + at) = lu;
+  }
 }
 
 // The same for rows that are no multiple of 8 long: dG and dU also go to copies
 // with rows of ld values, zeros behind the N-th, which the product reads (its
 // 16-byte pieces need the alignment).
-template <bool F16, int ACT>
+template <bool F16, int ACT, bool LOW>
 __global__ __launch_bounds__(kThreads) void glu_dgates_ragged_kernel(const uint16_t* g, const uint16_t* u,
                                                                      const uint16_t* dh, uint16_t* dg, uint16_t* du,
-                                                                     uint16_t* cg, uint16_t* cu, int64_t M, int N, int ld) {
+                                                                     uint16_t* cg, uint16_t* cu, uint16_t* clg,
+                                                                     uint16_t* clu, int64_t M, int N, int ld) {
   const int n = (blockIdx.y * kThreads + threadIdx.x) * 8, left = min(8, N - n);
   if (n >= ld) return;
   const bool whole = left == 8;
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
     const int64_t at = m * N + n;
-    u32x4 og, ou;
-    dgates8<F16, ACT>(whole ? load8(g + at) : load_part(g + at, left), whole ? load8(u + at) : load_part(u + at, left),
-                      whole ? load8(dh + at) : load_part(dh + at, left), og, ou);
+    u32x4 og, ou, lg, lu;
+    dgates8<F16, ACT, LOW>(whole ? load8(g + at) : load_part(g + at, left),
+                           whole ? load8(u + at) : load_part(u + at, left),
+                           whole ? load8(dh + at) : load_part(dh + at, left), og, ou, lg, lu);
     *reinterpret_cast<u32x4*>(cg + m * ld + n) = og;  // dh is zero behind the row, so og and ou are
     *reinterpret_cast<u32x4*>(cu + m * ld + n) = ou;
+    if constexpr (LOW) {
+      *reinterpret_cast<u32x4*>(clg + m * ld + n) = lg;
+      *reinterpret_cast<u32x4*>(clu + m * ld + n) = lu;
+    }
     if (whole) {
       __builtin_memcpy(dg + at, &og, 16);
       __builtin_memcpy(du + at, &ou, 16);
@@ -121,8 +146,12 @@ __global__ __launch_bounds__(kThreads) void glu_join_kernel(const float* part, u
 // and dense; 1 to 4096 tokens of 64 x 256 to 5632 x 2048): on average 1 % and at
 // most 12 % over the best cut of each size.  W4A16, 5632 x 2048: 512 tokens 57.9
 // with 128 x 128 and 8 splits against 63.5 with 256 x 256 and 16, 2048 tokens 140
-// with 256 x 256 and 4 against 177 with 128 x 128 and 2.
-GluBwdPlan glu_backward_plan(int64_t N, int64_t K, int64_t M) {
+// with 256 x 256 and 4 against 177 with 128 x 128 and 2.  The same cut serves the
+// form with low parts, whose best cuts are the same or next to it: W4A16, 5632 x
+// 2048, the rule's is the best measured one at 1, 24, 391, 512, 2048 and 8192 tokens
+// and 3 to 4 % over it at 64 and 128; over 36 sizes of four formats 4 % on average,
+// at most 19 % (Q8_0, 1024 x 768, 2048 tokens: 44.5 against 37.5).
+GluBwdPlan glu_backward_plan(int64_t N, int64_t K, int64_t M, bool wide) {
   struct Tile {
     int k, m, units;  // columns, tokens; workgroups that share a unit
     double stage[3], round;
@@ -145,11 +174,13 @@ GluBwdPlan glu_backward_plan(int64_t N, int64_t K, int64_t M) {
       if (splits > 1) us += 2.0 + double(splits) * double(M) * double(K) * 8e-6 * 0.13;
       if (best.tiles && us >= best_us) continue;
       best_us = us;
-      best = GluBwdPlan{t, int(splits), int(steps), 0, tiles, splits > 1 ? splits * M * K * 4 : 0, 0};
+      best = GluBwdPlan{t, int(splits), int(steps), 0, tiles, splits > 1 ? splits * M * K * 4 : 0, 0, 0};
     }
   }
   best.ld = int((N + 7) / 8 * 8);
-  if (N % 8) best.copy_bytes = (M * best.ld * 2 + 15) / 16 * 16;
+  const int64_t copy = M * best.ld * 2;  // a multiple of 16
+  if (N % 8) best.copy_bytes = copy;
+  if (wide) best.low_bytes = copy;
   return best;
 }
 
@@ -165,37 +196,44 @@ hipError_t launch_glu_fwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_
 }
 
 hipError_t launch_glu_bwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_t* Wg, const uint8_t* Wu,
-                          const uint16_t* G, const uint16_t* U, const uint16_t* dH, bool f16, int act, uint16_t* dG,
-                          uint16_t* dU, uint16_t* dX, uint8_t* ws, hipStream_t s) {
+                          const uint16_t* G, const uint16_t* U, const uint16_t* dH, bool f16, int act,
+                          const GluBwdPlan& plan, uint16_t* dG, uint16_t* dU, uint16_t* dX, uint8_t* ws, hipStream_t s) {
   const Planes pl = planes_of(fmt, N, K);
-  const GluBwdPlan plan = glu_backward_plan(N, K, M);
   const int64_t mn = M * N, mk = M * K;
-  uint16_t *cg = dG, *cu = dU;
+  uint16_t *cg = dG, *cu = dU, *clg = nullptr, *clu = nullptr;
+  uint8_t* at = ws + plan.part_bytes;
   if (plan.copy_bytes) {
-    cg = reinterpret_cast<uint16_t*>(ws + plan.part_bytes);
-    cu = reinterpret_cast<uint16_t*>(ws + plan.part_bytes + plan.copy_bytes);
+    cg = reinterpret_cast<uint16_t*>(at);
+    cu = reinterpret_cast<uint16_t*>(at + plan.copy_bytes);
+    at += 2 * plan.copy_bytes;
   }
-  auto gates = [&]<bool F16, int ACT>() {
+  if (plan.low_bytes) {
+    clg = reinterpret_cast<uint16_t*>(at);
+    clu = reinterpret_cast<uint16_t*>(at + plan.low_bytes);
+  }
+  auto gates = [&]<bool F16, int ACT, bool LOW>() {
     if (plan.copy_bytes) {
       const dim3 grid(unsigned(std::min<int64_t>(M, 1 << 20)), unsigned((plan.ld / 8 + kThreads - 1) / kThreads));
-      hipLaunchKernelGGL((glu_dgates_ragged_kernel<F16, ACT>), grid, dim3(kThreads), 0, s, G, U, dH, dG, dU, cg, cu,
-                         M, int(N), plan.ld);
+      hipLaunchKernelGGL((glu_dgates_ragged_kernel<F16, ACT, LOW>), grid, dim3(kThreads), 0, s, G, U, dH, dG, dU, cg,
+                         cu, clg, clu, M, int(N), plan.ld);
     } else {
       const dim3 grid(unsigned((mn + 8 * kThreads - 1) / (8 * kThreads)));
-      hipLaunchKernelGGL((glu_dgates_kernel<F16, ACT>), grid, dim3(kThreads), 0, s, G, U, dH, dG, dU, mn);
+      hipLaunchKernelGGL((glu_dgates_kernel<F16, ACT, LOW>), grid, dim3(kThreads), 0, s, G, U, dH, dG, dU, clg, clu,
+                         mn);
     }
   };
-  auto by_act = [&]<bool F16>() {
-    if (act == QMV_ACT_SILU) gates.template operator()<F16, QMV_ACT_SILU>();
-    else if (act == QMV_ACT_GELU_TANH) gates.template operator()<F16, QMV_ACT_GELU_TANH>();
-    else gates.template operator()<F16, QMV_ACT_GELU>();
+  auto by_act = [&]<bool F16, bool LOW>() {
+    if (act == QMV_ACT_SILU) gates.template operator()<F16, QMV_ACT_SILU, LOW>();
+    else if (act == QMV_ACT_GELU_TANH) gates.template operator()<F16, QMV_ACT_GELU_TANH, LOW>();
+    else gates.template operator()<F16, QMV_ACT_GELU, LOW>();
   };
-  if (f16) by_act.template operator()<true>();
-  else by_act.template operator()<false>();
+  if (plan.low_bytes) f16 ? by_act.template operator()<true, true>() : by_act.template operator()<false, true>();
+  else f16 ? by_act.template operator()<true, false>() : by_act.template operator()<false, false>();
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   float* part = plan.splits > 1 ? reinterpret_cast<float*>(ws) : nullptr;
-  const GluBwdArgs p{mat_of(Wg, pl), mat_of(Wu, pl), cg, cu, dX, part, int(M), int(N), int(K), plan.ld, plan.steps};
+  const GluBwdArgs p{mat_of(Wg, pl), mat_of(Wu, pl), cg, cu, clg, clu, dX, part, int(M), int(N), int(K), plan.ld,
+                     plan.steps};
   switch (fmt) {
     case QMV_W4A16_G64: case QMV_Q4K: case QMV_DENSE_BF16: e = launch_glu_bwd_a(fmt, f16, p, plan, s); break;
     case QMV_Q8_0: case QMV_Q6K: case QMV_I8_ROW: e = launch_glu_bwd_b(fmt, f16, p, plan, s); break;

@@ -10,6 +10,7 @@ namespace qmv {
 struct GluBwdArgs {
   Mat wg, wu;
   const uint16_t *dg, *du;  // [M][ld], ld a multiple of 8; zeros where n >= N
+  const uint16_t *dgl, *dul;  // WIDE: their low parts, laid out the same
   uint16_t* dx;
   float* part;              // [splits][M][K] partial sums, or null: one split, dx written
   int M, N, K, ld;
@@ -43,12 +44,15 @@ template <int FMT>
 constexpr int kHalfLoads = FMT == QMV_Q6K ? 4 : is_fifth(FMT) ? 3 : 2;
 
 // dX[m][k] = sum_n dG[m][n] W~g[n][k] + dU[m][n] W~u[n][k], one f32 accumulator
-// over both sums.  Its operands are dG and dU as they leave the call, rounded
-// once to the 16-bit type: the matrix cores take no wider ones, and two passes
-// over a high and a low part would double the MFMAs that bound the kernel.  The
-// relative error of dX is therefore about sqrt(2) of what rounding dX alone
-// gives (more where the terms of a sum cancel), as in a model that trains in
-// this type.
+// over both sums.  The matrix cores take 16-bit operands.  Without WIDE these are
+// dG and dU as they leave the call, rounded once: the relative error of dX is then
+// about sqrt(2) of what rounding dX alone gives (more where the terms of a sum
+// cancel), as in a model that trains in this type.  With WIDE a second token tile
+// per stage holds what that rounding left over, rounded to the same type (dgates8),
+// and is multiplied by the same weight fragments: twice the MFMAs, one decoding.
+// W4A16, 5632 x 2048, the whole call: 24 tokens 20 us against 17, 512 tokens 74
+// against 56, 8192 tokens 760 against 435 - 450 (there the large tile, at its
+// register limit, spills some 20 values).
 //
 // RB, TB: 32-column blocks of dX and 32-token blocks per wave; WR x WT waves.
 //
@@ -65,12 +69,13 @@ constexpr int kHalfLoads = FMT == QMV_Q6K ? 4 : is_fifth(FMT) ? 3 : 2;
 // matrices 290), MFMAs busy ~50 % of the SIMDs' cycles at 1.95 GHz.  The wider
 // tile decodes a weight for 256 tokens; few tokens split the depth over
 // workgroups instead (glu_backward_plan), as a stage's latency is then what counts.
-template <int FMT, bool F16, int RB, int TB, int WR, int WT>
+template <int FMT, bool F16, bool WIDE, int RB, int TB, int WR, int WT>
 __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs p) {
   constexpr int NT = 64 * WR * WT;
   constexpr int BR = 32 * RB * WR, BM = 32 * TB * WT;
   constexpr int XPT = BM * 4 / NT, APT = BR * 4 / NT;  // 16-byte pieces per thread and stage
   constexpr bool DIRECT = FMT == QMV_DENSE_BF16 && !F16;
+  constexpr int P = WIDE ? 2 : 1;  // token tiles per stage: high parts, low parts
   static_assert(2 * BR == NT && XPT * NT == BM * 4 && APT * NT == BR * 4);
 
   __shared__ u32x4 A0[BR * 4], A1[BR * 4], A2[BR * 4], A3[BR * 4];
@@ -153,24 +158,29 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
   // the buffer, which reads as zero.
   const uint8_t* gx = reinterpret_cast<const uint8_t*>(p.dg + int64_t(m0) * ld);
   const uint8_t* ux = reinterpret_cast<const uint8_t*>(p.du + int64_t(m0) * ld);
+  const uint8_t* gw = WIDE ? reinterpret_cast<const uint8_t*>(p.dgl + int64_t(m0) * ld) : nullptr;
+  const uint8_t* uw = WIDE ? reinterpret_cast<const uint8_t*>(p.dul + int64_t(m0) * ld) : nullptr;
   const int xc = (tid & 3) ^ ((tid >> 4) & 3);
   uint32_t xo[XPT];
 #pragma unroll
   for (int t = 0; t < XPT; ++t)
     xo[t] = uint32_t(min(m0 + t * (NT / 4) + (tid >> 2), p.M - 1) - m0) * uint32_t(2 * ld) + 16 * xc;
   struct XWalk {
-    const uint8_t* p;
+    const uint8_t *p, *l;
     int nb, t;
   };
-  auto copy_x = [&](XWalk& w, u32x4* X) {  // and on to the next stage
+  auto copy_x = [&]<int PART>(XWalk& w, u32x4* X) {  // and, behind a stage's last part, on to the next stage
     const bool in = w.t < end && w.nb + 8 * xc < ld;
-    const Buf b = buffer_of(scalar_base(w.p), 0x7FFFFFFF);
+    const Buf b = buffer_of(scalar_base(PART ? w.l : w.p), 0x7FFFFFFF);
 #pragma unroll
     for (int t = 0; t < XPT; ++t) copy_to_lds(b, in ? xo[t] : 0x80000000u, 0, X + t * NT + wave * 64);
-    w.t += 1;
-    const bool turn = w.t == NS;
-    w.nb = turn ? 0 : w.nb + 32;
-    w.p = turn ? ux : w.p + 64;
+    if constexpr (PART == P - 1) {
+      w.t += 1;
+      const bool turn = w.t == NS;
+      w.nb = turn ? 0 : w.nb + 32;
+      w.p = turn ? ux : w.p + 64;
+      if constexpr (WIDE) w.l = turn ? uw : w.l + 64;
+    }
   };
 
   f32x16 acc[RB][TB];
@@ -186,7 +196,7 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
   struct Frag {
     u32x4 a[RB], b[TB];
   };
-  auto read = [&](Frag& f, const u32x4* A, const u32x4* X, int s) {
+  auto read_a = [&](Frag& f, const u32x4* A, int s) {
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
       const int n = 16 * s + 8 * fh + bj;
@@ -194,6 +204,8 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
       const u32x2 hi = read_tr(A, 2 * rows_at<BR>(n + 4, wr * RB + i, bh, bc >> 1) + (bc & 1));
       f.a[i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
     }
+  };
+  auto read_b = [&](Frag& f, const u32x4* X, int s) {
 #pragma unroll
     for (int i = 0; i < TB; ++i) f.b[i] = X[tile32_at((wt * TB + i) * 32 + fr, 2 * s + fh)];
   };
@@ -210,7 +222,8 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
 
   HalfRaw<FMT> c[4];
   Walk walk = walk_from(first);
-  XWalk xwalk{first < NS ? gx + 64 * int64_t(first) : ux + 64 * int64_t(first - NS), 32 * (first < NS ? first : first - NS), first};
+  const int64_t x0 = 64 * int64_t(first < NS ? first : first - NS);
+  XWalk xwalk{(first < NS ? gx : ux) + x0, WIDE ? (first < NS ? gw : uw) + x0 : nullptr, int(x0 >> 1), first};
   auto copy_a_next = [&](u32x4* A) {
     copy_a(walk, A);
     advance(walk);
@@ -228,9 +241,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = load_next();
   }
-  copy_x(xwalk, X0);
-  copy_x(xwalk, X1);
-  copy_x(xwalk, X2);
+  copy_x.template operator()<0>(xwalk, X0);
+  copy_x.template operator()<1 % P>(xwalk, X1);
+  copy_x.template operator()<2 % P>(xwalk, X2);
   if constexpr (!DIRECT) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -243,35 +256,45 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   lds_barrier16();
   Frag f0, f1;
-  read(f0, A0, X0, 0);
+  read_a(f0, A0, 0);
+  read_b(f0, X0, 0);
 #pragma unroll 1
   for (int st = first; st < end; st += 4) {
     [&]<int... H>(std::integer_sequence<int, H...>) {
       (([&] {
-         const u32x4 *A = At.template operator()<H>(), *X = Xt.template operator()<H>();
-         const u32x4 *A1n = At.template operator()<H + 1>(), *X1n = Xt.template operator()<H + 1>();
-         u32x4* A2n = At.template operator()<H + 2>();
-         copy_x(xwalk, Xt.template operator()<H + 3>());
-         if constexpr (DIRECT) copy_a_next(At.template operator()<H + 3>());
+         // token tile H: part `part` of stage S; a stage's weight fragments serve both parts
+         constexpr int S = H / P, part = H % P;
+         u32x4* A2n = At.template operator()<S + 2>();
+         copy_x.template operator()<(H + 3) % P>(xwalk, Xt.template operator()<H + 3>());
+         if constexpr (DIRECT && part == 0) {
+           if constexpr (WIDE) fence();  // the wait below counts on this order
+           copy_a_next(At.template operator()<S + 3>());
+         }
          fence();
-         read(f1, A, X, 1);
-         if constexpr (!DIRECT) decode(c[(H + 2) & 3], 0, A2n);
+         if constexpr (part == 0) read_a(f1, At.template operator()<S>(), 1);
+         read_b(f1, Xt.template operator()<H>(), 1);
+         if constexpr (!DIRECT && part == 0) decode(c[(S + 2) & 3], 0, A2n);
          mul(f0);
          fence();
-         read(f0, A1n, X1n, 0);
-         if constexpr (!DIRECT) {
-           decode(c[(H + 2) & 3], 1, A2n);
-           c[(H + 2) & 3] = load_next();
+         if constexpr (part == P - 1) read_a(f0, At.template operator()<S + 1>(), 0);
+         read_b(f0, Xt.template operator()<H + 1>(), 0);
+         if constexpr (!DIRECT && part == P - 1) {
+           decode(c[(S + 2) & 3], 1, A2n);
+           c[(S + 2) & 3] = load_next();
          }
          mul(f1);
          fence();
-         // Stage H + 2 is whole once the copies of the stage before this one have
-         // landed; certainly issued after those: two stages' loads and this stage's copies.
-         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(DIRECT ? XPT + APT : XPT + 2 * kHalfLoads<FMT>) : "memory");
+         // The next tile reads token tile H + 2 and, where it ends a stage, the weights of
+         // the stage after its own.  Those tokens were copied in the tile before this one,
+         // the weights in it or earlier.  Certainly issued after them: this tile's copies of
+         // tokens and, of these two tiles, one (WIDE) or two stages' loads of codes; with
+         // copied weights those of one stage, in this tile or behind the tokens of the last.
+         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(DIRECT ? XPT + APT : XPT + (WIDE ? 1 : 2) * kHalfLoads<FMT>)
+                      : "memory");
          lds_barrier16();
        }()),
        ...);
-    }(std::make_integer_sequence<int, 4>{});
+    }(std::make_integer_sequence<int, 4 * P>{});
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the copies past the end
   lds_barrier16();
@@ -322,16 +345,21 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
     }
 }
 
-template <int FMT, bool F16>
-hipError_t glu_bwd_go(const GluBwdArgs& p, const GluBwdPlan& plan, hipStream_t s) {
+template <int FMT, bool F16, bool WIDE>
+hipError_t glu_bwd_start(const GluBwdArgs& p, const GluBwdPlan& plan, hipStream_t s) {
   const dim3 grid(unsigned(plan.tiles), unsigned(plan.splits));
   if (plan.tile == 2)
-    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, 4, 2, 2, 4>), grid, dim3(512), 0, s, p);
+    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, WIDE, 4, 2, 2, 4>), grid, dim3(512), 0, s, p);
   else if (plan.tile == 1)
-    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, 2, 2, 2, 2>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, WIDE, 2, 2, 2, 2>), grid, dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, 2, 1, 2, 2>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((glu_bwd_kernel<FMT, F16, WIDE, 2, 1, 2, 2>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
+}
+
+template <int FMT, bool F16>
+hipError_t glu_bwd_go(const GluBwdArgs& p, const GluBwdPlan& plan, hipStream_t s) {
+  return plan.low_bytes ? glu_bwd_start<FMT, F16, true>(p, plan, s) : glu_bwd_start<FMT, F16, false>(p, plan, s);
 }
 
 }  // namespace

@@ -63,7 +63,8 @@ int qmv_gemm_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, c
  * The backward pass of qmv_gemm_glu for a gradient dH of H:
  *   dG = dH * U * act'(G),  dU = dH * act(G)         (f32, each rounded once to dtype)
  *   dX[m][k] = sum_n dG[m][n] W~g[n][k] + dU[m][n] W~u[n][k]
- * with the rounded dG and dU and W~ as above; sums are f32, dX is rounded once.
+ * with the rounded dG and dU and W~ as above (qmv_gemm_glu_backward_ex also takes them
+ * unrounded); sums are f32, dX is rounded once.
  * The packed weights are constants (codes have no gradient); dG and dU are
  * what trainable matrices beside them (adapters) take their gradients from.
  *   G, U, dH, dG, dU   [M][N] of dtype (QMV_BF16 or QMV_F16), device, 16-byte aligned
@@ -81,6 +82,27 @@ int qmv_gemm_glu_backward(int fmt, int64_t N, int64_t K, int64_t M, const void* 
 /* Bytes of scratch memory that qmv_gemm_glu_backward needs for these sizes
  * (0: none).  Host only.  Errors: FORMAT, SHAPE, NULL, OVERFLOW. */
 int qmv_gemm_glu_backward_bytes(int fmt, int64_t N, int64_t K, int64_t M, size_t* out_bytes);
+
+/* What qmv_gemm_glu_backward_ex does otherwise than qmv_gemm_glu_backward. */
+enum qmv_glu_flags {
+  /* dX is the sum over dG and dU as they are before their rounding to dtype:
+   * each enters the product as two 16-bit parts, the rounded value and what the
+   * rounding left over (16 bits of it in bf16, 22 in f16, there down to multiples
+   * of 2^-24).  dX is then off by its own rounding, where the sum over the rounded
+   * dG and dU is off by about sqrt(2) of that, and by more where its terms cancel.
+   * It takes twice the matrix operations.  Where dG or dU is past the type's
+   * largest value, dX is infinite or NaN with it, and where W~ is infinite, dX of
+   * that column is infinite or NaN. */
+  QMV_GLU_UNROUNDED = 1
+};
+
+/* qmv_gemm_glu_backward with a set of qmv_glu_flags (0: the same call), and the
+ * bytes of scratch memory that it needs with them.  dG and dU are the same with
+ * any flags.  Errors: as the calls without _ex; UNSUPPORTED also for an unknown flag. */
+int qmv_gemm_glu_backward_ex(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up,
+                             const void* G, const void* U, const void* dH, int dtype, int act, int flags, void* dG,
+                             void* dU, void* dX, void* ws, size_t ws_bytes, void* stream);
+int qmv_gemm_glu_backward_ex_bytes(int fmt, int64_t N, int64_t K, int64_t M, int flags, size_t* out_bytes);
 
 /* One tensor of qmv_rope: T tokens of `heads` heads of D values; strides in
  * elements (values of a head are adjacent). */
