@@ -309,7 +309,9 @@ def _run_own(c):
             H, G, U = qmv.gemm_glu(c["fmt"], c["Wg"], c["Wu"], c["X"], c["N"], c["K"], act=c["act"], save=True)
             return {"H": H, "G": G, "U": U}
         return {"H": qmv.gemm_glu(c["fmt"], c["Wg"], c["Wu"], c["X"], c["N"], c["K"], act=c["act"])}
-    dX, dG, dU = qmv.gemm_glu_backward(c["fmt"], c["Wg"], c["Wu"], c["G"], c["U"], c["dH"], c["N"], c["K"], act=c["act"])
+    # both reference forms sum dX over dG and dU as they are before their rounding
+    dX, dG, dU = qmv.gemm_glu_backward(c["fmt"], c["Wg"], c["Wu"], c["G"], c["U"], c["dH"], c["N"], c["K"], act=c["act"],
+                                       unrounded=True)
     return {"dX": dX, "dG": dG, "dU": dU}
 
 
