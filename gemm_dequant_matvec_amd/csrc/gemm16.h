@@ -411,6 +411,20 @@ __device__ __forceinline__ HalfRaw<FMT> load_half(const Mat& w, const RowAt<FMT>
   return x;
 }
 
+// Makes the weights of r zeros unless `keep`: with a scale of zero every format
+// gives zeros, whatever its codes.
+template <int FMT>
+__device__ __forceinline__ void keep_weights(HalfRaw<FMT>& r, bool keep) {
+  if constexpr (FMT == QMV_DENSE_BF16) {
+    const u32x4 zero = {0, 0, 0, 0};
+    r.q[0] = keep ? r.q[0] : zero;
+    r.q[1] = keep ? r.q[1] : zero;
+  } else {
+    constexpr int i = FMT == QMV_Q6K ? 1 : 0;  // the factor of all others
+    r.m.v[i] = keep ? r.m.v[i] : 0u;
+  }
+}
+
 // Word w of unit u as one 16-byte piece; its codes are the i-th of r.
 template <int FMT, bool F16>
 __device__ __forceinline__ u32x4 word_piece(const HalfRaw<FMT>& r, int u, int w, int i) {

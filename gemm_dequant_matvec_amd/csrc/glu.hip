@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kThreads) void glu_join_kernel(const float* part, u
 // with 256 x 256 and 4 against 177 with 128 x 128 and 2.  The same cut serves the
 // form with low parts, whose best cuts are the same or next to it: W4A16, 5632 x
 // 2048, the rule's is the best measured one at 1, 24, 391, 512, 2048 and 8192 tokens
-// and 3 to 4 % over it at 64 and 128; over 36 sizes of four formats 4 % on average,
+// and 3 to 4 % over it at 64 and 128; over 36 sizes of four formats 2 % on average,
 // at most 19 % (Q8_0, 1024 x 768, 2048 tokens: 44.5 against 37.5).
 GluBwdPlan glu_backward_plan(int64_t N, int64_t K, int64_t M, bool wide) {
   struct Tile {

@@ -134,6 +134,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
     for (int i = 0; i < kPlanes<FMT>; ++i) r.o[i] = nl <= int(lastrow) ? nl_at.o[i] : lastrow * row_bytes<FMT>(i, K);
     return load_half<FMT, kByUnit>(w.m, r, u, half);
   };
+  // Rows past N and stages past the end meet zero tokens, but an infinite weight
+  // (f16: past 65504) times zero would be a NaN: their weights are zeros too.
+  auto rows_of = [&](int t) { return t < end ? N - 32 * (t < NS ? t : t - NS) : 0; };
   auto decode = [&](const HalfRaw<FMT>& c, int i, u32x4* A) {
     A[rows_at<BR>(nl, ul, half, i)] = word_piece<FMT, F16>(c, u, 2 * half + i, i);
   };
@@ -147,11 +150,12 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
     ao[t] = 64 * unit + 32 * ((s >> 1) & 1) + 16 * ((s & 1) ^ ((n >> 2) & 1));
     an[t] = n;
   }
-  auto copy_a = [&](const Walk& w, u32x4* A) {
-    const Buf b = buffer_of(scalar_base(w.m.p[0]));
+  auto copy_a = [&](const Walk& w, int stage, u32x4* A) {  // an offset past the buffer reads as zero
+    const Buf b = buffer_of(scalar_base(w.m.p[0]), 0x7FFFFFFF);
+    const int rows = rows_of(stage);
 #pragma unroll
     for (int t = 0; t < APT; ++t)
-      copy_to_lds(b, uint32_t(min(an[t], N - 1 - w.nb)) * uint32_t(2 * K) + ao[t], 0, A + t * NT + wave * 64);
+      copy_to_lds(b, an[t] < rows ? uint32_t(an[t]) * uint32_t(2 * K) + ao[t] : 0x80000000u, 0, A + t * NT + wave * 64);
   };
   // Tokens: LDS slot tid + t * NT of a tile is row (tid + t * NT) / 4.  Pieces past
   // the row, and all pieces of a stage past the split's end, get an offset past
@@ -224,8 +228,8 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
   Walk walk = walk_from(first);
   const int64_t x0 = 64 * int64_t(first < NS ? first : first - NS);
   XWalk xwalk{(first < NS ? gx : ux) + x0, WIDE ? (first < NS ? gw : uw) + x0 : nullptr, int(x0 >> 1), first};
-  auto copy_a_next = [&](u32x4* A) {
-    copy_a(walk, A);
+  auto copy_a_next = [&](int stage, u32x4* A) {
+    copy_a(walk, stage, A);
     advance(walk);
   };
   auto load_next = [&] {
@@ -234,9 +238,9 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
     return r;
   };
   if constexpr (DIRECT) {
-    copy_a_next(A0);
-    copy_a_next(A1);
-    copy_a_next(A2);
+    copy_a_next(first, A0);
+    copy_a_next(first + 1, A1);
+    copy_a_next(first + 2, A2);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = load_next();
@@ -245,6 +249,8 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
   copy_x.template operator()<1 % P>(xwalk, X1);
   copy_x.template operator()<2 % P>(xwalk, X2);
   if constexpr (!DIRECT) {
+    keep_weights(c[0], nl < rows_of(first));
+    keep_weights(c[1], nl < rows_of(first + 1));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       decode(c[0], i, A0);
@@ -268,12 +274,15 @@ __global__ __launch_bounds__(64 * WR * WT) void glu_bwd_kernel(const GluBwdArgs 
          copy_x.template operator()<(H + 3) % P>(xwalk, Xt.template operator()<H + 3>());
          if constexpr (DIRECT && part == 0) {
            if constexpr (WIDE) fence();  // the wait below counts on this order
-           copy_a_next(At.template operator()<S + 3>());
+           copy_a_next(st + S + 3, At.template operator()<S + 3>());
          }
          fence();
          if constexpr (part == 0) read_a(f1, At.template operator()<S>(), 1);
          read_b(f1, Xt.template operator()<H>(), 1);
-         if constexpr (!DIRECT && part == 0) decode(c[(S + 2) & 3], 0, A2n);
+         if constexpr (!DIRECT && part == 0) {
+           keep_weights(c[(S + 2) & 3], nl < rows_of(st + S + 2));
+           decode(c[(S + 2) & 3], 0, A2n);
+         }
          mul(f0);
          fence();
          if constexpr (part == P - 1) read_a(f0, At.template operator()<S + 1>(), 0);
