@@ -12,10 +12,11 @@
 // 32768 tokens: 81 us, 4.95 TB/s (a copy of 1 GiB runs at 5.1); bf16, 36 heads of
 // 64, 4096 tokens: 8.7 us, 4.3 TB/s; one token 2.8 us, the launch.
 //
-// The angle of a far position needs more than f32: pos * freq is formed in f64,
-// turned into revolutions, reduced to an eighth of a turn there and only then
-// rounded to f32, where sin and cos are the Taylor polynomials (degree 11 and
-// 10: truncation below 1e-9 on [-pi/4, pi/4]).
+// The angle of a far position needs more than f64 gives to a product: pos * freq
+// has 31 + 24 bits.  It is kept as a rounded product and what the rounding left
+// over, turned into revolutions by a 1 / (2 pi) of two parts, and reduced to an
+// eighth of a turn, all in f64, and only then rounded to f32, where sin and cos are
+// the Taylor polynomials (degree 11 and 10: truncation below 1e-9 on [-pi/4, pi/4]).
 #include <algorithm>
 #include <cmath>
 
@@ -43,8 +44,13 @@ struct RopeArgs {
 };
 
 __device__ __forceinline__ void turn(int64_t pos, float freq, float& c, float& s) {
-  const double rev = double(pos) * double(freq) * 0.15915494309189535;  // 1 / (2 pi)
-  const double r = rev - rint(rev);                                      // [-1/2, 1/2]
+#pragma clang fp contract(off)  // a product must be rounded where its rest is taken
+  const double a = double(pos), f = double(freq);
+  const double t = a * f, t_low = fma(a, f, -t);  // a f = t + t_low
+  constexpr double kInv = 0.15915494309189535, kInvLow = -9.839338337591243e-18;  // 1 / (2 pi)
+  const double rev = t * kInv;
+  const double low = fma(t, kInv, -rev) + fma(t, kInvLow, t_low * kInv);
+  const double r = (rev - rint(rev)) + low;  // [-1/2, 1/2], off by less than 2^-52
   const double q = rint(4.0 * r);
   const float y = float((r - 0.25 * q) * 6.283185307179586);             // [-pi/4, pi/4]
   const float z = y * y;
