@@ -15,8 +15,12 @@
 // The angle of a far position needs more than f64 gives to a product: pos * freq
 // has 31 + 24 bits.  It is kept as a rounded product and what the rounding left
 // over, turned into revolutions by a 1 / (2 pi) of two parts, and reduced to an
-// eighth of a turn, all in f64, and only then rounded to f32, where sin and cos are
-// the Taylor polynomials (degree 11 and 10: truncation below 1e-9 on [-pi/4, pi/4]).
+// eighth of a turn, all in f64.  For f32 heads sin and cos are Taylor polynomials in
+// f64 (degree 13 and 12: truncation below 1e-12 on [-pi/4, pi/4]), and what a pair is
+// multiplied by, amplitude included, is rounded to f32 once.  For 16-bit heads the
+// reduced angle is rounded to f32 and the polynomials are f32 (degree 11 and 10,
+// below 1e-9): 2^-22 against the 2^-12 of their own rounding, and the f64 ones take
+// longer than the bytes there (4096 tokens 11.0 against 8.9 us, bf16).
 #include <algorithm>
 #include <cmath>
 
@@ -43,7 +47,9 @@ struct RopeArgs {
   float amplitude, sign;
 };
 
-__device__ __forceinline__ void turn(int64_t pos, float freq, float& c, float& s) {
+// amplitude cos(pos freq) and amplitude sin(pos freq); WIDE: rounded to f32 once.
+template <bool WIDE>
+__device__ __forceinline__ void turn(int64_t pos, float freq, float amplitude, float& c, float& s) {
 #pragma clang fp contract(off)  // a product must be rounded where its rest is taken
   const double a = double(pos), f = double(freq);
   const double t = a * f, t_low = fma(a, f, -t);  // a f = t + t_low
@@ -52,13 +58,33 @@ __device__ __forceinline__ void turn(int64_t pos, float freq, float& c, float& s
   const double low = fma(t, kInv, -rev) + fma(t, kInvLow, t_low * kInv);
   const double r = (rev - rint(rev)) + low;  // [-1/2, 1/2], off by less than 2^-52
   const double q = rint(4.0 * r);
-  const float y = float((r - 0.25 * q) * 6.283185307179586);             // [-pi/4, pi/4]
-  const float z = y * y;
-  const float sp = y * fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.50521084e-8f, 2.75573192e-6f), -1.98412698e-4f),
-                                            8.33333333e-3f), -1.66666667e-1f), 1.0f);
-  const float cp = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.75573192e-7f, 2.48015873e-5f), -1.38888889e-3f),
-                                        4.16666667e-2f), -0.5f), 1.0f);
+  const double y = (r - 0.25 * q) * 6.283185307179586;  // [-pi/4, pi/4]
   const int n = int(q) & 3;  // quarter turns
+  float sp, cp;
+  if constexpr (WIDE) {
+    const double z = y * y;
+    double sd = 1.0 / 6227020800, cd = 1.0 / 479001600;  // 1 / 13!, 1 / 12!
+    sd = fma(z, sd, -1.0 / 39916800);
+    cd = fma(z, cd, -1.0 / 3628800);
+    sd = fma(z, sd, 1.0 / 362880);
+    cd = fma(z, cd, 1.0 / 40320);
+    sd = fma(z, sd, -1.0 / 5040);
+    cd = fma(z, cd, -1.0 / 720);
+    sd = fma(z, sd, 1.0 / 120);
+    cd = fma(z, cd, 1.0 / 24);
+    sd = fma(z, sd, -1.0 / 6);
+    cd = fma(z, cd, -1.0 / 2);
+    sp = float(amplitude * (y * fma(z, sd, 1.0)));
+    cp = float(amplitude * fma(z, cd, 1.0));
+  } else {
+    const float yf = float(y), z = yf * yf;
+    sp = yf * fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.50521084e-8f, 2.75573192e-6f), -1.98412698e-4f),
+                                   8.33333333e-3f), -1.66666667e-1f), 1.0f);
+    cp = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.75573192e-7f, 2.48015873e-5f), -1.38888889e-3f),
+                              4.16666667e-2f), -0.5f), 1.0f);
+    sp *= amplitude;
+    cp *= amplitude;
+  }
   c = n == 0 ? cp : n == 1 ? -sp : n == 2 ? -cp : sp;
   s = n == 0 ? sp : n == 1 ? cp : n == 2 ? -sp : -cp;
 }
@@ -127,8 +153,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs p) {
     for (int i = tid; i < nt * P; i += kThreads) {
       const int t = i / P, f = i - t * P;
       float c, s;
-      turn(p.pos[t0 + t], p.freqs[f], c, s);
-      cs[i] = make_float2(p.amplitude * c, p.sign * p.amplitude * s);
+      turn<E == 0>(p.pos[t0 + t], p.freqs[f], p.amplitude, c, s);
+      cs[i] = make_float2(c, p.sign * s);
     }
     __syncthreads();
 
