@@ -430,6 +430,16 @@ def _on_current_device(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _no_gradient(what: str, *tensors) -> None:
+    """The calls below record nothing for autograd: a result of tensors that want a
+    gradient would lose it without a word."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{what} records no gradient, and a tensor passed to it requires one: call it under "
+                                 "torch.no_grad() or in an autograd function, or pass it detached")
+
+
 def _weight(W: torch.Tensor, nbytes: int, device: int, what: str) -> int:
     """Pointer of a packed matrix."""
     if W.nbytes < nbytes:
@@ -463,10 +473,13 @@ def gemm_glu(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, X: torch.Tensor, N: 
 
     act: "silu", "gelu_tanh" or "gelu".  With save=True (or G and U given) the
     two products are kept for gemm_glu_backward and (H, G, U) is returned.
+    Nothing is recorded for autograd: where gradients are enabled, tensors that
+    require one are refused (here and in the two functions below).
     """
     if stream is not None:  # what is allocated here belongs to that stream too
         with torch.cuda.stream(stream):
             return gemm_glu(fmt, W_gate, W_up, X, N, K, act, H, G, U, save)
+    _no_gradient("gemm_glu", X, H, G, U)
     if X.dim() != 2 or X.shape[1] != K:
         raise ValueError(f"X has shape {tuple(X.shape)}, expected [M][{K}]")
     if X.dtype not in _DTYPES:
@@ -513,6 +526,7 @@ def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Te
     if stream is not None:  # what is allocated here belongs to that stream too
         with torch.cuda.stream(stream):
             return gemm_glu_backward(fmt, W_gate, W_up, G, U, dH, N, K, act, dG, dU, dX, workspace, None, unrounded)
+    _no_gradient("gemm_glu_backward", G, U, dH, dG, dU, dX)
     if G.dtype not in _DTYPES:
         raise ValueError("G dtype must be float32, float16 or bfloat16")
     shape, f, a = (G.shape[0], N), _fmt(fmt), _act(act)
@@ -589,6 +603,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torc
     if stream is not None:  # what is allocated here belongs to that stream too
         with torch.cuda.stream(stream):
             return rope(q, k, pos, freqs, layout, amplitude, inverse, q_out, k_out)
+    _no_gradient("rope", q, k, freqs, q_out, k_out)
     if layout in ROPE_LAYOUTS:
         layout = ROPE_LAYOUTS[layout]
     elif isinstance(layout, str):
