@@ -440,6 +440,15 @@ def _no_gradient(what: str, *tensors) -> None:
                                  "torch.no_grad() or in an autograd function, or pass it detached")
 
 
+def _written(*tensors) -> None:
+    """Tells autograd that the caller's own tensors were written to, as torch's
+    in-place operations do: a backward pass that saved one of them then refuses to
+    run on the new values."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _weight(W: torch.Tensor, nbytes: int, device: int, what: str) -> int:
     """Pointer of a packed matrix."""
     if W.nbytes < nbytes:
@@ -492,13 +501,16 @@ def gemm_glu(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, X: torch.Tensor, N: 
     wg, wu = _weight(W_gate, nbytes, device, "W_gate"), _weight(W_up, nbytes, device, "W_up")
     if not X.is_contiguous():
         raise ValueError("tensors passed to libqmv must be contiguous")
+    given = H, G, U
     H = _like(H, X, shape, "H")
     if not save and G is None:
         _check(_lib.qmv_gemm_glu(f, N, K, shape[0], wg, wu, X.data_ptr(), dt, a, H.data_ptr(), dt, None, None, s))
+        _written(*given)
         return H
     G, U = _like(G, X, shape, "G"), _like(U, X, shape, "U")
     _check(_lib.qmv_gemm_glu(f, N, K, shape[0], wg, wu, X.data_ptr(), dt, a, H.data_ptr(), dt, G.data_ptr(),
                              U.data_ptr(), s))
+    _written(*given)
     return H, G, U
 
 
@@ -537,6 +549,7 @@ def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Te
     s, device = _on_current_device(G), G.get_device()
     nbytes = _packed_bytes_cached(f, N, K)
     wg, wu = _weight(W_gate, nbytes, device, "W_gate"), _weight(W_up, nbytes, device, "W_up")
+    given = dG, dU, dX, workspace
     dG, dU, dX = _like(dG, G, shape, "dG"), _like(dU, G, shape, "dU"), _like(dX, G, (M, K), "dX")
     unrounded = bool(unrounded)
     nbytes = _backward_bytes_cached(f, N, K, M, unrounded)
@@ -548,6 +561,7 @@ def gemm_glu_backward(fmt, W_gate: torch.Tensor, W_up: torch.Tensor, G: torch.Te
     _check(_lib.qmv_gemm_glu_backward_ex(f, N, K, M, wg, wu, G.data_ptr(), U.data_ptr(), dH.data_ptr(),
                                          _DTYPES[G.dtype], a, GLU_UNROUNDED if unrounded else 0, dG.data_ptr(),
                                          dU.data_ptr(), dX.data_ptr(), ws, nbytes, s))
+    _written(*given)
     return dX, dG, dU
 
 
@@ -624,6 +638,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torc
         raise ValueError("q, k, pos and freqs must be on one device")
     if not (pos.is_contiguous() and freqs.is_contiguous()):
         raise ValueError("tensors passed to libqmv must be contiguous")
+    given = q_out, k_out
     q_out = _rope_out(q, q_out, "q")
     fields = _rope_fields(q, q_out, "q")
     if k is not None:
@@ -632,6 +647,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torc
     _check(_lib.qmv_rope(T, D, 2 * freqs.numel(), layout, len(fields) // 7, _RopeFields[len(fields)].pack(*fields),
                          _DTYPES[q.dtype],
                          pos.data_ptr(), freqs.data_ptr(), amplitude, inverse, s))
+    _written(*given)
     return q_out, None if k is None else k_out
 
 
