@@ -467,6 +467,14 @@ int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_r
     if (t.heads >= lim) return fail(QMV_ERR_OVERFLOW, "tensors[%d].heads too large", i);
     heads += t.heads;
   }
+  // one launch turns all tensors, in no order
+  for (int i = 0; i < count; ++i)
+    for (int j = 0; j < count; ++j) {
+      if (i < j && tensors[i].y == tensors[j].y)
+        return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].y and tensors[%d].y are one buffer", i, j);
+      if (i != j && tensors[i].y == tensors[j].x)
+        return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].y is the buffer of tensors[%d].x", i, j);
+    }
   // a block of tokens is indexed with 32-bit ints, the grid counts tokens
   if (D > (lim >> 3) || heads > (lim >> 3) / D || T >= lim)
     return fail(QMV_ERR_OVERFLOW, "T is past 2^31 or heads * D past 2^28");

@@ -109,7 +109,8 @@ int qmv_gemm_glu_backward_ex_bytes(int fmt, int64_t N, int64_t K, int64_t M, int
 #define QMV_ROPE_MAX 4
 typedef struct qmv_rope_tensor {
   const void* x;
-  void* y;          /* output; x itself with the same strides (in place), or no overlap with any x */
+  void* y;          /* output; x itself with the same strides (in place), or no overlap with any x;
+                       no overlap with another y */
   int64_t heads;
   int64_t x_token, x_head;
   int64_t y_token, y_head;
@@ -129,7 +130,8 @@ typedef struct qmv_rope_tensor {
  *   T < 2^31, the tensors' heads together times D <= 2^28
  *   dtype     QMV_F32, QMV_F16 or QMV_BF16, of every x and y, aligned to its element
  *   pos       int64 [T], freqs f32 [R/2] (device)
- * Errors: SHAPE, NULL, ALIGN, DTYPE, UNSUPPORTED (Q8X), OVERFLOW, DEVICE, LAUNCH.
+ * Errors: SHAPE, NULL, ALIGN, DTYPE, UNSUPPORTED (Q8X, unknown layout, in place with other
+ * strides, a y that is another tensor's x or y), OVERFLOW, DEVICE, LAUNCH.
  */
 int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_rope_tensor* tensors, int dtype,
              const int64_t* pos, const float* freqs, float amplitude, int inverse, void* stream);
