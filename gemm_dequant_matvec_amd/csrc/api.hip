@@ -9,8 +9,10 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "layer_internal.h"
 
@@ -478,6 +480,16 @@ int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_r
   // a block of tokens is indexed with 32-bit ints, the grid counts tokens
   if (D > (lim >> 3) || heads > (lim >> 3) / D || T >= lim)
     return fail(QMV_ERR_OVERFLOW, "T is past 2^31 or heads * D past 2^28");
+  for (int i = 0; i < count; ++i) {  // tokens and heads of an output: the larger stride passes what the smaller one reaches
+    const qmv_rope_tensor& t = tensors[i];
+    struct Axis {
+      int64_t n, st;
+    } in{t.heads, std::llabs(t.y_head)}, out{T, std::llabs(t.y_token)};
+    if (in.n > 1 && out.n > 1 && in.st > out.st) std::swap(in, out);
+    if (in.n > 1 && in.st < D) return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].y holds some values more than once", i);
+    const int64_t reach = in.n > 1 ? (in.n - 1) * in.st + D : D;
+    if (out.n > 1 && out.st < reach) return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].y holds some values more than once", i);
+  }
   if ((st = check_device())) return st;
   return launched(qmv::launch_rope(T, int(D), int(R), layout, count, tensors, dtype, pos, freqs, amplitude, inverse,
                                    as_stream(stream)),

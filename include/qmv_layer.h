@@ -110,7 +110,7 @@ int qmv_gemm_glu_backward_ex_bytes(int fmt, int64_t N, int64_t K, int64_t M, int
 typedef struct qmv_rope_tensor {
   const void* x;
   void* y;          /* output; x itself with the same strides (in place), or no overlap with any x;
-                       no overlap with another y */
+                       no overlap with another y, nor of its own values */
   int64_t heads;
   int64_t x_token, x_head;
   int64_t y_token, y_head;
@@ -131,7 +131,7 @@ typedef struct qmv_rope_tensor {
  *   dtype     QMV_F32, QMV_F16 or QMV_BF16, of every x and y, aligned to its element
  *   pos       int64 [T], freqs f32 [R/2] (device)
  * Errors: SHAPE, NULL, ALIGN, DTYPE, UNSUPPORTED (Q8X, unknown layout, in place with other
- * strides, a y that is another tensor's x or y), OVERFLOW, DEVICE, LAUNCH.
+ * strides, a y that is another tensor's x or y or holds values twice), OVERFLOW, DEVICE, LAUNCH.
  */
 int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_rope_tensor* tensors, int dtype,
              const int64_t* pos, const float* freqs, float amplitude, int inverse, void* stream);
