@@ -631,6 +631,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torc
     _need_dtype(freqs, torch.float32, "freqs")
     if pos.numel() != T:
         raise ValueError(f"pos holds {pos.numel()} positions, q {T} tokens")
+    if k is None and k_out is not None:
+        raise ValueError("k_out is given without k")
     if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype != q.dtype):
         raise ValueError(f"k has shape {tuple(k.shape)} and {k.dtype}, expected [{T}][heads][{D}] and {q.dtype}")
     s, device = _on_current_device(q), q.get_device()
