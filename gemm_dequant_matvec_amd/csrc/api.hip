@@ -509,11 +509,15 @@ int qmv_rope_freqs(int64_t R, double base, const qmv_rope_scaling* scaling, floa
     if (c.kind == QMV_ROPE_NTK) {
       if (R < 4) return fail(QMV_ERR_SHAPE, "R=%lld must be >= 4 for QMV_ROPE_NTK", (long long)R);
       base *= std::pow(c.factor, double(R) / double(R - 2));
+      if (!std::isfinite(base)) return fail(QMV_ERR_UNSUPPORTED, "base stretched by scaling->factor is not finite");
     }
     if (c.kind == QMV_ROPE_PARTS &&
         !(std::isfinite(c.original) && c.original > 0 && std::isfinite(c.low) && std::isfinite(c.high) && c.low < c.high))
       return fail(QMV_ERR_UNSUPPORTED, "scaling->original must be > 0 and low < high, all finite");
   }
+  // the frequencies run from 1 to this one
+  if (!(std::pow(base, -2.0 * double(R / 2 - 1) / double(R)) <= 3.4028234663852886e38))
+    return fail(QMV_ERR_UNSUPPORTED, "base=%g gives frequencies past the f32 range", base);
   for (int64_t i = 0; i < R / 2; ++i) {
     double f = std::pow(base, -2.0 * double(i) / double(R));
     if (scaling && scaling->kind == QMV_ROPE_LINEAR) f /= scaling->factor;

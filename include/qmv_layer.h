@@ -151,8 +151,8 @@ typedef struct qmv_rope_scaling {
 /*
  * freqs[i] = base^(-2i / R), i < R/2, stretched by `scaling` (NULL: not), as
  * f32 into host memory.  Host only; computed in f64 and rounded once.
- * Errors: SHAPE (R odd, < 2 or > 4096; NTK: R < 4), NULL, UNSUPPORTED (kind, or a parameter
- * that is not finite or out of its range).
+ * Errors: SHAPE (R odd, < 2 or > 4096; NTK: R < 4), NULL, UNSUPPORTED (kind, a parameter that is
+ * not finite or out of its range, or a frequency that f32 does not hold).
  */
 int qmv_rope_freqs(int64_t R, double base, const qmv_rope_scaling* scaling, float* freqs);
 
