@@ -356,6 +356,21 @@ static int check_buffer(const void* p, const char* name) {
   return QMV_OK;
 }
 
+// Bytes [p, p + bytes) of a call's buffers.
+struct Range {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+};
+
+// The workgroups of a launch read and write in no order: what one writes, none may read or write elsewhere.
+static int check_apart(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  if (x < y + uintptr_t(b.bytes) && y < x + uintptr_t(a.bytes))
+    return fail(QMV_ERR_UNSUPPORTED, "%s overlaps %s", a.name, b.name);
+  return QMV_OK;
+}
+
 int qmv_gemm_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up, const void* X,
                  int x_dtype, int act, void* H, int h_dtype, void* G, void* U, void* stream) {
   int st;
@@ -369,6 +384,12 @@ int qmv_gemm_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, c
   if (G && ((st = check_buffer(G, "G")) || (st = check_buffer(U, "U")))) return st;
   if (H == X || G == X || U == X) return fail(QMV_ERR_UNSUPPORTED, "an output is the buffer of X");
   if (G && (G == H || U == H || G == U)) return fail(QMV_ERR_UNSUPPORTED, "two of H, G and U are one buffer");
+  const Range rx{X, 2 * M * K, "X"}, out[] = {{H, 2 * M * N, "H"}, {G, 2 * M * N, "G"}, {U, 2 * M * N, "U"}};
+  for (int i = 0; i < (G ? 3 : 1); ++i) {
+    if ((st = check_apart(out[i], rx))) return st;
+    for (int j = 0; j < i; ++j)
+      if ((st = check_apart(out[i], out[j]))) return st;
+  }
   if ((st = check_device())) return st;
   return launched(qmv::launch_glu_fwd(fmt, N, K, M, static_cast<const uint8_t*>(W_gate),
                                       static_cast<const uint8_t*>(W_up), static_cast<const uint16_t*>(X),
@@ -426,6 +447,12 @@ int qmv_gemm_glu_backward_ex(int fmt, int64_t N, int64_t K, int64_t M, const voi
       return fail(QMV_ERR_SHAPE, "ws_bytes=%llu, the call needs %llu", (unsigned long long)ws_bytes,
                   (unsigned long long)need);
   }
+  Range r[7];
+  for (int i = 0; i < 6; ++i) r[i] = Range{bufs[i], 2 * M * (i == 5 ? K : N), names[i]};
+  r[6] = Range{ws, int64_t(need), "ws"};
+  for (int i = 3; i < (need ? 7 : 6); ++i)  // dG and dU may be G, U or dH, as a whole
+    for (int j = 0; j < i; ++j)
+      if (!(i < 5 && j < 3 && r[i].p == r[j].p) && (st = check_apart(r[i], r[j]))) return st;
   if ((st = check_device())) return st;
   return launched(qmv::launch_glu_bwd(fmt, N, K, M, static_cast<const uint8_t*>(W_gate),
                                       static_cast<const uint8_t*>(W_up), static_cast<const uint16_t*>(G),

@@ -54,7 +54,7 @@ enum qmv_rope_kind {
  * the call.  Within a row the result does not depend
  * on the other rows' values, and calls repeat bit for bit.
  * Errors: FORMAT, SHAPE, NULL, ALIGN, DTYPE, UNSUPPORTED (x_dtype f32 / Q8X, h_dtype other than
- * x_dtype, unknown act, one buffer given twice), OVERFLOW, DEVICE, LAUNCH.
+ * x_dtype, unknown act, buffers that overlap), OVERFLOW, DEVICE, LAUNCH.
  */
 int qmv_gemm_glu(int fmt, int64_t N, int64_t K, int64_t M, const void* W_gate, const void* W_up, const void* X,
                  int x_dtype, int act, void* H, int h_dtype, void* G, void* U, void* stream);
