@@ -559,18 +559,25 @@ __global__ __launch_bounds__(64 * W) void glu_fwd_fewest_kernel(const GluFwdArgs
 
 template <int FMT, bool F16>
 hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
-  // W4A16, K = 2048, us (N = 5632 / 1024): one token 7.6 / 4.3 with 8 + 8 rows per
-  // workgroup against 8.1 / 5.5 with 16 + 16 and 8.9 / 8.4 with 32 + 32; 16 tokens
-  // 11.3 / 5.5, 10.6 / 6.7 and 9.6 / 9.2; 64 tokens 18.5 / 17.6 with 32 + 32,
-  // 24.9 / 12.8 with 16 + 16.  More rows per workgroup read the tokens fewer times,
-  // fewer rows keep more workgroups at work.
+  // More rows per workgroup read the tokens fewer times, fewer rows keep more
+  // workgroups at work: 16 + 16 rows as long as these are one round of the chip (256
+  // units), 32 + 32 past it.  W4A16, K = 2048, us with 8 + 8 / 16 + 16 / 32 + 32 rows:
+  //   N            2048             4096             5632             8192
+  //    1 token   4.4  5.6  8.1    5.7  5.7  8.2    7.5  7.8  8.3    8.8  7.9  8.3
+  //   16 tokens  5.6  6.7  9.3    8.4  6.9  9.4   11.0 10.3  9.4   13.6 10.5  9.5
+  //   32 tokens       8.6 11.2         8.7 11.3        15.2 11.4        15.2 11.5
+  //   64 tokens      12.6 17.6        12.8 17.6        24.1 17.9        24.2 18.2
+  // Q6K at N = 4096, 16 and 64 tokens, 8.3 and 14.2 with 16 + 16 against 12.0 and 20.2.
+  // Over 320 sizes of five formats (N 2048 to 14336, 1 to 64 tokens) the choice is 5 %
+  // over the best on average; worst where 64 x 64 tiles would do better, 33 to 64
+  // tokens of very wide matrices (14336 x 4096, 64 tokens: 56 against 33).
   if (p.M <= 16 && int64_t(p.M) * p.N <= 24576) {
     hipLaunchKernelGGL((glu_fwd_fewest_kernel<FMT, F16, 8>), dim3((p.N + 7) / 8), dim3(512), 0, s, p);
     return hipGetLastError();
   }
   const int64_t blocks = (p.M + 63) / 64, few = int64_t((p.N + 15) / 16) * blocks;
   if (p.M <= 64 || few <= 256) {
-    const bool wide = p.M <= 64 && p.N >= 4096;
+    const bool wide = p.M <= 64 && p.N > 4096;
     const dim3 grid(unsigned(wide ? (p.N + 31) / 32 : (p.N + 15) / 16), unsigned(blocks));
     if (p.M <= 16 && wide)
       hipLaunchKernelGGL((glu_fwd_few_kernel<FMT, F16, 1, 2, 8>), grid, dim3(512), 0, s, p);
@@ -594,6 +601,8 @@ hipError_t glu_fwd_go(const GluFwdArgs& p, hipStream_t s) {
   //            256 tokens       38        26         31         47
   //            512 tokens       59        41         34         50
   //           1024 tokens      113        73         68         56
+  // Over 315 sizes of seven formats (N 1333 to 14336, 96 to 2048 tokens) 0.5 % over the
+  // best tile on average, at most 12 % (Q6K, 14336 x 4096, 768 tokens: 238 against 212).
   // The few-token kernel up to 256 groups, the 64 x 64 tile past them: Q4K, 1024 x
   // 1024, 128 tokens (128 groups) 7.9 against 11.0; W4A16, 1333 x 768, 197 tokens
   // (336) 12.8 against 10.8; 5632 x 2048, 128 tokens (704) 38 against 20.

@@ -7,7 +7,7 @@ def forward_variant(M, N, K):
         return "fewest"
     blocks = -(-M // 64)
     if M <= 64 or -(-N // 16) * blocks <= 256:
-        wide = 2 if M <= 64 and N >= 4096 else 1
+        wide = 2 if M <= 64 and N > 4096 else 1
         return "few", 1 if M <= 16 else 2 if M <= 32 else 4, wide
 
     def tiles(bn, bm):

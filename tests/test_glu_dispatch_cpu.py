@@ -24,3 +24,9 @@ def test_loops():
                 groups = v[1] if v[0] == "64x64" else 1
                 assert K // 256 >= 3 * groups - 1  # runs of each group: two and three, or three and more
                 assert K // 32 % 8 or wl.BLOCK[fmt] == 256
+
+
+def test_one_round_of_the_chip():
+    """16 + 16 rows to a workgroup up to 256 workgroups, 32 + 32 past them."""
+    for M, m in ((16, 1), (20, 2), (64, 4)):
+        assert forward_variant(M, 4096, 2048) == ("few", m, 1) and forward_variant(M, 4097, 2048) == ("few", m, 2)
