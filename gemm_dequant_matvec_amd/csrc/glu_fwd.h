@@ -52,16 +52,21 @@ constexpr int issued_after(int from, bool codes, int now) {
 // workgroup, two stages ahead.  The first fragments of a stage are read before
 // the barrier that ends the stage before it, so no wave waits for LDS behind a
 // barrier (with 64-deep steps in two buffers, all read after the barrier, a step
-// took 1.85 us for 0.92 us of MFMA).
+// took 1.85 us for 0.92 us of MFMA).  Dense weights fill a tile of codes per stage:
+// they are copied in the stage before the one that reads them, every stage ends
+// with a wait for all copies, and nothing stays in flight over a barrier (512 tokens
+// 41 us against W4A16's 35, 8192 tokens 408 against 366).
 //
 // Bound by the matrix cores and what shares their issue slots.  W4A16, 5632 x
 // 2048: 8192 tokens with G and U kept take 365 - 394 us, 0.96 - 1.04 PFLOP/s (414
 // where call follows call for long and the clock falls; a dense bf16 library
 // product of the two matrices alone takes 393).  The MFMAs are busy 52 % of the
 // SIMDs' cycles at the 1.86 GHz that the card holds under this load, LDS 30 %; the
-// rest is the decoding (~24 VALU instructions per 8 weights), the barriers and
-// ~26 us of stores.  512 tokens take 32 - 36 us, 0.65 - 0.74 PFLOP/s: one round of
-// the chip, of which ~10 us is launch, first loads and epilogue.
+// rest is the decoding (~24 VALU instructions per 8 weights), the barriers,
+// ~26 us of stores, and units without work: 1408 tiles are 5.5 rounds of 256 units
+// (busy 0.85 - 0.87 of the time).  512 tokens take 31 - 36 us, 0.65 - 0.77 PFLOP/s:
+// 176 tiles, 0.69 of one round (units busy 0.50 of the time), and ~10 us of launch,
+// first loads and epilogue.
 template <int FMT, bool F16, int RB, int TB, int WR, int WT, int KG>
 __global__ __launch_bounds__(64 * WR * WT * KG) void glu_fwd_kernel(const GluFwdArgs p) {
   constexpr int NT = 64 * WR * WT;      // threads of a group
