@@ -41,7 +41,8 @@ enum qmv_rope_kind {
  *   H[m][n] = act(g) * u,  g = sum_k X[m][k] W~g[n][k],  u = sum_k X[m][k] W~u[n][k]
  * for m < M, n < N.  W~ is the dequantized weight rounded once, to nearest
  * even, to x_dtype: the matrix cores take both operands in one 16-bit type
- * (QMV_F16: a weight past 65504 becomes an infinity).  Sums and the activation
+ * (QMV_F16: a weight past 65504 becomes an infinity; the packed scales themselves
+ * are finite, and below 2^120 in QMV_I8_ROW).  Sums and the activation
  * are f32; every output is rounded once.
  *   fmt      any format; W_gate and W_up packed matrices of one shape
  *   X        [M][K] of x_dtype QMV_BF16 or QMV_F16, device, 16-byte aligned
