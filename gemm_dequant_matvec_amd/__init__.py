@@ -408,6 +408,11 @@ ROPE_KINDS = {"linear": 1, "ntk": 2, "parts": 3}
 # The many-token operators below are called once or twice per layer, for single
 # tokens too: their checks are kept to attribute reads (sizes are cached, the
 # stream comes as a raw handle), a few microseconds per call.
+#
+# stream= runs a call there, like every call's: the caller has that stream wait for
+# the work that fills the tensors, and keeps the tensors, or tells the allocator
+# (Tensor.record_stream), until it is done.  What a call allocates itself belongs to
+# that stream.
 _packed_bytes_cached = functools.lru_cache(maxsize=4096)(packed_bytes)
 
 

@@ -66,7 +66,7 @@ __device__ __forceinline__ void store_part(uint16_t* p, u32x4 v, int n) {
 // outputs of that type, and what the product takes; LOW: what the rounding left
 // over goes to clg and clu.  Bound by memory, 5 x 2 (LOW: 7 x 2) bytes per value:
 // 8192 x 5632 values take 68 us (6.8 TB/s; what was written last is partly still in
-// the 256 MB cache).
+// the 256 MB cache), LOW 98 us.
 template <bool F16, int ACT, bool LOW>
 __global__ __launch_bounds__(kThreads) void glu_dgates_kernel(const uint16_t* g, const uint16_t* u, const uint16_t* dh,
                                                               uint16_t* dg, uint16_t* du, uint16_t* clg, uint16_t* clu,
@@ -150,7 +150,10 @@ __global__ __launch_bounds__(kThreads) void glu_join_kernel(const float* part, u
 // form with low parts, whose best cuts are the same or next to it: W4A16, 5632 x
 // 2048, the rule's is the best measured one at 1, 24, 391, 512, 2048 and 8192 tokens
 // and 3 to 4 % over it at 64 and 128; over 36 sizes of four formats 2 % on average,
-// at most 19 % (Q8_0, 1024 x 768, 2048 tokens: 44.5 against 37.5).
+// at most 19 % (Q8_0, 1024 x 768, 2048 tokens: 44.5 against 37.5).  Past the fitted
+// sizes, 14336 x 4096 (W4A16, Q4K) and 8192 x 2816 (Q6K) with 1 to 4096 tokens, the cut
+// is the best measured one at all 24 sizes; with low parts 4 % over it on average, at
+// most 23 % (Q6K, 1024 tokens: 330 against 268 with 128 x 128, as the large tile spills).
 GluBwdPlan glu_backward_plan(int64_t N, int64_t K, int64_t M, bool wide) {
   struct Tile {
     int k, m, units;  // columns, tokens; workgroups that share a unit

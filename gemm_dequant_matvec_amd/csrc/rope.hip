@@ -10,7 +10,7 @@
 // heads, so that its threads have several 16-byte pieces each and the sines are
 // not the longer part, but no more than leave 512 blocks.  f16, 24 heads of 128,
 // 32768 tokens: 81 us, 4.95 TB/s (a copy of 1 GiB runs at 5.1); bf16, 36 heads of
-// 64, 4096 tokens: 8.7 us, 4.3 TB/s; one token 2.8 us, the launch.
+// 64, 4096 tokens: 8.8 us, 4.3 TB/s; one token (f32) 3.0 us, the launch.
 //
 // The angle of a far position needs more than f64 gives to a product: pos * freq
 // has 31 + 24 bits.  It is kept as a rounded product and what the rounding left
