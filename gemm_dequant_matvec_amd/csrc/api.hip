@@ -507,7 +507,8 @@ int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_r
   // a block of tokens is indexed with 32-bit ints, the grid counts tokens
   if (D > (lim >> 3) || heads > (lim >> 3) / D || T >= lim)
     return fail(QMV_ERR_OVERFLOW, "T is past 2^31 or heads * D past 2^28");
-  for (int i = 0; i < count; ++i) {  // tokens and heads of an output: the larger stride passes what the smaller one reaches
+  // tokens and heads of an output: the larger stride passes what the smaller one reaches
+  for (int i = 0; i < count; ++i) {
     const qmv_rope_tensor& t = tensors[i];
     struct Axis {
       int64_t n, st;

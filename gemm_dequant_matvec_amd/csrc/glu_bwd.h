@@ -27,7 +27,8 @@ namespace {
 // pieces of a pair by n / 4 % 2, which by the banks keeps apart both these reads
 // (four rows of one unit) and the decoders' writes (rows n and n + 4 of 8 half
 // units).  Conflicts are counted all the same, not traced to one of them: 0.74
-// cycles per LDS instruction (8192 tokens, W4A16; 0.63 with low parts).  In 16-byte pieces: row n, unit ul of the tile, half h, piece i.
+// cycles per LDS instruction (8192 tokens, W4A16; 0.63 with low parts).
+// In 16-byte pieces: row n, unit ul of the tile, half h, piece i.
 template <int BR>
 __device__ __forceinline__ int rows_at(int n, int ul, int h, int i) {
   return n * (BR / 8) + (ul ^ (n & 3)) * 4 + 2 * h + (i ^ ((n >> 2) & 1));
