@@ -13,6 +13,7 @@ Importing this package fails loudly when the library has not been built
     H, G, U = qmv.gemm_glu("q4k", Wg, Wu, X, N, K, act="silu", save=True)   # act(X Wg^T) * (X Wu^T)
     dX, dG, dU = qmv.gemm_glu_backward("q4k", Wg, Wu, G, U, dH, N, K, act="silu")
     q, k = qmv.rope(q, k, pos, qmv.rope_freqs(R))   # q [T][heads][D], k [T][kv_heads][D]
+    q, k = qmv.norm_rope(q, k, q_weight, k_weight, pos, qmv.rope_freqs(R))   # the heads' norms in the same pass
 """
 from __future__ import annotations
 
@@ -134,6 +135,14 @@ _lib.qmv_rope.argtypes = [_i64, _i64, _i64, _int, _int, _vp, _int, _vp, _vp, cty
 _lib.qmv_rope.restype = _int
 _lib.qmv_rope_freqs.argtypes = [_i64, ctypes.c_double, ctypes.POINTER(QmvRopeScaling), ctypes.POINTER(ctypes.c_float)]
 _lib.qmv_rope_freqs.restype = _int
+_lib.qmv_norm_rope.argtypes = [_i64, _i64, _i64, _int, _int, _vp, _int, _int, ctypes.c_float, ctypes.c_float, _vp, _vp,
+                               ctypes.c_float, _vp]
+_lib.qmv_norm_rope.restype = _int
+_lib.qmv_norm_rope_backward.argtypes = [_i64, _i64, _i64, _int, _int, _vp, _int, _int, ctypes.c_float, ctypes.c_float, _vp,
+                                        _vp, ctypes.c_float, _vp, ctypes.c_size_t, _vp]
+_lib.qmv_norm_rope_backward.restype = _int
+_lib.qmv_norm_rope_backward_bytes.argtypes = [_i64, _i64, _int, ctypes.POINTER(_i64), ctypes.POINTER(ctypes.c_size_t)]
+_lib.qmv_norm_rope_backward_bytes.restype = _int
 _lib.qmv_dequant.argtypes = [_int, _i64, _i64, _vp, _vp, _vp]
 _lib.qmv_dequant.restype = _int
 
@@ -141,7 +150,8 @@ EXPORTS = ("qmv_abi_version", "qmv_status_string", "qmv_last_error", "qmv_packed
            "qmv_pack", "qmv_matvec", "qmv_matvec_ex", "qmv_matvec_swiglu", "qmv_matvec_grouped", "qmv_gemm",
            "qmv_dequant", "qmv_quantize_x", "qmv_q8x_bytes")
 LAYER_EXPORTS = ("qmv_gemm_glu", "qmv_gemm_glu_backward", "qmv_gemm_glu_backward_bytes", "qmv_gemm_glu_backward_ex",
-                 "qmv_gemm_glu_backward_ex_bytes", "qmv_rope", "qmv_rope_freqs")
+                 "qmv_gemm_glu_backward_ex_bytes", "qmv_rope", "qmv_rope_freqs", "qmv_norm_rope", "qmv_norm_rope_backward",
+                 "qmv_norm_rope_backward_bytes")
 
 
 class QmvError(RuntimeError):
@@ -589,13 +599,14 @@ def rope_freqs(R: int, base: float = 10000.0, scaling: str | None = None, factor
 _RopeFields = {7: struct.Struct("7q"), 14: struct.Struct("14q")}  # qmv_rope_tensor: seven 8-byte fields
 
 
-def _rope_out(x: torch.Tensor, y: torch.Tensor | None, what: str) -> torch.Tensor:
+def _rope_out(x: torch.Tensor, y: torch.Tensor | None, what: str, name: str | None = None) -> torch.Tensor:
+    """The output `name` (what_out) for x, called `what`."""
     if y is None:
         return torch.empty_like(x)
     if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != x.get_device():
-        raise ValueError(f"{what}_out must have {what}'s shape, dtype and device")
+        raise ValueError(f"{name or what + '_out'} must have {what}'s shape, dtype and device")
     if any(n > 1 and st == 0 for n, st in zip(y.shape, y.stride())):
-        raise ValueError(f"{what}_out holds some values more than once")
+        raise ValueError(f"{name or what + '_out'} holds some values more than once")
     return y
 
 
@@ -656,6 +667,154 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, freqs: torc
                          pos.data_ptr(), freqs.data_ptr(), amplitude, inverse, s))
     _written(*given)
     return q_out, None if k is None else k_out
+
+
+def _norm_rope_arguments(q, k, q_weight, k_weight, pos, freqs, layout):
+    """Checks that norm_rope and its backward pass share: (layout, w_dtype code, stream)."""
+    if layout in ROPE_LAYOUTS:
+        layout = ROPE_LAYOUTS[layout]
+    elif isinstance(layout, str):
+        raise ValueError(f"unknown layout {layout!r}; one of {sorted(ROPE_LAYOUTS)}")
+    if q.dim() != 3:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [T][heads][D]")
+    T, _, D = q.shape
+    if q.dtype not in _DTYPES:
+        raise ValueError("q dtype must be float32, float16 or bfloat16")
+    _need_dtype(pos, torch.int64, "pos")
+    _need_dtype(freqs, torch.float32, "freqs")
+    if pos.numel() != T:
+        raise ValueError(f"pos holds {pos.numel()} positions, q {T} tokens")
+    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype != q.dtype):
+        raise ValueError(f"k has shape {tuple(k.shape)} and {k.dtype}, expected [{T}][heads][{D}] and {q.dtype}")
+    if k is None and k_weight is not None:
+        raise ValueError("k_weight is given without k")
+    s, device = _on_current_device(q), q.get_device()
+    if pos.get_device() != device or freqs.get_device() != device or (k is not None and k.get_device() != device):
+        raise ValueError("q, k, pos and freqs must be on one device")
+    if not (pos.is_contiguous() and freqs.is_contiguous()):
+        raise ValueError("tensors passed to libqmv must be contiguous")
+    w_dtype = None
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            continue
+        if w.dim() != 1 or w.shape[0] != D:
+            raise ValueError(f"{what} has shape {tuple(w.shape)}, expected ({D},)")
+        if w.dtype != q.dtype and w.dtype != torch.float32:
+            raise ValueError(f"{what} must be float32 or {q.dtype}, got {w.dtype}")
+        if w_dtype is not None and w.dtype != w_dtype:
+            raise ValueError("q_weight and k_weight must have one dtype")
+        w_dtype = w.dtype
+        if w.get_device() != device:
+            raise ValueError(f"{what} is on {w.device}, the call's tensors on device {device}")
+        if not w.is_contiguous():
+            raise ValueError("tensors passed to libqmv must be contiguous")
+    return layout, _DTYPES[w_dtype or q.dtype], s
+
+
+def _head_strides(x: torch.Tensor, what: str) -> tuple:
+    t, h, d = x.stride()
+    if d != 1 and x.shape[2] > 1:
+        raise ValueError(f"the values of a head of {what} must be adjacent")
+    return t, h
+
+
+_NormFields = {8: struct.Struct("8q"), 16: struct.Struct("16q"),  # qmv_norm_rope_tensor: eight 8-byte fields
+               12: struct.Struct("12q"), 24: struct.Struct("24q")}  # qmv_norm_rope_grad: twelve
+
+
+def norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+              pos: torch.Tensor, freqs: torch.Tensor, eps: float = 1e-6, layout="half", amplitude: float = 1.0,
+              weight_offset: float = 0.0, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """The norm of every head of q [T][heads][D] and k [T][kv_heads][D] (or None) and
+    its rotary position, in one pass; returns (q_out, k_out).
+
+    Over a head's D <= 1024 values x: x / sqrt(mean(x^2) + eps) * (weight +
+    weight_offset), then the rotation as in rope.  q_weight and k_weight [D] are
+    f32 or of q's dtype (one for both); None: 1.  q and k may be strided, and
+    q_out=q, k_out=k works in place.
+    """
+    if stream is not None:  # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return norm_rope(q, k, q_weight, k_weight, pos, freqs, eps, layout, amplitude, weight_offset, q_out, k_out)
+    _no_gradient("norm_rope", q, k, q_weight, k_weight, freqs, q_out, k_out)
+    if k is None and k_out is not None:
+        raise ValueError("k_out is given without k")
+    layout, w_dtype, s = _norm_rope_arguments(q, k, q_weight, k_weight, pos, freqs, layout)
+    given = q_out, k_out
+    fields = ()
+    outs = []
+    for x, w, y, what in ((q, q_weight, q_out, "q"), (k, k_weight, k_out, "k")):
+        if x is None:
+            outs.append(None)
+            continue
+        y = _rope_out(x, y, what)
+        outs.append(y)
+        fields += (x.data_ptr(), y.data_ptr(), w.data_ptr() if w is not None else 0, x.shape[1],
+                   *_head_strides(x, what), *_head_strides(y, what + "_out"))
+    _check(_lib.qmv_norm_rope(q.shape[0], q.shape[2], 2 * freqs.numel(), layout, len(fields) // 8,
+                              _NormFields[len(fields)].pack(*fields), _DTYPES[q.dtype], w_dtype, eps, weight_offset,
+                              pos.data_ptr(), freqs.data_ptr(), amplitude, s))
+    _written(*given)
+    return tuple(outs)
+
+
+@functools.lru_cache(maxsize=4096)
+def norm_rope_backward_bytes(T: int, D: int, *heads: int) -> int:
+    """Bytes of scratch memory that norm_rope_backward needs for T tokens of these heads (q, or q and k)."""
+    out = ctypes.c_size_t(0)
+    _check(_lib.qmv_norm_rope_backward_bytes(T, D, len(heads), (_i64 * len(heads))(*heads), ctypes.byref(out)))
+    return out.value
+
+
+def norm_rope_backward(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None,
+                       k_weight: torch.Tensor | None, dq_out: torch.Tensor, dk_out: torch.Tensor | None, pos: torch.Tensor,
+                       freqs: torch.Tensor, eps: float = 1e-6, layout="half", amplitude: float = 1.0,
+                       weight_offset: float = 0.0, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                       weight_grads: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of norm_rope for the gradients dq_out and dk_out of
+    its results, from the q and k that it took.
+
+    weight_grads=False leaves the weights' gradients out (None), and they are None
+    where there is no weight.  dq may be q or dq_out itself, dk likewise.
+    workspace: scratch memory of norm_rope_backward_bytes bytes, allocated when absent.
+    """
+    if stream is not None:  # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, pos, freqs, eps, layout, amplitude,
+                                      weight_offset, dq, dk, weight_grads, workspace)
+    _no_gradient("norm_rope_backward", q, k, q_weight, k_weight, dq_out, dk_out, freqs, dq, dk)
+    if (k is None) != (dk_out is None) or (k is None and dk is not None):
+        raise ValueError("k, dk_out and dk go together")
+    layout, w_dtype, s = _norm_rope_arguments(q, k, q_weight, k_weight, pos, freqs, layout)
+    given = dq, dk, workspace
+    fields, outs, sums = (), [], []
+    for x, w, g, y, what in ((q, q_weight, dq_out, dq, "q"), (k, k_weight, dk_out, dk, "k")):
+        if x is None:
+            outs.append(None)
+            sums.append(None)
+            continue
+        if g.shape != x.shape or g.dtype != x.dtype or g.get_device() != x.get_device():
+            raise ValueError(f"d{what}_out must have {what}'s shape, dtype and device")
+        y = _rope_out(x, y, what, "d" + what)
+        dw = torch.empty_like(w) if w is not None and weight_grads else None
+        outs.append(y)
+        sums.append(dw)
+        fields += (x.data_ptr(), g.data_ptr(), y.data_ptr(), w.data_ptr() if w is not None else 0,
+                   dw.data_ptr() if dw is not None else 0, x.shape[1], *_head_strides(x, what),
+                   *_head_strides(g, f"d{what}_out"), *_head_strides(y, "d" + what))
+    T, _, D = q.shape
+    ws, nbytes = None, 0
+    if sums[0] is not None or sums[1] is not None:
+        nbytes = norm_rope_backward_bytes(T, D, q.shape[1]) if k is None else \
+            norm_rope_backward_bytes(T, D, q.shape[1], k.shape[1])
+        if workspace is None:
+            workspace = q.new_empty(nbytes, dtype=torch.uint8)
+        ws = _weight(workspace, nbytes, q.get_device(), "workspace")
+    _check(_lib.qmv_norm_rope_backward(T, D, 2 * freqs.numel(), layout, len(fields) // 12,
+                                       _NormFields[len(fields)].pack(*fields), _DTYPES[q.dtype], w_dtype, eps, weight_offset,
+                                       pos.data_ptr(), freqs.data_ptr(), amplitude, ws, nbytes, s))
+    _written(*given)
+    return outs[0], outs[1], sums[0], sums[1]
 
 
 def dequant(fmt, W: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None,

@@ -524,6 +524,170 @@ int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_r
                   "rope");
 }
 
+// Heads of T tokens that lie at strides: an output's own values must not meet.
+static int check_own_values(int64_t T, int64_t D, int64_t heads, int64_t token, int64_t head, int i, const char* name) {
+  struct Axis {
+    int64_t n, st;
+  } in{heads, std::llabs(head)}, out{T, std::llabs(token)};
+  if (in.n > 1 && out.n > 1 && in.st > out.st) std::swap(in, out);
+  const int64_t reach = in.n > 1 ? (in.n - 1) * in.st + D : D;
+  if ((in.n > 1 && in.st < D) || (out.n > 1 && out.st < reach))
+    return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].%s holds some values more than once", i, name);
+  return QMV_OK;
+}
+
+static bool is_dtype(int d) { return d == QMV_F32 || d == QMV_F16 || d == QMV_BF16 || d == QMV_Q8X; }
+static uintptr_t element(int dtype) { return dtype == QMV_F32 ? 4 : 2; }
+
+// Arguments that qmv_norm_rope and its backward pass share.
+static int check_norm_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const void* tensors, int dtype,
+                           int w_dtype, float eps, float w_offset, const int64_t* pos, const float* freqs) {
+  if (T < 1) return fail(QMV_ERR_SHAPE, "T=%lld must be >= 1", (long long)T);
+  if (D < 1 || D > 1024) return fail(QMV_ERR_SHAPE, "D=%lld must be in [1, 1024]", (long long)D);
+  if (R < 2 || R % 2 || R > D)
+    return fail(QMV_ERR_SHAPE, "R=%lld must be even, in [2, D] (D=%lld)", (long long)R, (long long)D);
+  if (layout != QMV_ROPE_HALF && layout != QMV_ROPE_INTERLEAVED)
+    return fail(QMV_ERR_UNSUPPORTED, "layout=%d is not a qmv_rope_layout", layout);
+  if (count < 1 || count > QMV_ROPE_MAX)
+    return fail(QMV_ERR_SHAPE, "count=%d must be in [1, %d]", count, QMV_ROPE_MAX);
+  if (!tensors) return fail(QMV_ERR_NULL, "tensors is NULL");
+  if (!pos) return fail(QMV_ERR_NULL, "pos is NULL");
+  if (!freqs) return fail(QMV_ERR_NULL, "freqs is NULL");
+  if (!is_dtype(dtype)) return fail(QMV_ERR_DTYPE, "dtype=%d is not a qmv_dtype", dtype);
+  if (dtype == QMV_Q8X) return fail(QMV_ERR_UNSUPPORTED, "norm_rope takes f32, f16 or bf16");
+  if (w_dtype != QMV_F32 && w_dtype != dtype)
+    return fail(QMV_ERR_DTYPE, "w_dtype=%d must be QMV_F32 or dtype", w_dtype);
+  if (!(std::isfinite(eps) && eps >= 0)) return fail(QMV_ERR_UNSUPPORTED, "eps must be finite and >= 0");
+  if (!std::isfinite(w_offset)) return fail(QMV_ERR_UNSUPPORTED, "w_offset must be finite");
+  if (!aligned(pos, 8)) return fail(QMV_ERR_ALIGN, "pos is not 8-byte aligned");
+  if (!aligned(freqs, 4)) return fail(QMV_ERR_ALIGN, "freqs is not 4-byte aligned");
+  if (T >= (int64_t(1) << 31)) return fail(QMV_ERR_OVERFLOW, "T is past 2^31");
+  return QMV_OK;
+}
+
+// heads of each tensor: a block of tokens is indexed with 32-bit ints
+static int check_heads(int64_t D, int count, const int64_t* heads) {
+  int64_t all = 0;
+  for (int i = 0; i < count; ++i) {
+    if (heads[i] < 1) return fail(QMV_ERR_SHAPE, "tensors[%d].heads=%lld must be >= 1", i, (long long)heads[i]);
+    if (heads[i] > (int64_t(1) << 28)) return fail(QMV_ERR_OVERFLOW, "tensors[%d].heads too large", i);
+    all += heads[i];
+  }
+  if (all > (int64_t(1) << 28) / D) return fail(QMV_ERR_OVERFLOW, "heads * D past 2^28");
+  return QMV_OK;
+}
+
+static int check_place(const void* p, uintptr_t align, int i, const char* name) {
+  if (!p) return fail(QMV_ERR_NULL, "tensors[%d].%s is NULL", i, name);
+  if (!aligned(p, align)) return fail(QMV_ERR_ALIGN, "tensors[%d].%s is not aligned to its element", i, name);
+  return QMV_OK;
+}
+
+int qmv_norm_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_norm_rope_tensor* tensors, int dtype,
+                  int w_dtype, float eps, float w_offset, const int64_t* pos, const float* freqs, float amplitude,
+                  void* stream) {
+  int st;
+  if ((st = check_norm_rope(T, D, R, layout, count, tensors, dtype, w_dtype, eps, w_offset, pos, freqs))) return st;
+  int64_t heads[QMV_ROPE_MAX];
+  for (int i = 0; i < count; ++i) heads[i] = tensors[i].heads;
+  if ((st = check_heads(D, count, heads))) return st;
+  for (int i = 0; i < count; ++i) {
+    const qmv_norm_rope_tensor& t = tensors[i];
+    if ((st = check_place(t.x, element(dtype), i, "x"))) return st;
+    if ((st = check_place(t.y, element(dtype), i, "y"))) return st;
+    if (t.weight && (st = check_place(t.weight, element(w_dtype), i, "weight"))) return st;
+    if (t.x == t.y && (t.x_token != t.y_token || t.x_head != t.y_head))
+      return fail(QMV_ERR_UNSUPPORTED, "tensors[%d] is in place with other strides", i);
+    if ((st = check_own_values(T, D, t.heads, t.y_token, t.y_head, i, "y"))) return st;
+  }
+  for (int i = 0; i < count; ++i)  // one launch works on all tensors, in no order
+    for (int j = 0; j < count; ++j) {
+      if (i < j && tensors[i].y == tensors[j].y)
+        return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].y and tensors[%d].y are one buffer", i, j);
+      if (i != j && tensors[i].y == tensors[j].x)
+        return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].y is the buffer of tensors[%d].x", i, j);
+      if (tensors[i].y == tensors[j].weight)
+        return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].y is the buffer of tensors[%d].weight", i, j);
+    }
+  if ((st = check_device())) return st;
+  return launched(qmv::launch_norm_rope(T, int(D), int(R), layout, count, tensors, dtype, w_dtype, eps, w_offset, pos, freqs,
+                                        amplitude, as_stream(stream)),
+                  "norm_rope");
+}
+
+int qmv_norm_rope_backward_bytes(int64_t T, int64_t D, int count, const int64_t* heads, size_t* out_bytes) {
+  int st;
+  if (T < 1) return fail(QMV_ERR_SHAPE, "T=%lld must be >= 1", (long long)T);
+  if (D < 1 || D > 1024) return fail(QMV_ERR_SHAPE, "D=%lld must be in [1, 1024]", (long long)D);
+  if (count < 1 || count > QMV_ROPE_MAX)
+    return fail(QMV_ERR_SHAPE, "count=%d must be in [1, %d]", count, QMV_ROPE_MAX);
+  if (!heads) return fail(QMV_ERR_NULL, "heads is NULL");
+  if (!out_bytes) return fail(QMV_ERR_NULL, "out_bytes is NULL");
+  if (T >= (int64_t(1) << 31)) return fail(QMV_ERR_OVERFLOW, "T is past 2^31");
+  if ((st = check_heads(D, count, heads))) return st;
+  *out_bytes = size_t(qmv::norm_backward_plan(T, D, count, heads).bytes);
+  return ok();
+}
+
+int qmv_norm_rope_backward(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_norm_rope_grad* tensors,
+                           int dtype, int w_dtype, float eps, float w_offset, const int64_t* pos, const float* freqs,
+                           float amplitude, void* ws, size_t ws_bytes, void* stream) {
+  int st;
+  if ((st = check_norm_rope(T, D, R, layout, count, tensors, dtype, w_dtype, eps, w_offset, pos, freqs))) return st;
+  int64_t heads[QMV_ROPE_MAX];
+  for (int i = 0; i < count; ++i) heads[i] = tensors[i].heads;
+  if ((st = check_heads(D, count, heads))) return st;
+  bool sums = false;
+  for (int i = 0; i < count; ++i) {
+    const qmv_norm_rope_grad& t = tensors[i];
+    if ((st = check_place(t.x, element(dtype), i, "x"))) return st;
+    if ((st = check_place(t.dy, element(dtype), i, "dy"))) return st;
+    if ((st = check_place(t.dx, element(dtype), i, "dx"))) return st;
+    if (t.weight && (st = check_place(t.weight, element(w_dtype), i, "weight"))) return st;
+    if (t.dweight) {
+      if (!t.weight) return fail(QMV_ERR_NULL, "tensors[%d].dweight is given without weight", i);
+      if ((st = check_place(t.dweight, element(w_dtype), i, "dweight"))) return st;
+      sums = true;
+    }
+    if ((t.dx == t.x && (t.dx_token != t.x_token || t.dx_head != t.x_head)) ||
+        (t.dx == t.dy && (t.dx_token != t.dy_token || t.dx_head != t.dy_head)))
+      return fail(QMV_ERR_UNSUPPORTED, "tensors[%d] is in place with other strides", i);
+    if ((st = check_own_values(T, D, t.heads, t.dx_token, t.dx_head, i, "dx"))) return st;
+  }
+  const qmv::NormBackwardPlan plan = qmv::norm_backward_plan(T, D, count, heads);
+  if (sums) {
+    if (!ws) return fail(QMV_ERR_NULL, "ws is NULL");
+    if (!aligned(ws, 16)) return fail(QMV_ERR_ALIGN, "ws is not 16-byte aligned");
+    if (ws_bytes < size_t(plan.bytes))
+      return fail(QMV_ERR_SHAPE, "ws_bytes=%llu, the call needs %lld", (unsigned long long)ws_bytes, (long long)plan.bytes);
+  }
+  const int64_t wb = D * int64_t(element(w_dtype));
+  for (int i = 0; i < count; ++i)
+    for (int j = 0; j < count; ++j) {
+      const qmv_norm_rope_grad &a = tensors[i], &b = tensors[j];
+      if (i < j && a.dx == b.dx) return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].dx and tensors[%d].dx are one buffer", i, j);
+      if (i != j && (a.dx == b.x || a.dx == b.dy))
+        return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].dx is the buffer of tensors[%d].%s", i, j, a.dx == b.x ? "x" : "dy");
+      if (a.dx == b.weight) return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].dx is the buffer of tensors[%d].weight", i, j);
+      if (!a.dweight) continue;
+      // the launch that writes a dweight runs after the one that reads the inputs; the weights may
+      // serve the next call, so what it writes is apart from all but its own
+      const Range r{a.dweight, wb, "dweight"};
+      if (b.weight && (st = check_apart(r, Range{b.weight, wb, "weight"}))) return st;
+      if (i < j && b.dweight && (st = check_apart(r, Range{b.dweight, wb, "another dweight"}))) return st;
+      if (a.dweight == b.x || a.dweight == b.dy || a.dweight == b.dx)
+        return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].dweight is the buffer of tensors[%d].x, dy or dx", i, j);
+      const Range w{ws, plan.bytes, "ws"};
+      if ((st = check_apart(w, r))) return st;
+      if (b.weight && (st = check_apart(w, Range{b.weight, wb, "weight"}))) return st;
+      if (b.x == ws || b.dy == ws || b.dx == ws) return fail(QMV_ERR_UNSUPPORTED, "ws is the buffer of tensors[%d].x, dy or dx", j);
+    }
+  if ((st = check_device())) return st;
+  return launched(qmv::launch_norm_rope_backward(T, int(D), int(R), layout, count, tensors, dtype, w_dtype, eps, w_offset, pos,
+                                                 freqs, amplitude, plan, static_cast<uint8_t*>(ws), as_stream(stream)),
+                  "norm_rope_backward");
+}
+
 int qmv_rope_freqs(int64_t R, double base, const qmv_rope_scaling* scaling, float* freqs) {
   if (R < 2 || R % 2 || R > 4096) return fail(QMV_ERR_SHAPE, "R=%lld must be even, in [2, 4096]", (long long)R);
   if (!freqs) return fail(QMV_ERR_NULL, "freqs is NULL");

@@ -26,4 +26,18 @@ hipError_t launch_glu_bwd(int fmt, int64_t N, int64_t K, int64_t M, const uint8_
 hipError_t launch_rope(int64_t T, int D, int R, int layout, int count, const qmv_rope_tensor* t, int dtype,
                        const int64_t* pos, const float* freqs, float amplitude, int inverse, hipStream_t s);
 
+// Backward pass of the norms: blocks per tensor, where its partial sums of dweight ([blocks][D] f32)
+// lie in the workspace, and bytes in all.
+struct NormBackwardPlan {
+  int blocks[QMV_ROPE_MAX];
+  int64_t offset[QMV_ROPE_MAX], bytes;
+};
+NormBackwardPlan norm_backward_plan(int64_t T, int64_t D, int count, const int64_t* heads);
+hipError_t launch_norm_rope(int64_t T, int D, int R, int layout, int count, const qmv_norm_rope_tensor* t, int dtype,
+                            int w_dtype, float eps, float offset, const int64_t* pos, const float* freqs, float amplitude,
+                            hipStream_t s);
+hipError_t launch_norm_rope_backward(int64_t T, int D, int R, int layout, int count, const qmv_norm_rope_grad* t, int dtype,
+                                     int w_dtype, float eps, float offset, const int64_t* pos, const float* freqs,
+                                     float amplitude, const NormBackwardPlan& plan, uint8_t* ws, hipStream_t s);
+
 }  // namespace qmv

@@ -1,8 +1,8 @@
 /*
  * qmv_layer.h -- what a decoder layer over block-quantized weights needs around
  * the products of qmv.h when it takes many tokens at once: the gated
- * feed-forward products with their backward pass, and the rotary positions of
- * the q and k heads.  Same library (libqmv.so), same conventions as qmv.h:
+ * feed-forward products with their backward pass, the rotary positions of the q
+ * and k heads, and these in one pass with the heads' norms, with the gradient.  Same library (libqmv.so), same conventions as qmv.h:
  * packed layout, device pointers, caller-owned buffers, status codes and
  * qmv_last_error, streams, no allocation, no synchronization, graph capture.
  */
@@ -136,6 +136,68 @@ typedef struct qmv_rope_tensor {
  */
 int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_rope_tensor* tensors, int dtype,
              const int64_t* pos, const float* freqs, float amplitude, int inverse, void* stream);
+
+/* One tensor of qmv_norm_rope: as qmv_rope_tensor, with the norm's weight. */
+typedef struct qmv_norm_rope_tensor {
+  const void* x;
+  void* y;            /* as qmv_rope_tensor.y */
+  const void* weight; /* [D] of w_dtype, device; NULL: 1 (the offset does not count then) */
+  int64_t heads;
+  int64_t x_token, x_head;
+  int64_t y_token, y_head;
+} qmv_norm_rope_tensor;
+
+/*
+ * The norm of every q and k head and its rotary position in one pass (aot-llm
+ * README, supported architectures: q / k norms), for up to QMV_ROPE_MAX tensors in
+ * one launch.  Over the D values x of a head
+ *   n = x / sqrt(mean(x^2) + eps),  y = rot(n * (weight + w_offset))
+ * with rot the rotation of qmv_rope (its layouts, its R <= D, its amplitude, which
+ * multiplies the rotated values only, and its far positions).  All of it is f32,
+ * sums included, and each output is rounded once to dtype; a head whose squares
+ * pass the f32 range gives zeros.  D <= 1024; otherwise the limits of qmv_rope.
+ *   w_dtype   QMV_F32 or dtype, of every weight, aligned to its element
+ *   eps       finite, >= 0;  w_offset: finite (1 where a model keeps weight - 1)
+ * Errors: as qmv_rope; SHAPE also for D > 1024, DTYPE for w_dtype, UNSUPPORTED for
+ * eps, w_offset and a weight that is an output's buffer.
+ */
+int qmv_norm_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_norm_rope_tensor* tensors, int dtype,
+                  int w_dtype, float eps, float w_offset, const int64_t* pos, const float* freqs, float amplitude,
+                  void* stream);
+
+/* One tensor of qmv_norm_rope_backward. */
+typedef struct qmv_norm_rope_grad {
+  const void* x;      /* what the forward call took */
+  const void* dy;     /* gradient of its y */
+  void* dx;           /* output; x or dy itself with the same strides, or no overlap with any x or dy;
+                         no overlap with another dx, nor of its own values */
+  const void* weight; /* as in the forward call */
+  void* dweight;      /* [D] of w_dtype, device: receives the weight's gradient; NULL: not wanted */
+  int64_t heads;
+  int64_t x_token, x_head;
+  int64_t dy_token, dy_head;
+  int64_t dx_token, dx_head;
+} qmv_norm_rope_grad;
+
+/*
+ * The backward pass of qmv_norm_rope: with g = rot^T(dy), h = g * (weight + w_offset)
+ * and n as above,
+ *   dx = (h - n mean(h n)) / sqrt(mean(x^2) + eps),  dweight = sum over tokens and heads of g n
+ * in f32, each output rounded once; the sums' order depends on the sizes only, so
+ * calls repeat bit for bit.
+ *   ws, ws_bytes   scratch memory, 16-byte aligned, of at least
+ *                  qmv_norm_rope_backward_bytes bytes; NULL and 0 where every dweight is NULL.
+ *                  Calls that overlap in time need a ws of their own.
+ * Errors: as qmv_norm_rope; NULL also for a dweight without weight, SHAPE for a ws_bytes
+ * that is too small, UNSUPPORTED for a dweight or ws that overlaps another buffer given.
+ */
+int qmv_norm_rope_backward(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_norm_rope_grad* tensors,
+                           int dtype, int w_dtype, float eps, float w_offset, const int64_t* pos, const float* freqs,
+                           float amplitude, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of scratch memory that qmv_norm_rope_backward needs for `count` tensors of
+ * T tokens with heads[i] heads of D values.  Host only.  Errors: SHAPE, NULL, OVERFLOW. */
+int qmv_norm_rope_backward_bytes(int64_t T, int64_t D, int count, const int64_t* heads, size_t* out_bytes);
 
 /* A stretch of the rotary frequencies.  With f_i the frequency of pair i and
  * r_i = original * f_i / (2 pi) its turns over the original context,
