@@ -14,6 +14,9 @@ Importing this package fails loudly when the library has not been built
     dX, dG, dU = qmv.gemm_glu_backward("q4k", Wg, Wu, G, U, dH, N, K, act="silu")
     q, k = qmv.rope(q, k, pos, qmv.rope_freqs(R))   # q [T][heads][D], k [T][kv_heads][D]
     q, k = qmv.norm_rope(q, k, q_weight, k_weight, pos, qmv.rope_freqs(R))   # the heads' norms in the same pass
+    cache = qmv.KVCache("q8_0", pages, kv_heads, D, page=64)                 # 8-bit or 4-bit blocks, paged
+    qmv.kv_write(cache, k, v, table, q_start, kv_len)                        # the new tokens of B sequences
+    o = qmv.kv_attention(cache, q, table, q_start, kv_len)                   # o as q
 """
 from __future__ import annotations
 
@@ -143,6 +146,33 @@ _lib.qmv_norm_rope_backward.argtypes = [_i64, _i64, _i64, _int, _int, _vp, _int,
 _lib.qmv_norm_rope_backward.restype = _int
 _lib.qmv_norm_rope_backward_bytes.argtypes = [_i64, _i64, _int, ctypes.POINTER(_i64), ctypes.POINTER(ctypes.c_size_t)]
 _lib.qmv_norm_rope_backward_bytes.restype = _int
+
+
+class QmvKvCache(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("page", ctypes.c_int32), ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("D", ctypes.c_int64), ("data", ctypes.c_void_p)]
+
+
+class QmvKvBatch(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("B", ctypes.c_int64), ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("columns", ctypes.c_int64), ("stride", ctypes.c_int64)]
+
+
+class QmvKvAttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("q_heads", ctypes.c_int64),
+                ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64), ("out_token", ctypes.c_int64),
+                ("out_head", ctypes.c_int64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("window", ctypes.c_int64), ("prefix", ctypes.c_int64), ("max_q", ctypes.c_int64), ("max_kv", ctypes.c_int64)]
+
+
+_lib.qmv_kv_cache_bytes.argtypes = [_vp, ctypes.POINTER(ctypes.c_size_t)]
+_lib.qmv_kv_cache_bytes.restype = _int
+_lib.qmv_kv_write.argtypes = _lib.qmv_kv_read.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp]
+_lib.qmv_kv_write.restype = _lib.qmv_kv_read.restype = _int
+_lib.qmv_kv_attention.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.qmv_kv_attention.restype = _int
+_lib.qmv_kv_attention_bytes.argtypes = [_vp, _vp, _vp, ctypes.POINTER(ctypes.c_size_t)]
+_lib.qmv_kv_attention_bytes.restype = _int
 _lib.qmv_dequant.argtypes = [_int, _i64, _i64, _vp, _vp, _vp]
 _lib.qmv_dequant.restype = _int
 
@@ -152,6 +182,7 @@ EXPORTS = ("qmv_abi_version", "qmv_status_string", "qmv_last_error", "qmv_packed
 LAYER_EXPORTS = ("qmv_gemm_glu", "qmv_gemm_glu_backward", "qmv_gemm_glu_backward_bytes", "qmv_gemm_glu_backward_ex",
                  "qmv_gemm_glu_backward_ex_bytes", "qmv_rope", "qmv_rope_freqs", "qmv_norm_rope", "qmv_norm_rope_backward",
                  "qmv_norm_rope_backward_bytes")
+CACHE_EXPORTS = ("qmv_kv_cache_bytes", "qmv_kv_write", "qmv_kv_read", "qmv_kv_attention", "qmv_kv_attention_bytes")
 
 
 class QmvError(RuntimeError):
@@ -815,6 +846,196 @@ def norm_rope_backward(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.
                                        pos.data_ptr(), freqs.data_ptr(), amplitude, ws, nbytes, s))
     _written(*given)
     return outs[0], outs[1], sums[0], sums[1]
+
+
+CACHE_FORMATS = {"q8_0": 1, "q4_0": 5}
+
+
+class KVCache:
+    """Keys and values of `heads` heads of D values (a multiple of 32, at most 256) in
+    8-bit ("q8_0") or 4-bit ("q4_0") blocks of 32: `pages` pages of `page` tokens (a
+    multiple of 16).  `data` is the device buffer (uint8, qmv_cache.h has its layout),
+    allocated when absent; what has not been written there is never looked at."""
+
+    def __init__(self, fmt, pages: int, heads: int, D: int, page: int = 64, data: torch.Tensor | None = None,
+                 device="cuda"):
+        if isinstance(fmt, str):
+            if fmt not in CACHE_FORMATS:
+                raise ValueError(f"unknown cache format {fmt!r}; one of {sorted(CACHE_FORMATS)}")
+            fmt = CACHE_FORMATS[fmt]
+        self.fmt, self.pages, self.heads, self.D, self.page = int(fmt), pages, heads, D, page
+        nbytes = kv_cache_bytes(self.fmt, pages, heads, D, page)
+        if data is None:
+            data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if data.nbytes < nbytes:
+            raise ValueError(f"data holds {data.nbytes} bytes, the cache needs {nbytes}")
+        if not data.is_contiguous():
+            raise ValueError("tensors passed to libqmv must be contiguous")
+        self.data = data
+
+
+@functools.lru_cache(maxsize=4096)
+def kv_cache_bytes(fmt, pages: int, heads: int, D: int, page: int = 64) -> int:
+    """Bytes of a cache of these sizes."""
+    out = ctypes.c_size_t(0)
+    c = QmvKvCache(CACHE_FORMATS[fmt] if isinstance(fmt, str) else fmt, page, pages, heads, D, None)
+    _check(_lib.qmv_kv_cache_bytes(ctypes.byref(c), ctypes.byref(out)))
+    return out.value
+
+
+_KvCacheFields, _KvBatchFields = struct.Struct("2i4q"), struct.Struct("7q")  # qmv_kv_cache, qmv_kv_batch
+_KvAttentionFields = struct.Struct("8qif4q")  # qmv_kv_attention_args
+
+
+def _kv_batch(cache: KVCache, T: int, device: int, table, q_start, kv_len) -> tuple:
+    """The cache and the batch as the C structs' bytes."""
+    if cache.data.get_device() != device:
+        raise ValueError(f"the cache is on {cache.data.device}, the call's tensors on device {device}")
+    if table.dim() != 2:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected [sequences][pages]")
+    B, columns = table.shape
+    if q_start.numel() != B + 1 or kv_len.numel() != B:
+        raise ValueError(f"q_start holds {q_start.numel()} and kv_len {kv_len.numel()} numbers, the table has {B} sequences")
+    for t, what in ((table, "table"), (q_start, "q_start"), (kv_len, "kv_len")):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{what} must be torch.int32, got {t.dtype}")
+        if t.get_device() != device:
+            raise ValueError(f"{what} is on {t.device}, the call's tensors on device {device}")
+    if not (q_start.is_contiguous() and kv_len.is_contiguous()) or (columns > 1 and table.stride(1) != 1):
+        raise ValueError("q_start, kv_len and the table's rows must be contiguous")
+    return (_KvCacheFields.pack(cache.fmt, cache.page, cache.pages, cache.heads, cache.D, cache.data.data_ptr()),
+            _KvBatchFields.pack(T, B, q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), columns, table.stride(0)))
+
+
+def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, q_start: torch.Tensor,
+             kv_len: torch.Tensor, stream=None) -> None:
+    """Writes k and v [T][heads][D] (f32, f16 or bf16; strided as long as a head's
+    values are adjacent) of the new tokens of B sequences to their places in the cache.
+
+    Rows q_start[b] .. q_start[b + 1] - 1 are the last tokens of sequence b, which is
+    kv_len[b] long with them; its page of position p is table[b][p // page] (int32,
+    all three on the device).  Rows from q_start[B] on are left out.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_write(cache, k, v, table, q_start, kv_len)
+    _no_gradient("kv_write", k, v)
+    if k.dim() != 3 or k.shape[1] != cache.heads or k.shape[2] != cache.D:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected [T][{cache.heads}][{cache.D}]")
+    if k.dtype not in _DTYPES:
+        raise ValueError("k dtype must be float32, float16 or bfloat16")
+    s, device = _on_current_device(k), k.get_device()
+    if v.shape != k.shape or v.dtype != k.dtype or v.get_device() != device:
+        raise ValueError("v must have k's shape, dtype and device")
+    c, b = _kv_batch(cache, k.shape[0], device, table, q_start, kv_len)
+    _check(_lib.qmv_kv_write(c, b, k.data_ptr(), *_head_strides(k, "k"), v.data_ptr(), *_head_strides(v, "v"),
+                             _DTYPES[k.dtype], s))
+    _written(cache.data)
+
+
+def kv_read(cache: KVCache, table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, T: int,
+            dtype: torch.dtype = torch.bfloat16, k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """(k, v) [T][heads][D] of the same rows as in kv_write, read back from the cache:
+    whole sequences with q_start the running sum of kv_len.  k and v are
+    allocated as `dtype` when absent; rows of no sequence are left as they are."""
+    if stream is not None:  # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return kv_read(cache, table, q_start, kv_len, T, dtype, k, v)
+    _no_gradient("kv_read", k, v)
+    s, device = _on_current_device(cache.data), cache.data.get_device()
+    given, shape = (k, v), (T, cache.heads, cache.D)
+    if k is not None or v is not None:
+        dtype = (k if k is not None else v).dtype
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    outs = []
+    for t, what in ((k, "k"), (v, "v")):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=cache.data.device)
+        if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+            raise ValueError(f"{what} must be {shape} of {dtype} on the cache's device")
+        if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+            raise ValueError(f"{what} holds some values more than once")
+        outs.append(t)
+    k, v = outs
+    c, b = _kv_batch(cache, T, device, table, q_start, kv_len)
+    _check(_lib.qmv_kv_read(c, b, k.data_ptr(), *_head_strides(k, "k"), v.data_ptr(), *_head_strides(v, "v"),
+                            _DTYPES[dtype], s))
+    _written(*given)
+    return k, v
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv_attention_bytes(cache_fields: tuple, batch_fields: tuple, q_heads: int, dtype: int, prefix: int, window: int,
+                        max_q: int, max_kv: int) -> int:
+    out = ctypes.c_size_t(0)
+    args = _KvAttentionFields.pack(0, 0, 0, q_heads, 0, 0, 0, 0, dtype, 1.0, window, prefix, max_q, max_kv)
+    _check(_lib.qmv_kv_attention_bytes(_KvCacheFields.pack(*cache_fields, 0), _KvBatchFields.pack(*batch_fields), args,
+                                       ctypes.byref(out)))
+    return out.value
+
+
+def kv_attention_bytes(cache: KVCache, T: int, q_heads: int, dtype: torch.dtype, B: int, columns: int, window: int = 0,
+                       prefix: int = 0, max_q: int | None = None, max_kv: int | None = None) -> int:
+    """Bytes of scratch memory that kv_attention needs for T rows of B sequences whose
+    table has `columns` pages, with the other arguments as given to it."""
+    return _kv_attention_bytes((cache.fmt, cache.page, cache.pages, cache.heads, cache.D), (T, B, 0, 0, 0, columns, columns),
+                               q_heads, _DTYPES[dtype], prefix, window, -(-T // B) if max_q is None else max_q,
+                               columns * cache.page if max_kv is None else max_kv)
+
+
+def kv_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                 scale: float | None = None, window: int = 0, prefix: int = 0, max_q: int | None = None,
+                 max_kv: int | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of q [T][q_heads][D] (f32, f16 or bf16) over the cache; returns out, shaped as q.
+
+    Rows, sequences and pages as in kv_write, which has to have written the rows'
+    own keys and values.  scale: D^-0.5 when absent.  window: a row at position p
+    sees p - window + 1 .. p (0: all up to p).  prefix: the first `prefix` positions
+    lie in the same pages in every sequence (as row 0 of the table names them); they
+    are then read once for the whole batch.  max_q, max_kv: the most rows and tokens
+    that a sequence is expected to have (T / B, and what the table holds, when
+    absent); they shape the launch, not the result.  lse f32 [T][q_heads] receives
+    ln(sum exp(s)).  A row that sees nothing gives zeros.  workspace: scratch
+    memory of kv_attention_bytes bytes, allocated when absent.
+    """
+    if stream is not None:  # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return kv_attention(cache, q, table, q_start, kv_len, scale, window, prefix, max_q, max_kv, out, lse, workspace)
+    _no_gradient("kv_attention", q, out)
+    if q.dim() != 3 or q.shape[2] != cache.D:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [T][heads][{cache.D}]")
+    if q.dtype not in _DTYPES:
+        raise ValueError("q dtype must be float32, float16 or bfloat16")
+    T, q_heads, D = q.shape
+    s, device = _on_current_device(q), q.get_device()
+    c, b = _kv_batch(cache, T, device, table, q_start, kv_len)
+    given = out, lse, workspace
+    if out is None:
+        out = torch.empty((T, q_heads, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != device:
+        raise ValueError("out must have q's shape, dtype and device")
+    elif any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
+        raise ValueError("out holds some values more than once")
+    if lse is not None and (lse.shape != (T, q_heads) or lse.dtype != torch.float32 or lse.get_device() != device
+                            or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 [{T}][{q_heads}] on q's device")
+    B, columns = table.shape
+    nbytes = kv_attention_bytes(cache, T, q_heads, q.dtype, B, columns, window, prefix, max_q, max_kv)
+    ws = None
+    if nbytes:
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        ws = _weight(workspace, nbytes, device, "workspace")
+    args = _KvAttentionFields.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), q_heads,
+                                   *_head_strides(q, "q"), *_head_strides(out, "out"), _DTYPES[q.dtype],
+                                   D ** -0.5 if scale is None else scale, window, prefix,
+                                   -(-T // B) if max_q is None else max_q,
+                                   columns * cache.page if max_kv is None else max_kv)
+    _check(_lib.qmv_kv_attention(c, b, args, ws, nbytes, s))
+    _written(*given)
+    return out
 
 
 def dequant(fmt, W: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None,

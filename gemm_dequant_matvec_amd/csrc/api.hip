@@ -14,6 +14,7 @@
 #include <mutex>
 #include <utility>
 
+#include "cache_internal.h"
 #include "layer_internal.h"
 
 namespace {
@@ -525,15 +526,13 @@ int qmv_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const qmv_r
 }
 
 // Heads of T tokens that lie at strides: an output's own values must not meet.
-static int check_own_values(int64_t T, int64_t D, int64_t heads, int64_t token, int64_t head, int i, const char* name) {
+static bool meets_itself(int64_t T, int64_t D, int64_t heads, int64_t token, int64_t head) {
   struct Axis {
     int64_t n, st;
   } in{heads, std::llabs(head)}, out{T, std::llabs(token)};
   if (in.n > 1 && out.n > 1 && in.st > out.st) std::swap(in, out);
   const int64_t reach = in.n > 1 ? (in.n - 1) * in.st + D : D;
-  if ((in.n > 1 && in.st < D) || (out.n > 1 && out.st < reach))
-    return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].%s holds some values more than once", i, name);
-  return QMV_OK;
+  return (in.n > 1 && in.st < D) || (out.n > 1 && out.st < reach);
 }
 
 static bool is_dtype(int d) { return d == QMV_F32 || d == QMV_F16 || d == QMV_BF16 || d == QMV_Q8X; }
@@ -598,7 +597,8 @@ int qmv_norm_rope(int64_t T, int64_t D, int64_t R, int layout, int count, const 
     if (t.weight && (st = check_place(t.weight, element(w_dtype), i, "weight"))) return st;
     if (t.x == t.y && (t.x_token != t.y_token || t.x_head != t.y_head))
       return fail(QMV_ERR_UNSUPPORTED, "tensors[%d] is in place with other strides", i);
-    if ((st = check_own_values(T, D, t.heads, t.y_token, t.y_head, i, "y"))) return st;
+    if (meets_itself(T, D, t.heads, t.y_token, t.y_head))
+      return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].y holds some values more than once", i);
   }
   for (int i = 0; i < count; ++i)  // one launch works on all tensors, in no order
     for (int j = 0; j < count; ++j) {
@@ -652,7 +652,8 @@ int qmv_norm_rope_backward(int64_t T, int64_t D, int64_t R, int layout, int coun
     if ((t.dx == t.x && (t.dx_token != t.x_token || t.dx_head != t.x_head)) ||
         (t.dx == t.dy && (t.dx_token != t.dy_token || t.dx_head != t.dy_head)))
       return fail(QMV_ERR_UNSUPPORTED, "tensors[%d] is in place with other strides", i);
-    if ((st = check_own_values(T, D, t.heads, t.dx_token, t.dx_head, i, "dx"))) return st;
+    if (meets_itself(T, D, t.heads, t.dx_token, t.dx_head))
+      return fail(QMV_ERR_UNSUPPORTED, "tensors[%d].dx holds some values more than once", i);
   }
   const qmv::NormBackwardPlan plan = qmv::norm_backward_plan(T, D, count, heads);
   if (sums) {
@@ -686,6 +687,179 @@ int qmv_norm_rope_backward(int64_t T, int64_t D, int64_t R, int layout, int coun
   return launched(qmv::launch_norm_rope_backward(T, int(D), int(R), layout, count, tensors, dtype, w_dtype, eps, w_offset, pos,
                                                  freqs, amplitude, plan, static_cast<uint8_t*>(ws), as_stream(stream)),
                   "norm_rope_backward");
+}
+
+// ------------------------------------------------------ key / value cache
+
+static int check_cache(const qmv_kv_cache* c, bool with_data) {
+  if (!c) return fail(QMV_ERR_NULL, "cache is NULL");
+  if (c->fmt != QMV_Q8_0 && c->fmt != QMV_Q4_0)
+    return fail(QMV_ERR_FORMAT, "cache->fmt=%d must be QMV_Q8_0 or QMV_Q4_0", int(c->fmt));
+  if (c->page < 16 || c->page % 16 || c->page > 1024)
+    return fail(QMV_ERR_SHAPE, "cache->page=%d must be a multiple of 16, at most 1024", int(c->page));
+  if (c->D < 32 || c->D % 32 || c->D > 256)
+    return fail(QMV_ERR_SHAPE, "cache->D=%lld must be a multiple of 32, at most 256", (long long)c->D);
+  if (c->heads < 1) return fail(QMV_ERR_SHAPE, "cache->heads=%lld must be >= 1", (long long)c->heads);
+  if (c->pages < 1) return fail(QMV_ERR_SHAPE, "cache->pages=%lld must be >= 1", (long long)c->pages);
+  if (c->heads > 65535) return fail(QMV_ERR_OVERFLOW, "cache->heads is past 65535");
+  if (c->pages > 0x7FFFFFFF) return fail(QMV_ERR_OVERFLOW, "cache->pages is past 2^31 - 1");
+  if (with_data) {
+    if (!c->data) return fail(QMV_ERR_NULL, "cache->data is NULL");
+    if (!aligned(c->data, 16)) return fail(QMV_ERR_ALIGN, "cache->data is not 16-byte aligned");
+  }
+  return QMV_OK;
+}
+
+static int64_t cache_bytes(const qmv_kv_cache& c) {  // below 2^31 * 2^16 * 2^20 at most
+  return c.pages * c.heads * (c.page / 16) * qmv::kv_set_bytes(c.fmt, c.D);
+}
+
+int qmv_kv_cache_bytes(const qmv_kv_cache* cache, size_t* out_bytes) {
+  int st;
+  if ((st = check_cache(cache, false))) return st;
+  if (!out_bytes) return fail(QMV_ERR_NULL, "out_bytes is NULL");
+  if (cache->pages > (int64_t(1) << 50) / (cache->heads << 20)) return fail(QMV_ERR_OVERFLOW, "the cache is past 2^50 bytes");
+  *out_bytes = size_t(cache_bytes(*cache));
+  return ok();
+}
+
+static int check_batch(const qmv_kv_cache* c, const qmv_kv_batch* b, bool with_pointers) {
+  if (!b) return fail(QMV_ERR_NULL, "batch is NULL");
+  if (b->T < 1) return fail(QMV_ERR_SHAPE, "batch->T=%lld must be >= 1", (long long)b->T);
+  if (b->B < 1) return fail(QMV_ERR_SHAPE, "batch->B=%lld must be >= 1", (long long)b->B);
+  if (b->columns < 1) return fail(QMV_ERR_SHAPE, "batch->columns=%lld must be >= 1", (long long)b->columns);
+  if (b->T >= (int64_t(1) << 31)) return fail(QMV_ERR_OVERFLOW, "batch->T is past 2^31");
+  // a launch has a workgroup for each sequence and head, and counts threads in 32 bits
+  if (b->B > (int64_t(1) << 23) / c->heads) return fail(QMV_ERR_OVERFLOW, "batch->B * heads is past 2^23");
+  if (b->columns > (int64_t(1) << 30) / c->page) return fail(QMV_ERR_OVERFLOW, "batch->columns * page is past 2^30");
+  if (!with_pointers) return QMV_OK;
+  if (b->B > 1 && b->stride < b->columns)
+    return fail(QMV_ERR_SHAPE, "batch->stride=%lld is below columns=%lld", (long long)b->stride, (long long)b->columns);
+  if (!b->q_start) return fail(QMV_ERR_NULL, "batch->q_start is NULL");
+  if (!b->kv_len) return fail(QMV_ERR_NULL, "batch->kv_len is NULL");
+  if (!b->table) return fail(QMV_ERR_NULL, "batch->table is NULL");
+  if (!aligned(b->q_start, 4) || !aligned(b->kv_len, 4) || !aligned(b->table, 4))
+    return fail(QMV_ERR_ALIGN, "batch->q_start, kv_len or table is not 4-byte aligned");
+  return QMV_OK;
+}
+
+static bool in_cache(const qmv_kv_cache& c, const void* p) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p), d = reinterpret_cast<uintptr_t>(c.data);
+  return x >= d && x < d + uintptr_t(cache_bytes(c));
+}
+
+static int check_kv_dtype(int dtype) {
+  if (!is_dtype(dtype)) return fail(QMV_ERR_DTYPE, "dtype=%d is not a qmv_dtype", dtype);
+  if (dtype == QMV_Q8X) return fail(QMV_ERR_UNSUPPORTED, "the cache takes and gives f32, f16 or bf16");
+  return QMV_OK;
+}
+
+static int check_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const void* k, const void* v, int dtype) {
+  int st;
+  size_t bytes;
+  if ((st = check_cache(cache, true))) return st;
+  if ((st = qmv_kv_cache_bytes(cache, &bytes))) return st;
+  if ((st = check_batch(cache, batch, true))) return st;
+  if ((st = check_kv_dtype(dtype))) return st;
+  const void* p[] = {k, v};
+  const char* names[] = {"k", "v"};
+  for (int i = 0; i < 2; ++i) {
+    if (!p[i]) continue;
+    if (!aligned(p[i], element(dtype))) return fail(QMV_ERR_ALIGN, "%s is not aligned to its element", names[i]);
+    if (in_cache(*cache, p[i])) return fail(QMV_ERR_UNSUPPORTED, "%s lies in the cache", names[i]);
+  }
+  return QMV_OK;
+}
+
+int qmv_kv_write(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const void* k, int64_t k_token, int64_t k_head,
+                 const void* v, int64_t v_token, int64_t v_head, int dtype, void* stream) {
+  int st;
+  if ((st = check_kv(cache, batch, k, v, dtype))) return st;
+  if (!k) return fail(QMV_ERR_NULL, "k is NULL");
+  if (!v) return fail(QMV_ERR_NULL, "v is NULL");
+  if ((st = check_device())) return st;
+  return launched(qmv::launch_kv_write(*cache, *batch, k, k_token, k_head, v, v_token, v_head, dtype, as_stream(stream)),
+                  "kv_write");
+}
+
+int qmv_kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, void* k, int64_t k_token, int64_t k_head, void* v,
+                int64_t v_token, int64_t v_head, int dtype, void* stream) {
+  int st;
+  if ((st = check_kv(cache, batch, k, v, dtype))) return st;
+  if (!k && !v) return fail(QMV_ERR_NULL, "k and v are NULL");
+  if (k && meets_itself(batch->T, cache->D, cache->heads, k_token, k_head))
+    return fail(QMV_ERR_UNSUPPORTED, "k holds some values more than once");
+  if (v && meets_itself(batch->T, cache->D, cache->heads, v_token, v_head))
+    return fail(QMV_ERR_UNSUPPORTED, "v holds some values more than once");
+  if (k == v) return fail(QMV_ERR_UNSUPPORTED, "k and v are one buffer");
+  if ((st = check_device())) return st;
+  return launched(qmv::launch_kv_read(*cache, *batch, k, k_token, k_head, v, v_token, v_head, dtype, as_stream(stream)),
+                  "kv_read");
+}
+
+static int check_attention_sizes(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const qmv_kv_attention_args* a,
+                                 bool call) {
+  int st;
+  size_t bytes;
+  if ((st = check_cache(cache, call))) return st;
+  if ((st = qmv_kv_cache_bytes(cache, &bytes))) return st;
+  if ((st = check_batch(cache, batch, call))) return st;
+  if (!a) return fail(QMV_ERR_NULL, "args is NULL");
+  if (a->q_heads < 1 || a->q_heads % cache->heads)
+    return fail(QMV_ERR_SHAPE, "args->q_heads=%lld must be a multiple of the cache's heads (%lld)", (long long)a->q_heads,
+                (long long)cache->heads);
+  if ((st = check_kv_dtype(a->dtype))) return st;
+  if (a->window < 0) return fail(QMV_ERR_SHAPE, "args->window=%lld must be >= 0", (long long)a->window);
+  if (a->prefix < 0) return fail(QMV_ERR_SHAPE, "args->prefix=%lld must be >= 0", (long long)a->prefix);
+  if (a->max_q < 1) return fail(QMV_ERR_SHAPE, "args->max_q=%lld must be >= 1", (long long)a->max_q);
+  if (a->max_kv < 1) return fail(QMV_ERR_SHAPE, "args->max_kv=%lld must be >= 1", (long long)a->max_kv);
+  // the rows of a k / v head are counted in 32 bits, with room for a tile
+  if (a->q_heads > (int64_t(1) << 20) || a->q_heads / cache->heads > (int64_t(1) << 30) / batch->T)
+    return fail(QMV_ERR_OVERFLOW, "args->q_heads is past 2^20, or T * q_heads / heads past 2^30");
+  return QMV_OK;
+}
+
+int qmv_kv_attention_bytes(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const qmv_kv_attention_args* args,
+                           size_t* out_bytes) {
+  int st;
+  if ((st = check_attention_sizes(cache, batch, args, false))) return st;
+  if (!out_bytes) return fail(QMV_ERR_NULL, "out_bytes is NULL");
+  *out_bytes = size_t(qmv::kv_attention_plan(*cache, *batch, *args).bytes);
+  return ok();
+}
+
+int qmv_kv_attention(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const qmv_kv_attention_args* args, void* ws,
+                     size_t ws_bytes, void* stream) {
+  int st;
+  if ((st = check_attention_sizes(cache, batch, args, true))) return st;
+  const qmv_kv_attention_args& a = *args;
+  if (!a.q) return fail(QMV_ERR_NULL, "args->q is NULL");
+  if (!a.out) return fail(QMV_ERR_NULL, "args->out is NULL");
+  if (!aligned(a.q, element(a.dtype))) return fail(QMV_ERR_ALIGN, "args->q is not aligned to its element");
+  if (!aligned(a.out, element(a.dtype))) return fail(QMV_ERR_ALIGN, "args->out is not aligned to its element");
+  if (a.lse && !aligned(a.lse, 4)) return fail(QMV_ERR_ALIGN, "args->lse is not 4-byte aligned");
+  if (!std::isfinite(a.scale)) return fail(QMV_ERR_UNSUPPORTED, "args->scale must be finite");
+  if (a.out == a.q && (a.out_token != a.q_token || a.out_head != a.q_head))
+    return fail(QMV_ERR_UNSUPPORTED, "args->out is q with other strides");
+  if (meets_itself(batch->T, cache->D, a.q_heads, a.out_token, a.out_head))
+    return fail(QMV_ERR_UNSUPPORTED, "args->out holds some values more than once");
+  if (in_cache(*cache, a.out)) return fail(QMV_ERR_UNSUPPORTED, "args->out lies in the cache");
+  if (a.lse && in_cache(*cache, a.lse)) return fail(QMV_ERR_UNSUPPORTED, "args->lse lies in the cache");
+  if (a.lse && (static_cast<const void*>(a.lse) == a.q || static_cast<void*>(a.lse) == a.out))
+    return fail(QMV_ERR_UNSUPPORTED, "args->lse is the buffer of q or out");
+  const qmv::KvAttentionPlan plan = qmv::kv_attention_plan(*cache, *batch, a);
+  if (plan.bytes) {
+    if ((st = check_buffer(ws, "ws"))) return st;
+    if (ws_bytes < size_t(plan.bytes))
+      return fail(QMV_ERR_SHAPE, "ws_bytes=%llu, the call needs %lld", (unsigned long long)ws_bytes, (long long)plan.bytes);
+    const Range w{ws, plan.bytes, "ws"};
+    if ((st = check_apart(w, Range{cache->data, cache_bytes(*cache), "the cache"}))) return st;
+    if (a.lse && (st = check_apart(w, Range{a.lse, 4 * batch->T * a.q_heads, "args->lse"}))) return st;
+    if (ws == a.q || ws == a.out) return fail(QMV_ERR_UNSUPPORTED, "ws is the buffer of q or out");
+  }
+  if ((st = check_device())) return st;
+  return launched(qmv::launch_kv_attention(*cache, *batch, a, plan, static_cast<uint8_t*>(ws), as_stream(stream)),
+                  "kv_attention");
 }
 
 int qmv_rope_freqs(int64_t R, double base, const qmv_rope_scaling* scaling, float* freqs) {

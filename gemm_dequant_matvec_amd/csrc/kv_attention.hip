@@ -1,0 +1,113 @@
+// Attention over the quantised cache: how a call is cut, the join of partial
+// results, and the choice of the kernel's instance (kv_attention.h).
+#include "kv_attention.h"
+
+namespace qmv {
+namespace {
+
+constexpr int kThreads = 256;
+
+// out = sum of 2^(ref_i - ref) o_i / sum of 2^(ref_i - ref) sum_i over a row's partial results, in
+// their order.  A row has D / 4 threads.
+template <int E>
+__global__ __launch_bounds__(kThreads) void kv_join_kernel(const KvAttnArgs a) {
+  const int D = 32 * a.kv.nb, per = D >> 2, rows = kThreads / per;
+  const int mine = threadIdx.x / per, x = threadIdx.x - mine * per;
+  const int64_t end = int64_t(kv_row_start(a.kv, a.kv.B)) * a.q_heads;
+  if (mine >= rows) return;
+  for (int64_t row = int64_t(blockIdx.x) * rows + mine; row < end; row += int64_t(gridDim.x) * rows) {
+    const int token = int(row / a.q_heads), h = int(row - int64_t(token) * a.q_heads);
+    const float2* st = a.stats + row * a.slots;
+    const float* sums = a.sums + row * a.slots * D + 4 * x;
+    float ref = -kInf;
+    for (int i = 0; i < a.slots; ++i) ref = fmaxf(ref, st[i].x);
+    const float from = ref == -kInf ? 0.0f : ref;
+    f32x4 o = {0, 0, 0, 0};
+    float sum = 0.0f;
+    for (int i = 0; i < a.slots; ++i) {
+      const float2 s = st[i];
+      if (s.y == 0.0f) continue;
+      const float f = __builtin_amdgcn_exp2f(s.x - from);
+      const f32x4 v = *reinterpret_cast<const f32x4*>(sums + int64_t(i) * D);
+      sum = fmaf(s.y, f, sum);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] = fmaf(v[r], f, o[r]);
+    }
+    if (a.lse && x == 0) a.lse[row] = sum == 0.0f ? -kInf : 0.69314718f * (ref + __builtin_amdgcn_logf(sum));
+    f32x4 v = o * (1.0f / sum);
+    if (sum == 0.0f) v = f32x4{0, 0, 0, 0};
+    const int64_t to = token * a.out_token + h * a.out_head + 4 * x;
+    if constexpr (E == 0) {
+      __builtin_memcpy(static_cast<float*>(a.out) + to, &v, 16);
+    } else {
+      const u32x2 w = {pack16<E == 1>(v[0], v[1]), pack16<E == 1>(v[2], v[3])};
+      __builtin_memcpy(static_cast<uint16_t*>(a.out) + to, &w, 8);
+    }
+  }
+}
+
+// How many parts to cut `tokens` into so that `items` workgroups become about two per unit,
+// of 256 tokens at least.
+int parts(int64_t items, int64_t tokens) {
+  const int64_t want = (512 + items - 1) / items, most = std::max<int64_t>(1, (tokens + 255) / 256);
+  return int(std::min<int64_t>({want, most, 64}));
+}
+
+}  // namespace
+
+KvAttentionPlan kv_attention_plan(const qmv_kv_cache& c, const qmv_kv_batch& b, const qmv_kv_attention_args& a) {
+  KvAttentionPlan p{};
+  const int64_t group = a.q_heads / c.heads, longest = std::min<int64_t>(a.max_kv, b.columns * c.page);
+  auto cut = [&](int64_t rows, int64_t sequences, int64_t tokens, int& tiles, int& blocks, int& splits) {
+    tiles = rows > 16 ? 2 : 1;
+    blocks = int(std::min<int64_t>((rows + 16 * tiles - 1) / (16 * tiles), 65535));
+    splits = parts(c.heads * sequences * blocks, tokens);
+  };
+  const int64_t q = std::min(a.max_q, b.T);
+  int64_t own = std::max<int64_t>(1, longest - a.prefix);
+  if (a.window) own = std::min(own, a.window + q);
+  cut(q * group, b.B, own, p.tiles, p.row_blocks, p.splits);
+  if (a.prefix) {
+    cut(b.T * group, 1, std::min(longest, a.prefix), p.prefix_tiles, p.prefix_row_blocks, p.prefix_splits);
+    p.slots = p.prefix_splits + p.splits;
+  } else {
+    p.slots = p.splits > 1 ? p.splits : 0;
+  }
+  const int64_t parts = b.T * a.q_heads * p.slots;
+  p.sums_bytes = parts * c.D * 4;
+  p.bytes = p.sums_bytes + (parts * 8 + 15) / 16 * 16;
+  return p;
+}
+
+hipError_t launch_kv_attention(const qmv_kv_cache& c, const qmv_kv_batch& b, const qmv_kv_attention_args& t,
+                               const KvAttentionPlan& plan, uint8_t* ws, hipStream_t s) {
+  KvAttnArgs a{};
+  a.kv = kv_args(c, b);
+  a.q = t.q;
+  a.out = t.out;
+  a.lse = t.lse;
+  a.sums = reinterpret_cast<float*>(ws);
+  a.stats = reinterpret_cast<float2*>(ws + plan.sums_bytes);
+  a.q_token = t.q_token, a.q_head = t.q_head, a.out_token = t.out_token, a.out_head = t.out_head;
+  a.scale = t.scale * 1.44269504f;
+  a.group = int(t.q_heads / c.heads);
+  a.q_heads = int(t.q_heads);
+  // past the longest sequence a window hides nothing and a prefix shares everything
+  a.window = int(std::min<int64_t>(t.window, int64_t(1) << 30));
+  a.prefix = int(std::min<int64_t>(t.prefix, b.columns * c.page));
+  a.slots = plan.slots;
+  const bool q4 = c.fmt == QMV_Q4_0;
+  hipError_t e;
+  if (t.dtype == QMV_F32) e = q4 ? kv_attention_q4_f32(a, plan, s) : kv_attention_q8_f32(a, plan, s);
+  else if (t.dtype == QMV_F16) e = q4 ? kv_attention_q4_f16(a, plan, s) : kv_attention_q8_f16(a, plan, s);
+  else e = q4 ? kv_attention_q4_bf16(a, plan, s) : kv_attention_q8_bf16(a, plan, s);
+  if (e != hipSuccess || !plan.slots) return e;
+  const int per_block = kThreads / int(c.D / 4);
+  const dim3 grid(unsigned(std::min<int64_t>((b.T * t.q_heads + per_block - 1) / per_block, 1 << 22)));
+  if (t.dtype == QMV_F32) hipLaunchKernelGGL((kv_join_kernel<0>), grid, dim3(kThreads), 0, s, a);
+  else if (t.dtype == QMV_F16) hipLaunchKernelGGL((kv_join_kernel<1>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((kv_join_kernel<2>), grid, dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace qmv

@@ -1,0 +1,291 @@
+// Writing keys and values into the quantised cache, and reading them back.
+//
+//   d = f16(max |x| / s), q = rint(x * (1 / d))   (blocks of 32 values of a head)
+//
+// Bound by memory.  Four lanes take a block of four tokens that lie side by side in
+// a page (a group): each holds 8 dimensions of the four tokens, the block's maximum
+// of a token is a four-lane maximum, and what a lane writes (or reads) of the cache
+// is then one run of 32 bytes (Q4_0: 16): for K the dimensions 8 j .. 8 j + 7 of the
+// four tokens, for V the dimensions 4 j .. 4 j + 3 and 16 + 4 j .. of the four.  A
+// group of which the call has only some tokens (a single new token, the ends of a
+// prompt) is written in bytes, and only theirs.
+//
+// A wave takes a group of a sequence, its 16 quads the group's (head, k or v,
+// block) items.  Groups are counted so that the wave of a group follows from q_start
+// alone: sequence b starts at group q_start[b] / 4 + 2 b, which leaves room for
+// the ends of both sides, and T / 4 + 2 B groups are launched.
+#include <algorithm>
+
+#include "cache_internal.h"
+#include "rope.h"
+
+namespace qmv {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct KvHeads {  // k or v of the new tokens, or where they are read to; NULL: not wanted
+  const void* p;
+  int64_t token, head;
+};
+
+// The four tokens of a group: which are the call's, and where they lie.
+struct Group {
+  int head_at;      // bytes from the page's head to the group's set; -1: the group is not there
+  int64_t page_at;  // bytes from the cache to the page
+  int t4;           // group of the set
+  int row, from, to;  // row of token 0, tokens from .. to - 1 are the call's
+};
+
+__device__ __forceinline__ bool group_of(const KvArgs& a, int64_t v, Group& g) {
+  const int b = kv_search(a.B, v, [&](int i) { return int64_t(kv_row_start(a, i) >> 2) + 2 * int64_t(i); });
+  const int r0 = kv_row_start(a, b), r1 = max(r0, kv_row_start(a, b + 1)), n = r1 - r0;
+  const int64_t first = int64_t(a.kv_len[b]) - n;  // position of row r0
+  // groups are counted from the first position's, rounded down (also below 0)
+  const int64_t p = ((first >> 2) + (v - ((r0 >> 2) + 2 * int64_t(b)))) * 4;  // position of token 0
+  g.from = int(max(int64_t(0), first - p));
+  g.to = int(min(int64_t(4), first + n - p));
+  g.row = int(r0 + (p - first));
+  if (g.from >= g.to) return false;
+  g.head_at = -1;
+  if (p >= 0 && p < int64_t(a.columns) * a.sets * 16) {  // groups do not straddle position 0
+    int set;
+    const int page = kv_page_of(a, uint32_t(p >> 4), set);
+    const int id = a.table[b * a.stride + page];
+    if (id >= 0 && id < a.pages) {
+      g.head_at = set * a.set_bytes;
+      g.page_at = id * a.page_bytes;
+      g.t4 = int(p >> 2) & 3;
+    }
+  }
+  return true;
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, true)));
+}
+
+// Dimension of value i (0 .. 7) of lane j of a quad.
+template <bool V>
+__device__ __forceinline__ int dim_of(int j, int i) {
+  return V ? 4 * j + (i & 3) + 16 * (i >> 2) : 8 * j + i;
+}
+template <int E, bool V>
+__device__ __forceinline__ void load8_of(const typename Elem<E>::T* p, int j, float (&x)[8]) {
+  if constexpr (E == 0) {
+    float lo[4], hi[4];
+    Elem<0>::load(p + dim_of<V>(j, 0), 4, lo);
+    Elem<0>::load(p + dim_of<V>(j, 4), 4, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
+  } else {
+    uint32_t w[4];
+    __builtin_memcpy(w, p + dim_of<V>(j, 0), 8);
+    __builtin_memcpy(w + 2, p + dim_of<V>(j, 4), 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = unpack16<E == 1>(w[i] & 0xFFFFu);
+      x[2 * i + 1] = unpack16<E == 1>(w[i] >> 16);
+    }
+  }
+}
+template <int E, bool V>
+__device__ __forceinline__ void store8_of(typename Elem<E>::T* p, int j, const float (&x)[8]) {
+  if constexpr (E == 0) {
+    __builtin_memcpy(p + dim_of<V>(j, 0), x, 16);
+    __builtin_memcpy(p + dim_of<V>(j, 4), x + 4, 16);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack16<E == 1>(x[2 * i], x[2 * i + 1]);
+    __builtin_memcpy(p + dim_of<V>(j, 0), w, 8);
+    __builtin_memcpy(p + dim_of<V>(j, 4), w + 2, 8);
+  }
+}
+
+// One item: block `blk` of a head of K or V, its four tokens.  rec: the set's record.
+template <int E, bool Q4, bool V>
+__device__ __forceinline__ void write_item(const KvArgs& a, const Group& g, uint8_t* rec, const KvHeads& src, int head,
+                                           int blk, int j) {
+  constexpr int C = Q4 ? 256 : 512, W = Q4 ? 4 : 8;  // words that a lane writes
+  constexpr float kTop = Q4 ? 7.0f : 127.0f, kLow = Q4 ? -8.0f : -127.0f, kSpan = Q4 ? 7.5f : 127.0f;
+  uint32_t code[4][2];  // four tokens, 8 codes each: in Q4_0 the second word holds the high halves
+  uint32_t scale[4];
+  typedef typename Elem<E>::T T;
+  const T* p = static_cast<const T*>(src.p) + head * src.head + 32 * blk;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    float x[8];
+    const bool here = t >= g.from && t < g.to;
+    if (here) {
+      load8_of<E, V>(p + int64_t(g.row + t) * src.token, j, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    }
+    uint32_t top = 0;  // as bits: NaN > infinity > numbers
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(uint32_t, x[i]) & 0x7FFFFFFFu);
+    top = dpp_max<0x4E>(dpp_max<0xB1>(top));
+    const bool bad = top >= 0x7F800000u;
+    const _Float16 d = static_cast<_Float16>(fminf(__builtin_bit_cast(float, top) / kSpan, 65504.0f));
+    const float df = static_cast<float>(d), inv = df > 0.0f && !bad ? 1.0f / df : 0.0f;
+    scale[t] = bad ? 0x7E00u : uint32_t(__builtin_bit_cast(uint16_t, d));
+    code[t][0] = code[t][1] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = bad ? 0.0f : fminf(fmaxf(rintf(x[i] * inv), kLow), kTop);
+      code[t][i >> 2] |= uint32_t(int(q) + (Q4 ? 8 : 128)) << (8 * (i & 3));
+    }
+  }
+  const int nb = a.nb;
+  uint8_t* dst = rec + (V ? nb * C : 0) + blk * C;
+  uint8_t* sc = rec + 2 * nb * C + (V ? nb * 32 : 0) + (g.t4 * nb + blk) * 8;
+  const bool full = g.from == 0 && g.to == 4;
+  if constexpr (!V) {  // token t: W / 4 words of its 8 codes
+    dst += (16 * j + 4 * g.t4) * W;
+    uint32_t w[W];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (Q4) w[t] = code[t][0] | code[t][1] << 4;
+      else w[2 * t] = code[t][0], w[2 * t + 1] = code[t][1];
+    }
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) *reinterpret_cast<u32x4*>(dst + 4 * i) = u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (t >= g.from && t < g.to) {
+          if constexpr (Q4) *reinterpret_cast<uint32_t*>(dst + 4 * t) = w[t];
+          else *reinterpret_cast<u32x2*>(dst + 8 * t) = u32x2{w[2 * t], w[2 * t + 1]};
+        }
+    }
+  } else {  // dimension 4 j + i, then (Q8_0) 16 + 4 j + i: a word of four tokens each
+    dst += (16 * g.t4 + 4 * j) * W;
+    uint32_t w[W];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t lo = 0, hi = 0;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        lo |= (code[t][0] >> (8 * i) & 0xFFu) << (8 * t);
+        hi |= (code[t][1] >> (8 * i) & 0xFFu) << (8 * t);
+      }
+      if constexpr (Q4) w[i] = lo | hi << 4;
+      else w[2 * i] = lo, w[2 * i + 1] = hi;
+    }
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) *reinterpret_cast<u32x4*>(dst + 4 * i) = u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (t >= g.from && t < g.to) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) dst[4 * i + t] = uint8_t(w[i] >> (8 * t));
+        }
+    }
+  }
+  if (j == 0) {
+    if (full) {
+      *reinterpret_cast<u32x2*>(sc) = u32x2{scale[0] | scale[1] << 16, scale[2] | scale[3] << 16};
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (t >= g.from && t < g.to) reinterpret_cast<uint16_t*>(sc)[t] = uint16_t(scale[t]);
+    }
+  }
+}
+
+template <int E, bool Q4, bool V>
+__device__ __forceinline__ void read_item(const KvArgs& a, const Group& g, const uint8_t* rec, const KvHeads& dst, int head,
+                                          int blk, int j) {
+  constexpr int C = Q4 ? 256 : 512, W = Q4 ? 4 : 8;
+  typedef typename Elem<E>::T T;
+  T* p = static_cast<T*>(const_cast<void*>(dst.p)) + head * dst.head + 32 * blk;
+  uint32_t w[W];
+  uint32_t sw[2] = {0, 0};
+  if (rec) {
+    const int nb = a.nb;
+    const uint8_t* src = rec + (V ? nb * C : 0) + blk * C + (V ? 16 * g.t4 + 4 * j : 16 * j + 4 * g.t4) * W;
+    __builtin_memcpy(w, __builtin_assume_aligned(src, 16), 4 * W);
+    __builtin_memcpy(sw, __builtin_assume_aligned(rec + 2 * nb * C + (V ? nb * 32 : 0) + (g.t4 * nb + blk) * 8, 8), 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0;
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (t < g.from || t >= g.to) continue;
+    const float d = f16_bits_to_f32(sw[t >> 1] >> (16 * (t & 1)) & 0xFFFFu);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t q;
+      if constexpr (!V && Q4) q = w[t] >> (8 * (i & 3) + 4 * (i >> 2)) & 15u;
+      else if constexpr (!V) q = w[2 * t + (i >> 2)] >> (8 * (i & 3)) & 255u;
+      else if constexpr (Q4) q = w[i & 3] >> (8 * t + 4 * (i >> 2)) & 15u;
+      else q = w[2 * (i & 3) + (i >> 2)] >> (8 * t) & 255u;
+      x[i] = rec ? float(int(q) - (Q4 ? 8 : 128)) * d : 0.0f;
+    }
+    store8_of<E, V>(p + int64_t(g.row + t) * dst.token, j, x);
+  }
+}
+
+template <int E, bool Q4, bool WRITE>
+__global__ __launch_bounds__(kThreads) void kv_cache_kernel(const KvArgs a, const KvHeads k, const KvHeads v) {
+  const int quad = (threadIdx.x & 63) >> 2, j = threadIdx.x & 3;
+  const int64_t groups = (int64_t(a.T) >> 2) + 2 * int64_t(a.B);
+  for (int64_t n = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); n < groups; n += int64_t(gridDim.x) * 4) {
+    Group g;
+    if (!group_of(a, n, g)) continue;
+    const bool there = g.head_at >= 0;
+    if (WRITE && !there) continue;
+    const int items = a.heads * 2 * a.nb;
+    for (int it = quad; it < items; it += 16) {
+      const int hv = it / a.nb, blk = it - hv * a.nb, h = hv >> 1;
+      uint8_t* rec = there ? a.data + g.page_at + int64_t(h) * a.head_bytes + g.head_at : nullptr;
+      if constexpr (WRITE) {
+        if (hv & 1) write_item<E, Q4, true>(a, g, rec, v, h, blk, j);
+        else write_item<E, Q4, false>(a, g, rec, k, h, blk, j);
+      } else {
+        if (hv & 1) {
+          if (v.p) read_item<E, Q4, true>(a, g, rec, v, h, blk, j);
+        } else {
+          if (k.p) read_item<E, Q4, false>(a, g, rec, k, h, blk, j);
+        }
+      }
+    }
+  }
+}
+
+template <bool WRITE>
+hipError_t launch(const qmv_kv_cache& c, const qmv_kv_batch& b, const KvHeads& k, const KvHeads& v, int dtype, hipStream_t s) {
+  const KvArgs a = kv_args(c, b);
+  const int64_t groups = (b.T >> 2) + 2 * b.B;
+  const dim3 grid(unsigned(std::min<int64_t>((groups + 3) / 4, 1 << 20)));
+  auto go = [&](auto e) {
+    if (c.fmt == QMV_Q4_0) hipLaunchKernelGGL((kv_cache_kernel<decltype(e)::value, true, WRITE>), grid, dim3(kThreads), 0, s, a, k, v);
+    else hipLaunchKernelGGL((kv_cache_kernel<decltype(e)::value, false, WRITE>), grid, dim3(kThreads), 0, s, a, k, v);
+  };
+  if (dtype == QMV_F32) go(std::integral_constant<int, 0>{});
+  else if (dtype == QMV_F16) go(std::integral_constant<int, 1>{});
+  else go(std::integral_constant<int, 2>{});
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(const qmv_kv_cache& c, const qmv_kv_batch& b, const void* k, int64_t k_token, int64_t k_head,
+                           const void* v, int64_t v_token, int64_t v_head, int dtype, hipStream_t s) {
+  return launch<true>(c, b, KvHeads{k, k_token, k_head}, KvHeads{v, v_token, v_head}, dtype, s);
+}
+
+hipError_t launch_kv_read(const qmv_kv_cache& c, const qmv_kv_batch& b, void* k, int64_t k_token, int64_t k_head, void* v,
+                          int64_t v_token, int64_t v_head, int dtype, hipStream_t s) {
+  return launch<false>(c, b, KvHeads{k, k_token, k_head}, KvHeads{v, v_token, v_head}, dtype, s);
+}
+
+}  // namespace qmv
