@@ -44,12 +44,12 @@ inline KvArgs kv_args(const qmv_kv_cache& c, const qmv_kv_batch& b) {
   return a;
 }
 
-// How an attention call is cut: rows of 16 * tiles queries per workgroup, `row_blocks` of
-// them per sequence, each sequence's tokens in `splits`; the same for the shared prefix.
-// slots: partial results per row (0: the only workgroup of a row writes it).
+// How an attention call is cut: `row_blocks` workgroups share a sequence's rows (many: of the
+// kernel for more than 16 of them), each sequence's tokens go to `splits`; the same for the
+// shared prefix.  slots: partial results per row (0: the only workgroup of a row writes it).
 struct KvAttentionPlan {
-  int tiles, row_blocks, splits;
-  int prefix_tiles, prefix_row_blocks, prefix_splits;
+  bool many, prefix_many;
+  int row_blocks, splits, prefix_row_blocks, prefix_splits;
   int slots;
   int64_t sums_bytes, bytes;  // partial sums, then a reference and a weight sum of each
 };

@@ -89,83 +89,118 @@ __device__ __forceinline__ uint32_t codes16(uint32_t w, uint32_t sel) {
   return __builtin_bit_cast(uint32_t, v - b);
 }
 
-// Where q rows of this launch's tile lie.  A row r of a sequence (or, for the shared
-// prefix, of the whole call) is token r / group and head r % group of the k / v head.
-struct Row {
-  int token;   // row of q, -1: none
-  int lo, hi;  // positions that it sees
-};
-
-template <bool Q4, int E, int NB>
-struct Step {  // 32 tokens: two sets of 16 in the lane's share
-  static constexpr int W = Q4 ? 1 : 2;  // words of a lane and block
-  uint32_t k[2][NB][W], v[2][NB][W];
-  uint32_t ks[2][NB][2], vs[2][NB][2];  // four tokens' scales
-  bool there[2];
-
-  __device__ __forceinline__ void load(const KvArgs& a, int head, int i, int page, int set, int lane) {
-    constexpr int C = Q4 ? 256 : 512;
-    there[i] = page >= 0;
-    const uint8_t* p = a.data + max(page, 0) * a.page_bytes + int64_t(head) * a.head_bytes + set * a.set_bytes;
-    const uint32_t code_at = uint32_t(lane) * (4 * W), scale_at = uint32_t(lane >> 4) * (8 * NB);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) __builtin_memcpy(k[i][b], __builtin_assume_aligned(p + b * C + code_at, 4 * W), 4 * W);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-      __builtin_memcpy(ks[i][b], __builtin_assume_aligned(p + 2 * NB * C + b * 8 + scale_at, 8), 8);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-      __builtin_memcpy(v[i][b], __builtin_assume_aligned(p + (NB + b) * C + code_at, 4 * W), 4 * W);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-      __builtin_memcpy(vs[i][b], __builtin_assume_aligned(p + 2 * NB * C + NB * 32 + b * 8 + scale_at, 8), 8);
-  }
-  // operand of K's block b: the lane's token, 8 dimensions
-  __device__ __forceinline__ u32x4 k_codes(int i, int b) const {
-    if constexpr (Q4) {
-      const uint32_t lo = k[i][b][0] & 0x0F0F0F0Fu, hi = k[i][b][0] >> 4 & 0x0F0F0F0Fu;
-      return u32x4{codes16<8>(lo, 0x04010400u), codes16<8>(lo, 0x04030402u), codes16<8>(hi, 0x04010400u),
-                   codes16<8>(hi, 0x04030402u)};
-    } else {
-      return u32x4{codes16<128>(k[i][b][0], 0x04010400u), codes16<128>(k[i][b][0], 0x04030402u),
-                   codes16<128>(k[i][b][1], 0x04010400u), codes16<128>(k[i][b][1], 0x04030402u)};
-    }
-  }
-  // operand of V's block b, dimensions 16 m .. 16 m + 15: the lane's dimension, 4 + 4 tokens
-  __device__ __forceinline__ u32x4 v_codes(int b, int m) const {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if constexpr (Q4) w[i] = v[i][b][0] >> (4 * m) & 0x0F0F0F0Fu;
-      else w[i] = v[i][b][m];
-    }
-    constexpr int BIAS = Q4 ? 8 : 128;
-    return u32x4{codes16<BIAS>(w[0], 0x04010400u), codes16<BIAS>(w[0], 0x04030402u), codes16<BIAS>(w[1], 0x04010400u),
-                 codes16<BIAS>(w[1], 0x04030402u)};
-  }
-};
-
-__device__ __forceinline__ float half_of(const uint32_t (&w)[2], int r) {
-  return f16_bits_to_f32(w[r >> 1] >> (16 * (r & 1)) & 0xFFFFu);
+__device__ __forceinline__ float half_of(u32x2 w, int r) {
+  const uint32_t bits = w[r >> 1];
+  return f16_bits_to_f32(bits >> (16 * (r & 1)) & 0xFFFFu);
 }
 
-template <bool Q4, int E, int NB, int TILES, bool PREFIX>
-struct Attend {
+// A row of q: token r / group and head r % group of the k / v head, for row r of a sequence
+// (or, for the shared prefix, of the whole call).
+struct Row {
+  int token;   // row of q, -1: none
+  int head;    // of q
+  int lo, hi;  // positions that it sees, lo .. hi - 1
+};
+
+template <bool PREFIX>
+__device__ __forceinline__ Row row_of(const KvAttnArgs& a, uint32_t r, uint32_t rows, int kv_head, int first_row,
+                                      int64_t first_pos, int from, int64_t cap) {
+  if (r >= rows) return Row{-1, 0, 0, 0};
+  const int i = int(r / uint32_t(a.group));
+  Row w;
+  w.token = first_row + i;
+  w.head = kv_head * a.group + int(r) - i * a.group;
+  int64_t pos;
+  if constexpr (PREFIX) {  // its sequence by bisection
+    int x = 0, n = a.kv.B;
+    while (n > 1) {
+      const int h = n >> 1;
+      if (kv_row_start(a.kv, x + h) <= w.token) x += h, n -= h;
+      else n = h;
+    }
+    const int end = kv_row_start(a.kv, x + 1);
+    if (w.token < kv_row_start(a.kv, x) || w.token >= end) return Row{-1, 0, 0, 0};
+    pos = int64_t(a.kv.kv_len[x]) - end + w.token;
+  } else {
+    pos = first_pos + i;
+  }
+  const int64_t lo = a.window ? max(int64_t(0), pos - a.window + 1) : 0;
+  w.lo = int(min(max(lo, int64_t(from)), cap));
+  w.hi = int(max(int64_t(0), min(pos + 1, cap)));
+  return w;
+}
+
+// The rows and positions that a workgroup works on: a sequence's own, or the prefix's.
+struct Span {
+  int kv_head, split, r0;
+  uint32_t rows;
+  int64_t first_pos, cap;
+  const int32_t* table;
+};
+template <bool PREFIX>
+__device__ __forceinline__ Span span_of(const KvAttnArgs& a, int splits) {
+  const KvArgs& kv = a.kv;
+  Span s;
+  const int item = blockIdx.x / kv.heads, b = PREFIX ? 0 : item / splits;
+  s.kv_head = blockIdx.x - item * kv.heads;
+  s.split = item - b * splits;
+  s.r0 = PREFIX ? 0 : kv_row_start(kv, b);
+  const int r1 = PREFIX ? kv_row_start(kv, kv.B) : max(s.r0, kv_row_start(kv, b + 1));
+  s.rows = uint32_t(r1 - s.r0) * uint32_t(a.group);  // below 2^31
+  const int64_t cap = int64_t(kv.columns) * kv.sets * 16;
+  s.cap = PREFIX ? min(cap, int64_t(a.prefix)) : cap;
+  s.first_pos = PREFIX ? 0 : int64_t(kv.kv_len[b]) - (r1 - s.r0);
+  s.table = kv.table + (PREFIX ? 0 : b * kv.stride);
+  return s;
+}
+
+// What a split takes of the sets s0 .. s1 - 1: [u0, u1).  Shares are whole steps of `unit`
+// sets, and 256 tokens at least, so that short sequences end with fewer parts.
+__device__ __forceinline__ void share_of(int s0, int s1, int splits, int split, int unit, int& u0, int& u1) {
+  const int share = (max((s1 - s0 + splits - 1) / splits, 16) + unit - 1) / unit * unit;
+  u0 = int(min(int64_t(s1), s0 + int64_t(split) * share));
+  u1 = min(s1, u0 + share);
+}
+
+// 16 * TILES queries of a wave: operands, running reference, sum and accumulator.
+template <int E, int NB, int TILES>
+struct Rows {
   static constexpr int QP = E == 0 ? 2 : 1;  // f16 parts of q
   static constexpr int PP = E == 2 ? 1 : 2;  // of a probability times scale
-  typedef Step<Q4, E, NB> St;
 
   u32x4 q[TILES][NB][QP];
   f32x4 o[TILES][NB][2];
   float factor[TILES], ref[TILES], sum[TILES];
   int lo[TILES], hi[TILES];
-  int all_lo, all_hi;  // every row of the workgroup sees all_lo .. all_hi - 1
+  int all_lo, all_hi;  // every row sees all_lo .. all_hi - 1
+  int any_lo, any_hi;  // no row sees anything outside any_lo .. any_hi - 1
 
-  __device__ __forceinline__ void load_q(const KvAttnArgs& a, int tile, const Row& row, int head, int lane) {
+  __device__ __forceinline__ void load(const KvAttnArgs& a, const Row (&row)[TILES], int lane) {
+    int most_lo = 0, least_hi = 0x7FFFFFFF, least_lo = 0x7FFFFFFF, most_hi = 0;
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+      if (row[j].token >= 0) {
+        most_lo = max(most_lo, row[j].lo);
+        least_hi = min(least_hi, row[j].hi);
+        if (row[j].lo < row[j].hi) {
+          least_lo = min(least_lo, row[j].lo);
+          most_hi = max(most_hi, row[j].hi);
+        }
+      }
+      load_q(a, j, row[j], lane);
+    }
+    all_lo = wave_max(most_lo);
+    all_hi = -wave_max(-least_hi);
+    any_lo = -wave_max(-least_lo);
+    any_hi = wave_max(most_hi);
+    if (any_lo >= any_hi) any_lo = any_hi = 0;
+  }
+
+  __device__ __forceinline__ void load_q(const KvAttnArgs& a, int j, const Row& row, int lane) {
     float x[NB][8];
     uint32_t top = 0;
     if (row.token >= 0) {
-      const int64_t at = row.token * a.q_token + head * a.q_head + 8 * (lane >> 4);
+      const int64_t at = row.token * a.q_token + row.head * a.q_head + 8 * (lane >> 4);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         if constexpr (E == 0) {
@@ -195,37 +230,32 @@ struct Attend {
     // 2^up brings the largest value to [2^14, 2^15); up to 2^126 for f32 that are next to nothing
     const int up = min(126, 14 - (int(top >> 23) - 127));
     const float scale = __builtin_bit_cast(float, uint32_t(127 + up) << 23);
-    factor[tile] = top >= 0x7F800000u ? __builtin_nanf("") : a.scale * __builtin_bit_cast(float, uint32_t(127 - up) << 23);
+    factor[j] = top >= 0x7F800000u ? __builtin_nanf("") : a.scale * __builtin_bit_cast(float, uint32_t(127 - up) << 23);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      float lowp[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[b][i] *= scale;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t w = pack16<true>(x[b][2 * i], x[b][2 * i + 1]);
-        q[tile][b][0][i] = w;
-        lowp[2 * i] = x[b][2 * i] - unpack16<true>(w & 0xFFFFu);
-        lowp[2 * i + 1] = x[b][2 * i + 1] - unpack16<true>(w >> 16);
-      }
-      if constexpr (QP == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[tile][b][1][i] = pack16<true>(lowp[2 * i], lowp[2 * i + 1]);
+        const float y = x[b][2 * i] * scale, z = x[b][2 * i + 1] * scale;
+        const uint32_t w = pack16<true>(y, z);
+        q[j][b][0][i] = w;
+        if constexpr (QP == 2) q[j][b][1][i] = pack16<true>(y - unpack16<true>(w & 0xFFFFu), z - unpack16<true>(w >> 16));
       }
     }
-    lo[tile] = row.token >= 0 ? row.lo : 0;
-    hi[tile] = row.token >= 0 ? row.hi : 0x7FFFFFFF;
-    ref[tile] = -kInf;
-    sum[tile] = 0.0f;
+    lo[j] = row.token >= 0 ? row.lo : 0;
+    hi[j] = row.token >= 0 ? row.hi : 0x7FFFFFFF;
+    ref[j] = -kInf;
+    sum[j] = 0.0f;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) o[tile][b][m] = f32x4{0, 0, 0, 0};
+      for (int m = 0; m < 2; ++m) o[j][b][m] = f32x4{0, 0, 0, 0};
   }
 
-  // 32 tokens from position `at`; MASK: some row may not see all of them
-  template <bool MASK>
-  __device__ __forceinline__ void step(const St& t, int at, int lane) {
+  // 32 tokens from position `at`; MASK: some row may not see all of them; there0, there1: the
+  // page of the first, second 16 is there.  T gives the operands k(i, b), v(b, m) and the scales
+  // ks(i, b), vs(i, b).
+  template <bool MASK, class T>
+  __device__ __forceinline__ void step(const T& t, int at, bool there0, bool there1, int lane) {
     const int quad = lane >> 4;
     f32x4 s[TILES][2];
     bool seen[TILES][2][4];
@@ -237,22 +267,25 @@ struct Attend {
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const u32x4 k = t.k_codes(i, b);
+        const u32x4 k = t.k(i, b);
+        const u32x2 ks = t.ks(i, b);
 #pragma unroll
         for (int j = 0; j < TILES; ++j) {
           f32x4 d = mfma16<true>(k, q[j][b][0], f32x4{0, 0, 0, 0});
           if constexpr (QP == 2) d = mfma16<true>(k, q[j][b][1], d);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) s[j][i][r] = fmaf(d[r], half_of(t.ks[i][b], r), s[j][i][r]);
+          for (int r = 0; r < 4; ++r) s[j][i][r] = fmaf(d[r], half_of(ks, r), s[j][i][r]);
         }
       }
+    u32x2 vs[2][NB];
     uint32_t top_scale = 0;
-    if constexpr (!MASK) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) top_scale = max_u16(top_scale, max_u16(t.vs[i][b][0], t.vs[i][b][1]));
-    }
+      for (int b = 0; b < NB; ++b) {
+        vs[i][b] = t.vs(i, b);
+        if constexpr (!MASK) top_scale = max_u16(top_scale, max_u16(vs[i][b][0], vs[i][b][1]));
+      }
 #pragma unroll
     for (int j = 0; j < TILES; ++j) {
       uint32_t top_v = top_scale;
@@ -263,11 +296,13 @@ struct Attend {
           s[j][i][r] *= factor[j];
           if constexpr (MASK) {
             const int p = at + 16 * i + 4 * quad + r;
-            seen[j][i][r] = t.there[i] && p >= lo[j] && p < hi[j];
+            seen[j][i][r] = (i ? there1 : there0) && p >= lo[j] && p < hi[j];
             s[j][i][r] = seen[j][i][r] ? s[j][i][r] : -kInf;
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-              top_v = max(top_v, seen[j][i][r] ? t.vs[i][b][r >> 1] >> (16 * (r & 1)) & 0xFFFFu : 0u);
+            for (int b = 0; b < NB; ++b) {
+              const uint32_t w = vs[i][b][r >> 1];
+              top_v = max(top_v, seen[j][i][r] ? w >> (16 * (r & 1)) & 0xFFFFu : 0u);
+            }
           }
         }
       if constexpr (!MASK) top_v = max(top_v & 0xFFFFu, top_v >> 16);
@@ -302,7 +337,7 @@ struct Attend {
     // s is p now; what a row does not see is zero, whatever its scale
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const u32x4 v0 = t.v_codes(b, 0), v1 = t.v_codes(b, 1);
+      const u32x4 v0 = t.v(b, 0), v1 = t.v(b, 1);
 #pragma unroll
       for (int j = 0; j < TILES; ++j) {
         float pv[8];
@@ -310,16 +345,16 @@ struct Attend {
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            float sv = half_of(t.vs[i][b], r);
+            float sv = half_of(vs[i][b], r);
             if constexpr (MASK) sv = seen[j][i][r] ? sv : 0.0f;
             pv[4 * i + r] = s[j][i][r] * sv;
           }
         u32x4 p, pl;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          p[i] = pack16<true>(pv[2 * i], pv[2 * i + 1]);
-          if constexpr (PP == 2)
-            pl[i] = pack16<true>(pv[2 * i] - unpack16<true>(p[i] & 0xFFFFu), pv[2 * i + 1] - unpack16<true>(p[i] >> 16));
+          const uint32_t w = pack16<true>(pv[2 * i], pv[2 * i + 1]);
+          p[i] = w;
+          if constexpr (PP == 2) pl[i] = pack16<true>(pv[2 * i] - unpack16<true>(w & 0xFFFFu), pv[2 * i + 1] - unpack16<true>(w >> 16));
         }
         o[j][b][0] = mfma16<true>(v0, p, o[j][b][0]);
         o[j][b][1] = mfma16<true>(v1, p, o[j][b][1]);
@@ -330,210 +365,340 @@ struct Attend {
       }
     }
   }
+  template <class T>
+  __device__ __forceinline__ void work(const T& t, int at, bool there0, bool there1, int lane) {
+    if (there0 && there1 && at >= all_lo && at + 32 <= all_hi) step<false>(t, at, true, true, lane);
+    else step<true>(t, at, there0, there1, lane);
+  }
+
+  // A tile's result, its sum already that of the whole column: final, or a part for the join.
+  __device__ __forceinline__ void store(const KvAttnArgs& a, int j, const Row& row, int slot, int lane) {
+    if (row.token < 0) return;
+    const int64_t at = row.token * int64_t(a.q_heads) + row.head;
+    if (a.slots) {
+      const int64_t part = at * a.slots + slot;
+      if (lane < 16) a.stats[part] = make_float2(ref[j], sum[j]);
+      if (sum[j] != 0.0f) {  // nothing seen: the join does not look at it
+#pragma unroll
+        for (int i = 0; i < NB * 2; ++i)
+          *reinterpret_cast<f32x4*>(a.sums + part * (32 * NB) + 16 * i + 4 * (lane >> 4)) = o[j][i >> 1][i & 1];
+      }
+      return;
+    }
+    const float inv = 1.0f / sum[j];
+    if (a.lse && lane < 16)
+      a.lse[at] = sum[j] == 0.0f ? -kInf : 0.69314718f * (ref[j] + __builtin_amdgcn_logf(sum[j]));
+    const int64_t to = row.token * a.out_token + row.head * a.out_head + 4 * (lane >> 4);
+#pragma unroll
+    for (int i = 0; i < NB * 2; ++i) {
+      f32x4 v = o[j][i >> 1][i & 1] * inv;
+      if (sum[j] == 0.0f) v = f32x4{0, 0, 0, 0};
+      if constexpr (E == 0) {
+        __builtin_memcpy(static_cast<float*>(a.out) + to + 16 * i, &v, 16);
+      } else {
+        const u32x2 x = {pack16<E == 1>(v[0], v[1]), pack16<E == 1>(v[2], v[3])};
+        __builtin_memcpy(static_cast<uint16_t*>(a.out) + to + 16 * i, &x, 8);
+      }
+    }
+  }
 };
 
-// Row r of the tile: its token and the positions it sees in [from, to).
-template <bool PREFIX>
-__device__ __forceinline__ Row row_of(const KvAttnArgs& a, uint32_t r, uint32_t rows, int first_row, int64_t first_pos,
-                                      int from, int64_t cap) {
-  Row w{-1, 0, 0};
-  if (r >= rows) return w;
-  const int i = int(r / uint32_t(a.group));
-  int64_t pos;
-  w.token = first_row + i;
-  if constexpr (PREFIX) {  // its sequence by bisection
-    int x = 0, n = a.kv.B;
-    while (n > 1) {
-      const int h = n >> 1;
-      if (kv_row_start(a.kv, x + h) <= w.token) x += h, n -= h;
-      else n = h;
-    }
-    const int end = kv_row_start(a.kv, x + 1);
-    if (w.token < kv_row_start(a.kv, x) || w.token >= end) return Row{-1, 0, 0};
-    pos = int64_t(a.kv.kv_len[x]) - end + w.token;
-  } else {
-    pos = first_pos + i;
-  }
-  const int64_t lo = a.window ? max(int64_t(0), pos - a.window + 1) : 0;
-  w.lo = int(min(max(lo, int64_t(from)), cap));
-  w.hi = int(max(int64_t(0), min(pos + 1, cap)));
-  return w;
-}
+// Two sets in LDS as they are in the cache, and their codes as f16 operands.
+template <bool Q4, int NB>
+struct Raw {
+  static constexpr int C = Q4 ? 256 : 512, kSet = NB * (2 * C + 64), kPieces = kSet / 16;
+  static constexpr int W = Q4 ? 1 : 2;  // words of a lane and block
+  const u32x4* at;                      // kPieces each
+  int lane;
 
+  __device__ __forceinline__ const uint8_t* bytes(int i) const { return reinterpret_cast<const uint8_t*>(at + i * kPieces); }
+  // of K's block b: the lane's token, 8 dimensions
+  __device__ __forceinline__ u32x4 k(int i, int b) const {
+    uint32_t w[W];
+    __builtin_memcpy(w, __builtin_assume_aligned(bytes(i) + b * C + lane * (4 * W), 4 * W), 4 * W);
+    if constexpr (Q4) {
+      const uint32_t lo = w[0] & 0x0F0F0F0Fu, hi = w[0] >> 4 & 0x0F0F0F0Fu;
+      return u32x4{codes16<8>(lo, 0x04010400u), codes16<8>(lo, 0x04030402u), codes16<8>(hi, 0x04010400u),
+                   codes16<8>(hi, 0x04030402u)};
+    } else {
+      return u32x4{codes16<128>(w[0], 0x04010400u), codes16<128>(w[0], 0x04030402u), codes16<128>(w[1], 0x04010400u),
+                   codes16<128>(w[1], 0x04030402u)};
+    }
+  }
+  // of V's block b, dimensions 16 m .. 16 m + 15: the lane's dimension, 4 + 4 tokens
+  __device__ __forceinline__ u32x4 v(int b, int m) const {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t x[W];
+      __builtin_memcpy(x, __builtin_assume_aligned(bytes(i) + (NB + b) * C + lane * (4 * W), 4 * W), 4 * W);
+      if constexpr (Q4) w[i] = x[0] >> (4 * m) & 0x0F0F0F0Fu;
+      else w[i] = x[m];
+    }
+    constexpr int BIAS = Q4 ? 8 : 128;
+    return u32x4{codes16<BIAS>(w[0], 0x04010400u), codes16<BIAS>(w[0], 0x04030402u), codes16<BIAS>(w[1], 0x04010400u),
+                 codes16<BIAS>(w[1], 0x04030402u)};
+  }
+  __device__ __forceinline__ u32x2 scales(int i, int plane, int b) const {
+    return *reinterpret_cast<const u32x2*>(bytes(i) + NB * (2 * C + 32 * plane) + ((lane >> 4) * NB + b) * 8);
+  }
+  __device__ __forceinline__ u32x2 ks(int i, int b) const { return scales(i, 0, b); }
+  __device__ __forceinline__ u32x2 vs(int i, int b) const { return scales(i, 1, b); }
+
+  // Starts copies of set `set` of page `page` (0 for one that is not there) to dst: kCopies of them.
+  static constexpr int kCopies = (kPieces + 63) / 64;
+  static __device__ __forceinline__ void copy(const KvArgs& a, int head, int page, int set, u32x4* dst, int lane) {
+    const Buf src = buffer_of(a.data + max(page, 0) * a.page_bytes + int64_t(head) * a.head_bytes + set * a.set_bytes);
+#pragma unroll
+    for (int c = 0; c < kPieces / 64; ++c) copy_to_lds(src, lane * 16, c * 1024, dst + c * 64);
+    if constexpr (kPieces % 64 != 0)
+      if (lane < kPieces % 64) copy_to_lds(src, lane * 16, kPieces / 64 * 1024, dst + kPieces / 64 * 64);
+  }
+};
+
+// Pages of the next 32 steps: lane 2 n + i holds the page and place of set i of step n.
+struct Ahead {
+  int pages, places;
+  // step n: sets first + stride n and the next, up to end
+  __device__ __forceinline__ void look_up(const KvArgs& kv, const int32_t* table, int first, int stride, int n0, int end,
+                                          int lane) {
+    const int64_t u = first + int64_t(stride) * (n0 + (lane >> 1)) + (lane & 1);
+    int set, page = -1;
+    const int p = kv_page_of(kv, uint32_t(min(u, int64_t(end - 1))), set);
+    if (u < end) {
+      page = table[p];
+      if (page < 0 || page >= kv.pages) page = -1;
+    }
+    pages = page;
+    places = set;
+  }
+  __device__ __forceinline__ int page(int n, int i) const { return __builtin_amdgcn_readlane(pages, 2 * (n & 31) + i); }
+  __device__ __forceinline__ int place(int n, int i) const { return __builtin_amdgcn_readlane(places, 2 * (n & 31) + i); }
+};
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {  // until at most N are under way
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// What this wave has read of LDS has arrived: copies may overwrite it.
+__device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Up to 16 queries at a time: every wave has tokens of its own, 32 of them under way to its
+// part of LDS while it works on 32 others; no barrier before the waves meet.
 // grid: (k / v heads * splits * sequences (1 for the prefix), row blocks)
-template <bool Q4, int E, int NB, int TILES, bool PREFIX>
-__global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a, int splits, int first_slot) {
-  typedef Attend<Q4, E, NB, TILES, PREFIX> At;
-  typedef typename At::St St;
-  __shared__ f32x4 meet[3][NB * 2][64];
+template <bool Q4, int E, int NB, bool PREFIX>
+__global__ __launch_bounds__(256, 2) void kv_attention_few_kernel(const KvAttnArgs a, int splits, int first_slot) {
+  typedef Raw<Q4, NB> R;
+  constexpr int kStep = 2 * R::kPieces, kMeet = 3 * NB * 2 * 64;  // 16-byte pieces
+  __shared__ u32x4 ring0[kStep * 4 > kMeet ? kStep * 4 : kMeet], ring1[kStep * 4];
   __shared__ float2 meet_stats[3][64];
-  constexpr int kRows = 16 * TILES;
   const KvArgs& kv = a.kv;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int item = blockIdx.x / kv.heads, head = blockIdx.x - item * kv.heads;
-  const int b = PREFIX ? 0 : item / splits, split = item - b * splits;
-  const int r0 = PREFIX ? 0 : kv_row_start(kv, b);
-  const int r1 = PREFIX ? kv_row_start(kv, kv.B) : max(r0, kv_row_start(kv, b + 1));
-  const uint32_t rows = uint32_t(r1 - r0) * uint32_t(a.group);  // below 2^31
-  const int64_t cap64 = int64_t(kv.columns) * kv.sets * 16;
-  const int64_t cap = PREFIX ? min(cap64, int64_t(a.prefix)) : cap64;
-  const int64_t first_pos = PREFIX ? 0 : int64_t(kv.kv_len[b]) - (r1 - r0);
-  const int32_t* table = kv.table + (PREFIX ? 0 : b * kv.stride);
-
-  for (uint32_t base = blockIdx.y * kRows; base < rows; base += gridDim.y * kRows) {
-    At w;
-    int most_lo = 0, least_hi = 0x7FFFFFFF, least_lo = 0x7FFFFFFF, most_hi = 0;
-    Row row[TILES];
-    int row_head[TILES];
+  const Span sp = span_of<PREFIX>(a, splits);
+  for (uint32_t base = blockIdx.y * 16; base < sp.rows; base += gridDim.y * 16) {
+    Row row[1] = {row_of<PREFIX>(a, base + (lane & 15), sp.rows, sp.kv_head, sp.r0, sp.first_pos, PREFIX ? 0 : a.prefix, sp.cap)};
+    Rows<E, NB, 1> w;
+    w.load(a, row, lane);
+    int u0, u1;
+    share_of(w.any_lo >> 4, (w.any_hi + 15) >> 4, splits, sp.split, 8, u0, u1);
+    const int first = u0 + 2 * wave, steps = u1 > first ? (u1 - first + 7) >> 3 : 0;  // sets first + 8 n and the next
+    Ahead ahead;
+    auto fetch = [&](u32x4* ring, int n) {
+      lds_read();
+      if ((n & 31) == 0) ahead.look_up(kv, sp.table, first, 8, n, u1, lane);
 #pragma unroll
-    for (int j = 0; j < TILES; ++j) {
-      const uint32_t r = base + 16 * j + (lane & 15);
-      row[j] = row_of<PREFIX>(a, r, rows, r0, first_pos, PREFIX ? 0 : a.prefix, cap);
-      if (row[j].token >= 0) {
-        most_lo = max(most_lo, row[j].lo);
-        least_hi = min(least_hi, row[j].hi);
-        if (row[j].lo < row[j].hi) {
-          least_lo = min(least_lo, row[j].lo);
-          most_hi = max(most_hi, row[j].hi);
-        }
-      }
-      row_head[j] = head * a.group + int(r % uint32_t(a.group));
-      w.load_q(a, j, row[j], row_head[j], lane);
-    }
-    w.all_lo = wave_max(most_lo);
-    w.all_hi = -wave_max(-least_hi);
-    least_lo = -wave_max(-least_lo);
-    most_hi = wave_max(most_hi);
-    // the sets of 16 tokens that any row sees, and this split's share of them: whole steps of all waves
-    const int s0 = least_lo < most_hi ? least_lo >> 4 : 0, s1 = least_lo < most_hi ? (most_hi + 15) >> 4 : 0;
-    const int share = ((s1 - s0 + splits - 1) / splits + 7) & ~7;
-    const int u0 = s0 + split * share, u1 = min(s1, u0 + share);
-    const int steps = u1 > u0 + 2 * wave ? (u1 - u0 - 2 * wave + 7) >> 3 : 0;  // of this wave: sets u0 + 2 wave + 8 n
-
-    // pages of the wave's next 32 steps: lane 2 n + i holds the page of set i of step n
-    int pages = -1, places = 0;
-    auto look_up = [&](int n0) {
-      const int u = u0 + 2 * wave + 8 * (n0 + (lane >> 1)) + (lane & 1);
-      int set, page = -1;
-      const int p = kv_page_of(kv, uint32_t(min(u, s1 - 1)), set);
-      if (u < u1) {
-        page = table[p];
-        if (page < 0 || page >= kv.pages) page = -1;
-      }
-      pages = page;
-      places = set;
-    };
-    auto fetch = [&](St& t, int n) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int l = 2 * (n & 31) + i;
-        t.load(kv, head, i, __builtin_amdgcn_readlane(pages, l), __builtin_amdgcn_readlane(places, l), lane);
-      }
-    };
-    auto work = [&](const St& t, int n) {
-      const int at = (u0 + 2 * wave + 8 * n) * 16;
-      if (t.there[0] && t.there[1] && at >= w.all_lo && at + 32 <= w.all_hi) w.template step<false>(t, at, lane);
-      else w.template step<true>(t, at, lane);
+      for (int i = 0; i < 2; ++i)
+        R::copy(kv, sp.kv_head, ahead.page(n, i), ahead.place(n, i), ring + wave * kStep + i * R::kPieces, lane);
     };
     if (steps > 0) {
-      look_up(0);
-      St one, two;
-      fetch(one, 0);
+      fetch(ring0, 0);
+      bool a0 = ahead.page(0, 0) >= 0, a1 = ahead.page(0, 1) >= 0;
       for (int n = 0; n < steps; n += 2) {
-        if (n + 1 < steps) fetch(two, n + 1);
-        work(one, n);
-        if (n + 2 < steps) {
-          if (((n + 2) & 31) == 0) look_up(n + 2);
-          fetch(one, n + 2);
+        bool b0 = false, b1 = false;
+        if (n + 1 < steps) {
+          fetch(ring1, n + 1);
+          b0 = ahead.page(n + 1, 0) >= 0, b1 = ahead.page(n + 1, 1) >= 0;
+          wait_copies<2 * R::kCopies>();
+        } else {
+          wait_copies<0>();
         }
-        if (n + 1 < steps) work(two, n + 1);
+        w.work(R{ring0 + wave * kStep, lane}, (first + 8 * n) * 16, a0, a1, lane);
+        if (n + 1 >= steps) break;
+        if (n + 2 < steps) {
+          fetch(ring0, n + 2);
+          a0 = ahead.page(n + 2, 0) >= 0, a1 = ahead.page(n + 2, 1) >= 0;
+          wait_copies<2 * R::kCopies>();
+        } else {
+          wait_copies<0>();
+        }
+        w.work(R{ring1 + wave * kStep, lane}, (first + 8 * (n + 1)) * 16, b0, b1, lane);
       }
     }
 
-    // the four waves meet: wave j % 4 joins tile j
+    // the four waves meet: the first adds the others' results to its own
+    w.sum[0] = column_sum(w.sum[0]);
+    f32x4* meet = reinterpret_cast<f32x4*>(ring0);
+    __syncthreads();
+    if (wave) {
+#pragma unroll
+      for (int i = 0; i < NB * 2; ++i) meet[((wave - 1) * NB * 2 + i) * 64 + lane] = w.o[0][i >> 1][i & 1];
+      meet_stats[wave - 1][lane] = make_float2(w.ref[0], w.sum[0]);
+    }
+    __syncthreads();
+    if (!wave) {
+      float ref = w.ref[0];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) ref = fmaxf(ref, meet_stats[k][lane].x);
+      const float from = ref == -kInf ? 0.0f : ref, f = __builtin_amdgcn_exp2f(w.ref[0] - from);
+      w.ref[0] = ref;
+      w.sum[0] *= f;
+#pragma unroll
+      for (int i = 0; i < NB * 2; ++i) w.o[0][i >> 1][i & 1] *= f;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const float2 st = meet_stats[k][lane];
+        const float g = __builtin_amdgcn_exp2f(st.x - from);
+        w.sum[0] = fmaf(st.y, g, w.sum[0]);
+#pragma unroll
+        for (int i = 0; i < NB * 2; ++i) {
+          const f32x4 v = meet[(k * NB * 2 + i) * 64 + lane];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w.o[0][i >> 1][i & 1][r] = fmaf(v[r], g, w.o[0][i >> 1][i & 1][r]);
+        }
+      }
+      w.store(a, 0, row[0], first_slot + sp.split, lane);
+    }
+    __syncthreads();  // the next rows' tokens go where the results were
+  }
+}
+
+// A step's operands in LDS, converted once for the four waves.
+template <int NB>
+struct Ready {
+  u32x4 kc[2][NB][64], vc[NB][2][64];
+  u32x2 sc[2][2][4 * NB];  // set, K or V, (group of tokens, block)
+};
+template <int NB>
+struct ReadyView {
+  const Ready<NB>* r;
+  int lane;
+  __device__ __forceinline__ u32x4 k(int i, int b) const { return r->kc[i][b][lane]; }
+  __device__ __forceinline__ u32x4 v(int b, int m) const { return r->vc[b][m][lane]; }
+  __device__ __forceinline__ u32x2 ks(int i, int b) const { return r->sc[i][0][(lane >> 4) * NB + b]; }
+  __device__ __forceinline__ u32x2 vs(int i, int b) const { return r->sc[i][1][(lane >> 4) * NB + b]; }
+};
+
+// Many queries: each of the four waves has 16 * TILES rows of its own and all work on the
+// same 32 tokens.  A step's bytes are copied to LDS two steps ahead, its codes are turned
+// into operands, a quarter by each wave, one step ahead; one barrier a step.
+template <bool Q4, int E, int NB, int TILES, bool PREFIX>
+__global__ __launch_bounds__(256, 2) void kv_attention_many_kernel(const KvAttnArgs a, int splits, int first_slot) {
+  typedef Raw<Q4, NB> R;
+  constexpr int kStep = 2 * R::kPieces, kRows = 64 * TILES;
+  __shared__ u32x4 raw0[kStep], raw1[kStep];
+  __shared__ Ready<NB> ready0, ready1;
+  __shared__ int range[4][2];
+  const KvArgs& kv = a.kv;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Span sp = span_of<PREFIX>(a, splits);
+  for (uint32_t base = blockIdx.y * kRows; base < sp.rows; base += gridDim.y * kRows) {
+    Row row[TILES];
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+      row[j] = row_of<PREFIX>(a, base + wave * (16 * TILES) + 16 * j + (lane & 15), sp.rows, sp.kv_head, sp.r0, sp.first_pos,
+                              PREFIX ? 0 : a.prefix, sp.cap);
+    Rows<E, NB, TILES> w;
+    w.load(a, row, lane);
+    if (lane == 0) range[wave][0] = w.any_lo < w.any_hi ? w.any_lo : 0x7FFFFFFF, range[wave][1] = w.any_hi;
+    __syncthreads();
+    const int lo = min(min(range[0][0], range[1][0]), min(range[2][0], range[3][0]));
+    const int hi = max(max(range[0][1], range[1][1]), max(range[2][1], range[3][1]));
+    int u0, u1;
+    share_of(__builtin_amdgcn_readfirstlane(lo < hi ? lo >> 4 : 0), __builtin_amdgcn_readfirstlane(lo < hi ? (hi + 15) >> 4 : 0),
+             splits, sp.split, 2, u0, u1);
+    const int steps = u1 > u0 ? (u1 - u0 + 1) >> 1 : 0;
+    Ahead ahead;
+    int flags = 0;  // bit 2 (n % 4) + i: set i of step n is there
+    // wave w copies half w % 2 of set w / 2
+    auto fetch = [&](u32x4* raw, int n) {
+      if ((n & 31) == 0) ahead.look_up(kv, sp.table, u0, 2, n, u1, lane);
+      const int i = wave >> 1, part = wave & 1, p0 = ahead.page(n, 0), p1 = ahead.page(n, 1);
+      flags &= ~(3 << 2 * (n & 3));
+      flags |= (int(p0 >= 0) | int(p1 >= 0) << 1) << 2 * (n & 3);
+      const Buf src = buffer_of(kv.data + max(i ? p1 : p0, 0) * kv.page_bytes + int64_t(sp.kv_head) * kv.head_bytes +
+                                (i ? ahead.place(n, 1) : ahead.place(n, 0)) * kv.set_bytes);
+      constexpr int kHalf = R::kPieces / 2;  // kPieces is even
+      u32x4* dst = raw + i * R::kPieces + part * kHalf;
+#pragma unroll
+      for (int c = 0; c < kHalf / 64; ++c) copy_to_lds(src, lane * 16, (part * kHalf + c * 64) * 16, dst + c * 64);
+      if constexpr (kHalf % 64 != 0)
+        if (lane < kHalf % 64) copy_to_lds(src, lane * 16, (part * kHalf + kHalf / 64 * 64) * 16, dst + kHalf / 64 * 64);
+    };
+    // K's operands by set and block, then V's, in turn among the waves
+    auto convert = [&](const u32x4* raw, Ready<NB>& to) {
+      const R from{raw, lane};
+#pragma unroll
+      for (int x = 0; x < NB; ++x) {
+        const int y = 4 * x + wave;  // 0 .. 4 NB - 1
+        if (y < 2 * NB) to.kc[y & 1][y >> 1][lane] = from.k(y & 1, y >> 1);
+        else to.vc[(y - 2 * NB) >> 1][y & 1][lane] = from.v((y - 2 * NB) >> 1, y & 1);
+      }
+      const int i = wave >> 1, plane = wave & 1;
+      if (lane < 4 * NB)
+        to.sc[i][plane][lane] = *reinterpret_cast<const u32x2*>(from.bytes(i) + NB * (2 * R::C + 32 * plane) + lane * 8);
+    };
+    auto turn = [&](const u32x4* raw_next, u32x4* raw_free, Ready<NB>& next, const Ready<NB>& now, int n) {
+      // step n + 1 has landed, step n is converted, nobody reads `next` or raw_free any more
+      wait_copies<0>();
+      lds_barrier16();
+      if (n + 2 < steps) fetch(raw_free, n + 2);
+      if (n + 1 < steps) convert(raw_next, next);
+      const int at = (u0 + 2 * n) * 16, f = flags >> 2 * (n & 3);
+      if (at < w.any_hi && at + 32 > w.any_lo) w.work(ReadyView<NB>{&now, lane}, at, f & 1, f & 2, lane);
+    };
+    if (steps > 0) {
+      fetch(raw0, 0);
+      if (steps > 1) fetch(raw1, 1);
+      wait_copies<0>();
+      lds_barrier16();
+      convert(raw0, ready0);
+      for (int n = 0; n < steps; n += 2) {
+        turn(raw1, raw0, ready1, ready0, n);
+        if (n + 1 < steps) turn(raw0, raw1, ready0, ready1, n + 1);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < TILES; ++j) {
       w.sum[j] = column_sum(w.sum[j]);
-      const int owner = j & 3, slot = wave < owner ? wave : wave - 1;
-      if (wave != owner) {
-#pragma unroll
-        for (int i = 0; i < NB * 2; ++i) meet[slot][i][lane] = w.o[j][i >> 1][i & 1];
-        meet_stats[slot][lane] = make_float2(w.ref[j], w.sum[j]);
-      }
-      __syncthreads();
-      if (wave == owner) {
-        float ref = w.ref[j];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) ref = fmaxf(ref, meet_stats[k][lane].x);
-        const float from = ref == -kInf ? 0.0f : ref;
-        const float f = __builtin_amdgcn_exp2f(w.ref[j] - from);
-        float sum = w.sum[j] * f;
-#pragma unroll
-        for (int i = 0; i < NB * 2; ++i) w.o[j][i >> 1][i & 1] *= f;
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const float2 st = meet_stats[k][lane];
-          const float g = __builtin_amdgcn_exp2f(st.x - from);
-          sum = fmaf(st.y, g, sum);
-#pragma unroll
-          for (int i = 0; i < NB * 2; ++i) {
-            const f32x4 v = meet[k][i][lane];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) w.o[j][i >> 1][i & 1][r] = fmaf(v[r], g, w.o[j][i >> 1][i & 1][r]);
-          }
-        }
-        if (row[j].token >= 0) {
-          const int h = row_head[j];
-          const int64_t at = row[j].token * int64_t(a.q_heads) + h;
-          if (a.slots) {
-            const int64_t part = at * a.slots + first_slot + split;
-            if (lane < 16) a.stats[part] = make_float2(ref, sum);
-            if (sum != 0.0f) {  // nothing seen: the join does not look at it
-#pragma unroll
-              for (int i = 0; i < NB * 2; ++i)
-                *reinterpret_cast<f32x4*>(a.sums + part * (32 * NB) + 16 * i + 4 * (lane >> 4)) = w.o[j][i >> 1][i & 1];
-            }
-          } else {
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            if (a.lse && lane < 16)
-              a.lse[at] = sum == 0.0f ? -kInf : 0.69314718f * (ref + __builtin_amdgcn_logf(sum));
-            const int64_t to = row[j].token * a.out_token + h * a.out_head + 4 * (lane >> 4);
-#pragma unroll
-            for (int i = 0; i < NB * 2; ++i) {
-              f32x4 v = w.o[j][i >> 1][i & 1] * inv;
-              if (sum == 0.0f) v = f32x4{0, 0, 0, 0};
-              if constexpr (E == 0) {
-                __builtin_memcpy(static_cast<float*>(a.out) + to + 16 * i, &v, 16);
-              } else {
-                const u32x2 x = {pack16<E == 1>(v[0], v[1]), pack16<E == 1>(v[2], v[3])};
-                __builtin_memcpy(static_cast<uint16_t*>(a.out) + to + 16 * i, &x, 8);
-              }
-            }
-          }
-        }
-      }
-      __syncthreads();
+      w.store(a, j, row[j], first_slot + sp.split, lane);
     }
+    __syncthreads();  // range, and the steps' buffers, are done with
   }
 }
 
 }  // namespace
 
-// One head size's launch; tiles 1 or 2.
+// Tiles of 16 rows that a wave of the many-row kernel holds: what fits its registers.
+template <int E, int NB>
+constexpr int kManyTiles = (E == 0 ? NB > 3 : NB > 5) ? 1 : 2;
+inline int many_rows(int dtype, int64_t D) { return (dtype == QMV_F32 ? D > 96 : D > 160) ? 64 : 128; }
+
+// One head size's launches.
 template <bool Q4, int E, int NB>
 hipError_t kv_attention_go(const KvAttnArgs& a, const KvAttentionPlan& p, hipStream_t s) {
   const unsigned heads = unsigned(a.kv.heads);
+  constexpr int T = kManyTiles<E, NB>;
   if (a.prefix) {
     const dim3 grid(heads * unsigned(p.prefix_splits), unsigned(p.prefix_row_blocks), 1);
-    if (p.prefix_tiles == 1) hipLaunchKernelGGL((kv_attention_kernel<Q4, E, NB, 1, true>), grid, dim3(256), 0, s, a, p.prefix_splits, 0);
-    else hipLaunchKernelGGL((kv_attention_kernel<Q4, E, NB, 2, true>), grid, dim3(256), 0, s, a, p.prefix_splits, 0);
+    if (p.prefix_many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, T, true>), grid, dim3(256), 0, s, a, p.prefix_splits, 0);
+    else hipLaunchKernelGGL((kv_attention_few_kernel<Q4, E, NB, true>), grid, dim3(256), 0, s, a, p.prefix_splits, 0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const int first = a.prefix ? p.prefix_splits : 0;
   const dim3 grid(heads * unsigned(p.splits) * unsigned(a.kv.B), unsigned(p.row_blocks), 1);
-  if (p.tiles == 1) hipLaunchKernelGGL((kv_attention_kernel<Q4, E, NB, 1, false>), grid, dim3(256), 0, s, a, p.splits, first);
-  else hipLaunchKernelGGL((kv_attention_kernel<Q4, E, NB, 2, false>), grid, dim3(256), 0, s, a, p.splits, first);
+  if (p.many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, T, false>), grid, dim3(256), 0, s, a, p.splits, first);
+  else hipLaunchKernelGGL((kv_attention_few_kernel<Q4, E, NB, false>), grid, dim3(256), 0, s, a, p.splits, first);
   return hipGetLastError();
 }
 

@@ -46,11 +46,10 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(const KvAttnArgs a) {
   }
 }
 
-// How many parts to cut `tokens` into so that `items` workgroups become about two per unit,
-// of 256 tokens at least.
-int parts(int64_t items, int64_t tokens) {
-  const int64_t want = (512 + items - 1) / items, most = std::max<int64_t>(1, (tokens + 255) / 256);
-  return int(std::min<int64_t>({want, most, 64}));
+// How many parts to cut `tokens` into so that `items` workgroups become `want`, of 256 tokens
+// at least.
+int parts(int64_t items, int64_t tokens, int64_t want) {
+  return int(std::max<int64_t>(1, std::min<int64_t>({(want + items - 1) / items, (tokens + 255) / 256, 64})));
 }
 
 }  // namespace
@@ -58,17 +57,18 @@ int parts(int64_t items, int64_t tokens) {
 KvAttentionPlan kv_attention_plan(const qmv_kv_cache& c, const qmv_kv_batch& b, const qmv_kv_attention_args& a) {
   KvAttentionPlan p{};
   const int64_t group = a.q_heads / c.heads, longest = std::min<int64_t>(a.max_kv, b.columns * c.page);
-  auto cut = [&](int64_t rows, int64_t sequences, int64_t tokens, int& tiles, int& blocks, int& splits) {
-    tiles = rows > 16 ? 2 : 1;
-    blocks = int(std::min<int64_t>((rows + 16 * tiles - 1) / (16 * tiles), 65535));
-    splits = parts(c.heads * sequences * blocks, tokens);
+  auto cut = [&](int64_t rows, int64_t sequences, int64_t tokens, bool& many, int& blocks, int& splits) {
+    many = rows > 16;
+    const int per = many ? many_rows(a.dtype, c.D) : 16;
+    blocks = int(std::min<int64_t>((rows + per - 1) / per, 65535));
+    splits = parts(c.heads * sequences * blocks, tokens, 2048);
   };
   const int64_t q = std::min(a.max_q, b.T);
   int64_t own = std::max<int64_t>(1, longest - a.prefix);
   if (a.window) own = std::min(own, a.window + q);
-  cut(q * group, b.B, own, p.tiles, p.row_blocks, p.splits);
+  cut(q * group, b.B, own, p.many, p.row_blocks, p.splits);
   if (a.prefix) {
-    cut(b.T * group, 1, std::min(longest, a.prefix), p.prefix_tiles, p.prefix_row_blocks, p.prefix_splits);
+    cut(b.T * group, 1, std::min(longest, a.prefix), p.prefix_many, p.prefix_row_blocks, p.prefix_splits);
     p.slots = p.prefix_splits + p.splits;
   } else {
     p.slots = p.splits > 1 ? p.splits : 0;
