@@ -102,32 +102,54 @@ struct Row {
   int lo, hi;  // positions that it sees, lo .. hi - 1
 };
 
+// The sequence of each lane's token, for tokens of the whole call from `least` on (uniform) up: the
+// wave finds that of the first, takes the starts of the 64 from there on, and each lane searches
+// them; what lies further (past many sequences without rows) is found by bisection.
+struct Sequences {
+  int first, starts;  // starts: row start of sequence first + lane
+  __device__ __forceinline__ void look_up(const KvArgs& kv, int least, int lane) {
+    first = kv_search(kv.B, least, [&](int i) { return int64_t(kv_row_start(kv, i)); });
+    starts = kv_row_start(kv, min(first + lane, kv.B));
+  }
+  __device__ __forceinline__ int of(const KvArgs& kv, int token) const {  // by a whole wave
+    int x = 0;
+#pragma unroll
+    for (int h = 32; h > 0; h >>= 1)
+      if (__shfl(starts, x + h) <= token && first + x + h < kv.B) x += h;
+    int at = first + x;
+    if (x == 63) {
+      int n = kv.B - at;
+      while (n > 1) {
+        const int h = n >> 1;
+        if (kv_row_start(kv, at + h) <= token) at += h, n -= h;
+        else n = h;
+      }
+    }
+    return at;
+  }
+};
+
+// Called by a whole wave; seq: for the prefix.
 template <bool PREFIX>
-__device__ __forceinline__ Row row_of(const KvAttnArgs& a, uint32_t r, uint32_t rows, int kv_head, int first_row,
-                                      int64_t first_pos, int from, int64_t cap) {
-  if (r >= rows) return Row{-1, 0, 0, 0};
-  const int i = int(r / uint32_t(a.group));
+__device__ __forceinline__ Row row_of(const KvAttnArgs& a, const Sequences& seq, uint32_t r, uint32_t rows, int kv_head,
+                                      int first_row, int64_t first_pos, int from, int64_t cap) {
+  const int i = int(min(r, rows - 1) / uint32_t(a.group));
   Row w;
   w.token = first_row + i;
-  w.head = kv_head * a.group + int(r) - i * a.group;
+  w.head = kv_head * a.group + int(min(r, rows - 1)) - i * a.group;
   int64_t pos;
-  if constexpr (PREFIX) {  // its sequence by bisection
-    int x = 0, n = a.kv.B;
-    while (n > 1) {
-      const int h = n >> 1;
-      if (kv_row_start(a.kv, x + h) <= w.token) x += h, n -= h;
-      else n = h;
-    }
-    const int end = kv_row_start(a.kv, x + 1);
-    if (w.token < kv_row_start(a.kv, x) || w.token >= end) return Row{-1, 0, 0, 0};
+  bool there = r < rows;
+  if constexpr (PREFIX) {
+    const int x = seq.of(a.kv, w.token), start = kv_row_start(a.kv, x), end = kv_row_start(a.kv, x + 1);
     pos = int64_t(a.kv.kv_len[x]) - end + w.token;
+    there = there && w.token >= start && w.token < end;
   } else {
     pos = first_pos + i;
   }
   const int64_t lo = a.window ? max(int64_t(0), pos - a.window + 1) : 0;
   w.lo = int(min(max(lo, int64_t(from)), cap));
   w.hi = int(max(int64_t(0), min(pos + 1, cap)));
-  return w;
+  return there ? w : Row{-1, 0, 0, 0};
 }
 
 // The rows and positions that a workgroup works on: a sequence's own, or the prefix's.
@@ -229,8 +251,8 @@ struct Rows {
     top = max(top, uint32_t(__shfl_xor(int(top), 32)));
     // 2^up brings the largest value to [2^14, 2^15); up to 2^126 for f32 that are next to nothing
     const int up = min(126, 14 - (int(top >> 23) - 127));
-    const float scale = __builtin_bit_cast(float, uint32_t(127 + up) << 23);
-    factor[j] = top >= 0x7F800000u ? __builtin_nanf("") : a.scale * __builtin_bit_cast(float, uint32_t(127 - up) << 23);
+    const float scale = __builtin_copysignf(__builtin_bit_cast(float, uint32_t(127 + up) << 23), a.scale);
+    factor[j] = top >= 0x7F800000u ? __builtin_nanf("") : fabsf(a.scale) * __builtin_bit_cast(float, uint32_t(127 - up) << 23);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -312,19 +334,7 @@ struct Rows {
 #pragma unroll
         for (int r = 0; r < 4; ++r) most = fmaxf(most, s[j][i][r]);
       most += float(int(top_v >> 10 & 31u) - 14);  // V's scales lie below 2^(exponent - 14)
-      if (__builtin_expect(__any(most > ref[j] + 15.0f), 0)) {
-        const float need = column_max(most);
-        const float next = need > ref[j] + 15.0f ? need - 7.0f : ref[j];
-        const float f = ref[j] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(ref[j] - next);
-        ref[j] = next;
-        sum[j] *= f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[j][b][m][r] *= f;
-      }
+      if (__builtin_expect(__any(most > ref[j] + 15.0f), 0)) raise(j, most);
       const float from = ref[j] == -kInf ? 0.0f : ref[j];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -364,6 +374,102 @@ struct Rows {
         }
       }
     }
+  }
+  // The same with operands that have their scales in them: K 2^up_k and V 2^up_v, both below 2^15, in f16
+  // (bf16 calls) or as two f16 parts, without the product of two low parts.  The probabilities enter
+  // as p 2^-up_v, which the reference keeps below 2^15 as above.
+  template <bool MASK, class T>
+  __device__ __forceinline__ void fold_step(const T& t, int at, bool there0, bool there1, int up_k, int up_v, int lane) {
+    const int quad = lane >> 4;
+    const float down_k = __builtin_bit_cast(float, uint32_t(127 - up_k) << 23), up = __builtin_bit_cast(float, uint32_t(127 + up_v) << 23);
+    f32x4 s[TILES][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const u32x4 k = t.k(i, b);
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+          s[j][i] = mfma16<true>(k, q[j][b][0], b ? s[j][i] : f32x4{0, 0, 0, 0});
+          if constexpr (QP == 2) s[j][i] = mfma16<true>(k, q[j][b][1], s[j][i]);
+        }
+        if constexpr (PP == 2) {
+          const u32x4 kl = t.k_low(i, b);
+#pragma unroll
+          for (int j = 0; j < TILES; ++j) s[j][i] = mfma16<true>(kl, q[j][b][0], s[j][i]);
+        }
+      }
+    u32x4 p[TILES], pl[TILES];
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+      bool seen[2][4];
+      float most = -kInf;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (MASK) {
+            const int pos = at + 16 * i + 4 * quad + r;
+            seen[i][r] = (i ? there1 : there0) && pos >= lo[j] && pos < hi[j];
+            most = fmaxf(most, seen[i][r] ? s[j][i][r] : -kInf);
+          } else {
+            most = fmaxf(most, s[j][i][r]);
+          }
+        }
+      const float f = factor[j] * down_k;
+      most = fmaf(most, f, float(-up_v));
+      if (__builtin_expect(__any(most > ref[j] + 15.0f), 0)) raise(j, most);
+      const float from = (ref[j] == -kInf ? 0.0f : ref[j]) + float(up_v);
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = __builtin_amdgcn_exp2f(fmaf(s[j][i][r], f, -from));
+          if constexpr (MASK) x = seen[i][r] ? x : 0.0f;
+          s[j][i][r] = x;
+          part += x;
+        }
+      sum[j] = fmaf(part, up, sum[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = s[j][i >> 1][2 * (i & 1)], y = s[j][i >> 1][2 * (i & 1) + 1];
+        const uint32_t w = pack16<true>(x, y);
+        p[j][i] = w;
+        if constexpr (PP == 2) pl[j][i] = pack16<true>(x - unpack16<true>(w & 0xFFFFu), y - unpack16<true>(w >> 16));
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const u32x4 v = t.v(b, m);
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+          o[j][b][m] = mfma16<true>(v, p[j], o[j][b][m]);
+          if constexpr (PP == 2) o[j][b][m] = mfma16<true>(v, pl[j], o[j][b][m]);
+        }
+        if constexpr (PP == 2) {
+          const u32x4 vl = t.v_low(b, m);
+#pragma unroll
+          for (int j = 0; j < TILES; ++j) o[j][b][m] = mfma16<true>(vl, p[j], o[j][b][m]);
+        }
+      }
+  }
+
+  // A new reference for the columns in which products could pass 2^15: they start at 2^7 again.
+  __device__ __forceinline__ void raise(int j, float most) {
+    const float need = column_max(most);
+    const float next = need > ref[j] + 15.0f ? need - 7.0f : ref[j];
+    const float f = ref[j] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(ref[j] - next);
+    ref[j] = next;
+    sum[j] *= f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[j][b][m][r] *= f;
   }
   template <class T>
   __device__ __forceinline__ void work(const T& t, int at, bool there0, bool there1, int lane) {
@@ -496,7 +602,9 @@ __global__ __launch_bounds__(256, 2) void kv_attention_few_kernel(const KvAttnAr
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Span sp = span_of<PREFIX>(a, splits);
   for (uint32_t base = blockIdx.y * 16; base < sp.rows; base += gridDim.y * 16) {
-    Row row[1] = {row_of<PREFIX>(a, base + (lane & 15), sp.rows, sp.kv_head, sp.r0, sp.first_pos, PREFIX ? 0 : a.prefix, sp.cap)};
+    Sequences seq;
+    if constexpr (PREFIX) seq.look_up(kv, int(base / uint32_t(a.group)), lane);
+    Row row[1] = {row_of<PREFIX>(a, seq, base + (lane & 15), sp.rows, sp.kv_head, sp.r0, sp.first_pos, PREFIX ? 0 : a.prefix, sp.cap)};
     Rows<E, NB, 1> w;
     w.load(a, row, lane);
     int u0, u1;
@@ -572,59 +680,157 @@ __global__ __launch_bounds__(256, 2) void kv_attention_few_kernel(const KvAttnAr
   }
 }
 
-// A step's operands in LDS, converted once for the four waves.
-template <int NB>
+// A step's operands in LDS, made once for the four waves: K and V with their scales, in PARTS
+// f16 parts.
+template <int NB, int PARTS>
 struct Ready {
-  u32x4 kc[2][NB][64], vc[NB][2][64];
-  u32x2 sc[2][2][4 * NB];  // set, K or V, (group of tokens, block)
+  u32x4 kc[PARTS][2][NB][64], vc[PARTS][NB][2][64];
+  int up_k, up_v;
 };
-template <int NB>
+template <int NB, int PARTS>
 struct ReadyView {
-  const Ready<NB>* r;
+  const Ready<NB, PARTS>* r;
   int lane;
-  __device__ __forceinline__ u32x4 k(int i, int b) const { return r->kc[i][b][lane]; }
-  __device__ __forceinline__ u32x4 v(int b, int m) const { return r->vc[b][m][lane]; }
-  __device__ __forceinline__ u32x2 ks(int i, int b) const { return r->sc[i][0][(lane >> 4) * NB + b]; }
-  __device__ __forceinline__ u32x2 vs(int i, int b) const { return r->sc[i][1][(lane >> 4) * NB + b]; }
+  __device__ __forceinline__ u32x4 k(int i, int b) const { return r->kc[0][i][b][lane]; }
+  __device__ __forceinline__ u32x4 v(int b, int m) const { return r->vc[0][b][m][lane]; }
+  __device__ __forceinline__ u32x4 k_low(int i, int b) const { return r->kc[PARTS - 1][i][b][lane]; }
+  __device__ __forceinline__ u32x4 v_low(int b, int m) const { return r->vc[PARTS - 1][b][m][lane]; }
 };
 
+__device__ __forceinline__ uint32_t pk_mul(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) * __builtin_bit_cast(f16x2, b));
+}
+// Codes times scales: rounded to f16, and what the rounding left over (exact: the product has 19 bits).
+template <int PARTS>
+__device__ __forceinline__ void put_scaled(u32x4 codes, u32x4 scales, u32x4* hi, u32x4* low) {
+  u32x4 h, l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = codes[i], s = scales[i], w = pk_mul(c, s);
+    h[i] = w;
+    if constexpr (PARTS == 2)
+      l[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2, c), __builtin_bit_cast(f16x2, s),
+                                                                    -__builtin_bit_cast(f16x2, w)));
+  }
+  *hi = h;
+  if constexpr (PARTS == 2) *low = l;
+}
+
+// The largest scale of a step's K (plane 0) or V (1), as f16 bits, over the positions from
+// `lo` up to `hi` whose page is there; by a whole wave, the same in every lane.  FINITE: of those
+// that are numbers.
+template <bool FINITE, bool Q4, int NB>
+__device__ __forceinline__ uint32_t top_scale(const Raw<Q4, NB>& raw, int plane, int at, int lo, int hi, int there) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int w0 = 0; w0 < 16 * NB; w0 += 64) {  // words of two tokens
+    const int w = w0 + raw.lane, i = w >= 8 * NB, x = i ? w - 8 * NB : w;
+    if (w < 16 * NB) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(raw.bytes(i) + NB * (2 * Raw<Q4, NB>::C + 32 * plane) + x * 4);
+      const int p = at + 16 * i + x / (2 * NB) * 4 + 2 * (x & 1);
+      const bool ok = there >> i & 1;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t half = v >> (16 * r) & 0x7FFFu;
+        if (ok && p + r >= lo && p + r < hi && (!FINITE || half < 0x7C00u)) top = max(top, half);
+      }
+    }
+  }
+  return uint32_t(wave_max(int(top)));
+}
+// Exponent that brings scales below 2^(e - 14), e their largest biased exponent, below 2^8: with codes up to
+// 128 that is 2^15.  2^up is an f16 value.
+__device__ __forceinline__ int up_of(uint32_t top) { return min(15, 22 - int(top >> 10)); }
+__device__ __forceinline__ uint32_t two_to(int up) { return uint32_t(15 + up) << 10; }
+
+// A wave's quarter of a step's operands.  Scales of positions that no row sees are zeros in V (a probability of zero times whatever lies there is
+// zero then); a scale that is no number makes its token's scores NaN.
+template <bool Q4, int NB, int PARTS>
+__device__ __forceinline__ void make_ready(const Raw<Q4, NB>& raw, Ready<NB, PARTS>& to, int wave, int at, int lo, int hi,
+                                           int there) {
+  constexpr int C = Raw<Q4, NB>::C;
+  const int lane = raw.lane, ln = lane & 15;
+  uint32_t top_k = top_scale<false>(raw, 0, at, lo, hi, there), top_v = top_scale<false>(raw, 1, at, lo, hi, there);
+  const bool bad = top_v >= 0x7C00u;
+  if (__builtin_expect(bad, 0)) top_v = top_scale<true>(raw, 1, at, lo, hi, there);
+  if (__builtin_expect(top_k >= 0x7C00u, 0)) top_k = top_scale<true>(raw, 0, at, lo, hi, there);
+  const int up_k = up_of(top_k), up_v = up_of(top_v);
+  const uint32_t mk = two_to(up_k), mv = two_to(up_v) * 0x10001u;
+  const bool plain = there == 3 && at >= lo && at + 32 <= hi && !bad;
+#pragma unroll
+  for (int x = 0; x < NB; ++x) {
+    const int y = 4 * x + wave;  // K's operands by set and block, then V's
+    if (y < 2 * NB) {
+      const int i = y & 1, b = y >> 1;
+      const uint16_t* sc = reinterpret_cast<const uint16_t*>(raw.bytes(i) + 2 * NB * C) + (ln >> 2) * NB * 4 + (ln & 3);
+      uint32_t s = sc[4 * b];
+      if (!plain && b == 0) {
+        uint32_t worst = 0;
+#pragma unroll
+        for (int z = 0; z < NB; ++z) worst = max(worst, uint32_t(sc[16 * NB + 4 * z]) & 0x7FFFu);
+        if (worst >= 0x7C00u) s = 0x7E00u;
+      }
+      s = pk_mul(s, mk) & 0xFFFFu;
+      s |= s << 16;
+      put_scaled<PARTS>(raw.k(i, b), u32x4{s, s, s, s}, &to.kc[0][i][b][lane], &to.kc[PARTS - 1][i][b][lane]);
+    } else {
+      const int b = (y - 2 * NB) >> 1, m = y & 1;
+      u32x2 s[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s[i] = raw.vs(i, b);
+        if (!plain) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int p = at + 16 * i + 4 * (lane >> 4) + r;
+            const uint32_t w = s[i][r >> 1], half = w >> (16 * (r & 1)) & 0xFFFFu;
+            if (!(there >> i & 1) || p < lo || p >= hi || (half & 0x7FFFu) >= 0x7C00u) s[i][r >> 1] = w & (r & 1 ? 0xFFFFu : 0xFFFF0000u);
+          }
+        }
+      }
+      put_scaled<PARTS>(raw.v(b, m), u32x4{pk_mul(s[0][0], mv), pk_mul(s[0][1], mv), pk_mul(s[1][0], mv), pk_mul(s[1][1], mv)},
+                        &to.vc[0][b][m][lane], &to.vc[PARTS - 1][b][m][lane]);
+    }
+  }
+  if (wave == 0 && lane == 0) to.up_k = up_k, to.up_v = up_v;
+}
 // Many queries: each of the four waves has 16 * TILES rows of its own and all work on the
-// same 32 tokens.  A step's bytes are copied to LDS two steps ahead, its codes are turned
-// into operands, a quarter by each wave, one step ahead; one barrier a step.
+// same 32 tokens.  A step's bytes are copied to LDS one step ahead; each wave turns a quarter
+// of its codes into operands, and then works on all of them.
 template <bool Q4, int E, int NB, int TILES, bool PREFIX>
-__global__ __launch_bounds__(256, 2) void kv_attention_many_kernel(const KvAttnArgs a, int splits, int first_slot) {
+__global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(const KvAttnArgs a, int splits, int first_slot) {
   typedef Raw<Q4, NB> R;
   constexpr int kStep = 2 * R::kPieces, kRows = 64 * TILES;
+  constexpr int kParts = Rows<E, NB, TILES>::PP;
   __shared__ u32x4 raw0[kStep], raw1[kStep];
-  __shared__ Ready<NB> ready0, ready1;
+  __shared__ Ready<NB, kParts> ready;
   __shared__ int range[4][2];
   const KvArgs& kv = a.kv;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Span sp = span_of<PREFIX>(a, splits);
   for (uint32_t base = blockIdx.y * kRows; base < sp.rows; base += gridDim.y * kRows) {
     Row row[TILES];
+    Sequences seq;
+    if constexpr (PREFIX) seq.look_up(kv, int(min(base + wave * (16 * TILES), sp.rows - 1) / uint32_t(a.group)), lane);
 #pragma unroll
     for (int j = 0; j < TILES; ++j)
-      row[j] = row_of<PREFIX>(a, base + wave * (16 * TILES) + 16 * j + (lane & 15), sp.rows, sp.kv_head, sp.r0, sp.first_pos,
-                              PREFIX ? 0 : a.prefix, sp.cap);
+      row[j] = row_of<PREFIX>(a, seq, base + wave * (16 * TILES) + 16 * j + (lane & 15), sp.rows, sp.kv_head, sp.r0,
+                              sp.first_pos, PREFIX ? 0 : a.prefix, sp.cap);
     Rows<E, NB, TILES> w;
     w.load(a, row, lane);
     if (lane == 0) range[wave][0] = w.any_lo < w.any_hi ? w.any_lo : 0x7FFFFFFF, range[wave][1] = w.any_hi;
     __syncthreads();
-    const int lo = min(min(range[0][0], range[1][0]), min(range[2][0], range[3][0]));
-    const int hi = max(max(range[0][1], range[1][1]), max(range[2][1], range[3][1]));
+    const int lo = __builtin_amdgcn_readfirstlane(min(min(range[0][0], range[1][0]), min(range[2][0], range[3][0])));
+    const int hi = __builtin_amdgcn_readfirstlane(max(max(range[0][1], range[1][1]), max(range[2][1], range[3][1])));
     int u0, u1;
-    share_of(__builtin_amdgcn_readfirstlane(lo < hi ? lo >> 4 : 0), __builtin_amdgcn_readfirstlane(lo < hi ? (hi + 15) >> 4 : 0),
-             splits, sp.split, 2, u0, u1);
+    share_of(lo < hi ? lo >> 4 : 0, lo < hi ? (hi + 15) >> 4 : 0, splits, sp.split, 2, u0, u1);
     const int steps = u1 > u0 ? (u1 - u0 + 1) >> 1 : 0;
     Ahead ahead;
-    int flags = 0;  // bit 2 (n % 4) + i: set i of step n is there
-    // wave w copies half w % 2 of set w / 2
-    auto fetch = [&](u32x4* raw, int n) {
+    // wave w copies half w % 2 of set w / 2; returns which sets are there, as bits
+    auto fetch = [&](u32x4* raw, int n) -> int {
       if ((n & 31) == 0) ahead.look_up(kv, sp.table, u0, 2, n, u1, lane);
       const int i = wave >> 1, part = wave & 1, p0 = ahead.page(n, 0), p1 = ahead.page(n, 1);
-      flags &= ~(3 << 2 * (n & 3));
-      flags |= (int(p0 >= 0) | int(p1 >= 0) << 1) << 2 * (n & 3);
+      const int both = int(p0 >= 0) | int(p1 >= 0) << 1;
       const Buf src = buffer_of(kv.data + max(i ? p1 : p0, 0) * kv.page_bytes + int64_t(sp.kv_head) * kv.head_bytes +
                                 (i ? ahead.place(n, 1) : ahead.place(n, 0)) * kv.set_bytes);
       constexpr int kHalf = R::kPieces / 2;  // kPieces is even
@@ -633,38 +839,26 @@ __global__ __launch_bounds__(256, 2) void kv_attention_many_kernel(const KvAttnA
       for (int c = 0; c < kHalf / 64; ++c) copy_to_lds(src, lane * 16, (part * kHalf + c * 64) * 16, dst + c * 64);
       if constexpr (kHalf % 64 != 0)
         if (lane < kHalf % 64) copy_to_lds(src, lane * 16, (part * kHalf + kHalf / 64 * 64) * 16, dst + kHalf / 64 * 64);
+      return both;
     };
-    // K's operands by set and block, then V's, in turn among the waves
-    auto convert = [&](const u32x4* raw, Ready<NB>& to) {
-      const R from{raw, lane};
-#pragma unroll
-      for (int x = 0; x < NB; ++x) {
-        const int y = 4 * x + wave;  // 0 .. 4 NB - 1
-        if (y < 2 * NB) to.kc[y & 1][y >> 1][lane] = from.k(y & 1, y >> 1);
-        else to.vc[(y - 2 * NB) >> 1][y & 1][lane] = from.v((y - 2 * NB) >> 1, y & 1);
-      }
-      const int i = wave >> 1, plane = wave & 1;
-      if (lane < 4 * NB)
-        to.sc[i][plane][lane] = *reinterpret_cast<const u32x2*>(from.bytes(i) + NB * (2 * R::C + 32 * plane) + lane * 8);
-    };
-    auto turn = [&](const u32x4* raw_next, u32x4* raw_free, Ready<NB>& next, const Ready<NB>& now, int n) {
-      // step n + 1 has landed, step n is converted, nobody reads `next` or raw_free any more
+    auto turn = [&](const u32x4* raw, u32x4* raw_next, int n, int there, int& there_next) {
       wait_copies<0>();
+      lds_barrier16();  // step n has landed; nobody works on step n - 1 any more
+      if (n + 1 < steps) there_next = fetch(raw_next, n + 1);
+      const int at = (u0 + 2 * n) * 16;
+      make_ready(R{raw, lane}, ready, wave, at, lo, hi, there);
       lds_barrier16();
-      if (n + 2 < steps) fetch(raw_free, n + 2);
-      if (n + 1 < steps) convert(raw_next, next);
-      const int at = (u0 + 2 * n) * 16, f = flags >> 2 * (n & 3);
-      if (at < w.any_hi && at + 32 > w.any_lo) w.work(ReadyView<NB>{&now, lane}, at, f & 1, f & 2, lane);
+      if (at >= w.any_hi || at + 32 <= w.any_lo) return;
+      const ReadyView<NB, kParts> view{&ready, lane};
+      const int up_k = __builtin_amdgcn_readfirstlane(ready.up_k), up_v = __builtin_amdgcn_readfirstlane(ready.up_v);
+      if (there == 3 && at >= w.all_lo && at + 32 <= w.all_hi) w.template fold_step<false>(view, at, true, true, up_k, up_v, lane);
+      else w.template fold_step<true>(view, at, there & 1, there & 2, up_k, up_v, lane);
     };
     if (steps > 0) {
-      fetch(raw0, 0);
-      if (steps > 1) fetch(raw1, 1);
-      wait_copies<0>();
-      lds_barrier16();
-      convert(raw0, ready0);
+      int there0 = fetch(raw0, 0), there1 = 0;
       for (int n = 0; n < steps; n += 2) {
-        turn(raw1, raw0, ready1, ready0, n);
-        if (n + 1 < steps) turn(raw0, raw1, ready0, ready1, n + 1);
+        turn(raw0, raw1, n, there0, there1);
+        if (n + 1 < steps) turn(raw1, raw0, n + 1, there1, there0);
       }
     }
 #pragma unroll
@@ -678,16 +872,14 @@ __global__ __launch_bounds__(256, 2) void kv_attention_many_kernel(const KvAttnA
 
 }  // namespace
 
-// Tiles of 16 rows that a wave of the many-row kernel holds: what fits its registers.
-template <int E, int NB>
-constexpr int kManyTiles = (E == 0 ? NB > 3 : NB > 5) ? 1 : 2;
-inline int many_rows(int dtype, int64_t D) { return (dtype == QMV_F32 ? D > 96 : D > 160) ? 64 : 128; }
+constexpr int kManyTiles = 2;  // tiles of 16 rows that a wave of the many-row kernel holds
+constexpr int kManyRows = 64 * kManyTiles;
 
 // One head size's launches.
 template <bool Q4, int E, int NB>
 hipError_t kv_attention_go(const KvAttnArgs& a, const KvAttentionPlan& p, hipStream_t s) {
   const unsigned heads = unsigned(a.kv.heads);
-  constexpr int T = kManyTiles<E, NB>;
+  constexpr int T = kManyTiles;
   if (a.prefix) {
     const dim3 grid(heads * unsigned(p.prefix_splits), unsigned(p.prefix_row_blocks), 1);
     if (p.prefix_many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, T, true>), grid, dim3(256), 0, s, a, p.prefix_splits, 0);

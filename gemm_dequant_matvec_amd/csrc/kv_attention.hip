@@ -8,9 +8,10 @@ namespace {
 constexpr int kThreads = 256;
 
 // out = sum of 2^(ref_i - ref) o_i / sum of 2^(ref_i - ref) sum_i over a row's partial results, in
-// their order.  A row has D / 4 threads.
+// their order, eight of them under way at a time.  A row has D / 4 threads.
 template <int E>
 __global__ __launch_bounds__(kThreads) void kv_join_kernel(const KvAttnArgs a) {
+  constexpr int kAhead = 8;
   const int D = 32 * a.kv.nb, per = D >> 2, rows = kThreads / per;
   const int mine = threadIdx.x / per, x = threadIdx.x - mine * per;
   const int64_t end = int64_t(kv_row_start(a.kv, a.kv.B)) * a.q_heads;
@@ -19,19 +20,32 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(const KvAttnArgs a) {
     const int token = int(row / a.q_heads), h = int(row - int64_t(token) * a.q_heads);
     const float2* st = a.stats + row * a.slots;
     const float* sums = a.sums + row * a.slots * D + 4 * x;
-    float ref = -kInf;
-    for (int i = 0; i < a.slots; ++i) ref = fmaxf(ref, st[i].x);
-    const float from = ref == -kInf ? 0.0f : ref;
     f32x4 o = {0, 0, 0, 0};
-    float sum = 0.0f;
-    for (int i = 0; i < a.slots; ++i) {
-      const float2 s = st[i];
-      if (s.y == 0.0f) continue;
-      const float f = __builtin_amdgcn_exp2f(s.x - from);
-      const f32x4 v = *reinterpret_cast<const f32x4*>(sums + int64_t(i) * D);
-      sum = fmaf(s.y, f, sum);
+    float ref = -kInf, sum = 0.0f;
+    for (int i0 = 0; i0 < a.slots; i0 += kAhead) {
+      float2 s[kAhead];
+      f32x4 v[kAhead];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = fmaf(v[r], f, o[r]);
+      for (int i = 0; i < kAhead; ++i) {
+        const int at = min(i0 + i, a.slots - 1);
+        s[i] = st[at];
+        v[i] = *reinterpret_cast<const f32x4*>(sums + int64_t(at) * D);
+      }
+      float next = ref;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) next = fmaxf(next, s[i].x);
+      const float from = next == -kInf ? 0.0f : next, f = __builtin_amdgcn_exp2f(ref - from);
+      ref = next;
+      sum *= f;
+      o *= f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (i0 + i >= a.slots || s[i].y == 0.0f) continue;  // what saw nothing has no values
+        const float g = __builtin_amdgcn_exp2f(s[i].x - from);
+        sum = fmaf(s[i].y, g, sum);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = fmaf(v[i][r], g, o[r]);
+      }
     }
     if (a.lse && x == 0) a.lse[row] = sum == 0.0f ? -kInf : 0.69314718f * (ref + __builtin_amdgcn_logf(sum));
     f32x4 v = o * (1.0f / sum);
@@ -46,10 +60,13 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(const KvAttnArgs a) {
   }
 }
 
-// How many parts to cut `tokens` into so that `items` workgroups become `want`, of 256 tokens
-// at least.
-int parts(int64_t items, int64_t tokens, int64_t want) {
-  return int(std::max<int64_t>(1, std::min<int64_t>({(want + items - 1) / items, (tokens + 255) / 256, 64})));
+// How many parts to cut `tokens` into for `items` workgroups otherwise: up to two workgroups per
+// unit, of 256 tokens at least; beyond that parts of 2048 tokens, which even out sequences of
+// different lengths, up to eight workgroups per place.
+int parts(int64_t items, int64_t tokens) {
+  const int64_t fill = std::min(512 / items, (tokens + 255) / 256);
+  const int64_t even = std::min((tokens + 2047) / 2048, (4096 + items - 1) / items);
+  return int(std::max<int64_t>({1, std::min<int64_t>(fill, 64), std::min<int64_t>(even, 64)}));
 }
 
 }  // namespace
@@ -59,9 +76,9 @@ KvAttentionPlan kv_attention_plan(const qmv_kv_cache& c, const qmv_kv_batch& b, 
   const int64_t group = a.q_heads / c.heads, longest = std::min<int64_t>(a.max_kv, b.columns * c.page);
   auto cut = [&](int64_t rows, int64_t sequences, int64_t tokens, bool& many, int& blocks, int& splits) {
     many = rows > 16;
-    const int per = many ? many_rows(a.dtype, c.D) : 16;
+    const int per = many ? kManyRows : 16;
     blocks = int(std::min<int64_t>((rows + per - 1) / per, 65535));
-    splits = parts(c.heads * sequences * blocks, tokens, 2048);
+    splits = parts(c.heads * sequences * blocks, tokens);
   };
   const int64_t q = std::min(a.max_q, b.T);
   int64_t own = std::max<int64_t>(1, longest - a.prefix);

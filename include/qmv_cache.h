@@ -118,13 +118,17 @@ typedef struct qmv_kv_attention_args {
  *   s_t = scale * q . K_t,  out = sum_t softmax(s)_t V_t
  * over the positions t <= p that the window leaves and that are there; a row
  * that sees nothing gives zeros.  The rows' own keys and values are read from the
- * cache too: write them first.  K and V enter as d * q, not rounded to 16 bits: the codes
- * are exact operands of the 16-bit matrix cores, K's scales multiply the sums of 32,
- * V's scales the probabilities.  Scores, maxima, sums and accumulators are f32.  f32
- * queries, and f32 or f16 probabilities times scale, enter as two f16 parts (22 bits);
- * in bf16 calls the probabilities enter as one f16 value (11 bits, against the 8 of
- * the result).  A row whose q holds a NaN or an infinity is NaN; masked and absent
- * positions do not enter, whatever the cache holds there.
+ * cache too: write them first.  Scores, maxima, sums and accumulators are f32; the
+ * products run on the 16-bit matrix cores:
+ *   f32 and f16 calls: with K, V and the probabilities in operands of 22 bits (exact for K
+ *   and V; two f16 parts), f32 queries too;
+ *   bf16 calls: with the probabilities, and from 17 queries of a k / v head on (rows of a
+ *   sequence, or of the batch over a prefix, times q_heads / heads) d * q of K and V, rounded
+ *   once to f16 (11 bits against the result's 8; with an exponent of its own for
+ *   every 32 tokens).
+ * A row whose q holds a NaN or an infinity is NaN, and one that sees a block which reads
+ * back as NaN (in K altogether; in V in that block's dimensions at least).  Masked and
+ * absent positions do not enter, whatever the cache holds there.
  *   ws, ws_bytes   scratch memory, 16-byte aligned, of at least
  *                  qmv_kv_attention_bytes bytes (NULL if that is 0); calls that overlap
  *                  in time need a ws of their own

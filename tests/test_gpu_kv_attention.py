@@ -11,6 +11,12 @@ Probabilities times scale as f16: 2^-11 A for bf16 calls, 2^-22 A as two parts, 
 what lies below f16's normal values at most 2^-25 of products that start at 2^6:
 n 2^-31 max |V| for n positions.  Sums over tokens: (n / 32 + 100) 2^-23 A.  Then one
 rounding to the type.  lse: delta + 2^-21 (|lse| + 1).
+
+Calls that put more than 16 queries on a k / v head (of a sequence, or of the batch over a
+shared prefix) take K and V times their scales as f16 values in bf16: K's rounding adds
+2^-11 M_t to a score, V's and the probability's 2^-11 A each to the result.  In f16 and
+f32 they take two parts of each without the product of the low ones: 2^-22 M_t and
+2 2^-22 A more.
 """
 import math
 
@@ -88,6 +94,9 @@ class Case:
         c = self.qmv.KVCache(self.fmt, self.pages, self.heads, self.D, self.page, data=self.data.cuda())
         q = (self.q if q is None else q).cuda()
         kw.setdefault("prefix", self.prefix)
+        most = min(kw.get("max_q", -(-q.shape[0] // len(self.news))), q.shape[0])
+        self.many = bool(most * self.group > 16 or (kw["prefix"] and q.shape[0] * self.group > 16))
+        self.rounded = self.many and self.dt == torch.bfloat16
         return self.qmv.kv_attention(c, q, ints(self.table.tolist()), ints(self.starts), ints(self.lens), **kw)
 
     def sequence(self, b, n):
@@ -122,10 +131,10 @@ class Case:
                 t = keep
                 seen = (t <= pos[:, None]) & (t >= lo[:, None]) if t.numel() else torch.zeros(n, 0, dtype=torch.bool)
                 out, A, ls, M = attend(q, kk[keep], vv[keep], seen, scale)
-                delta = 64 * 2.0 ** -23 * M[..., None] + 2.0 ** -20
+                delta = (64 * 2.0 ** -23 + 2.0 ** -22 * self.many + 2.0 ** -11 * self.rounded) * M[..., None] + 2.0 ** -20
                 count = seen.sum(-1)[:, None, None].double()
                 vmax = vv[keep].abs().max() if keep.numel() else torch.zeros(())
-                part = 2.0 ** -11 if self.dt == torch.bfloat16 else 2.0 ** -22
+                part = 2.0 ** -10 if self.rounded else 2.0 ** -11 if self.dt == torch.bfloat16 else 2.0 ** -22 * (1 + 2 * self.many)
                 tol = A * (2 * delta + part + (count / 32 + 100) * 2.0 ** -23) + count * 2.0 ** -31 * vmax
                 tol = tol + e * (out.abs() + tol) + sub
                 err = (got[r, g] - out).abs()
@@ -274,6 +283,33 @@ def test_special_queries_and_blocks(qmv):
     half[ks[0, 0]] = float("nan")
     got = c.call()
     assert bool(torch.isnan(got[2:4]).all()) and torch.equal(got[:2], plain[:2]) and torch.equal(got[4], plain[4])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_bad_blocks_of_many_rows(qmv, dtype):
+    """Rows of one tile, some of which see a token whose K or V is no number: those are NaN (in the block's
+    dimensions at least), the others are untouched; K and V near the ends of their range."""
+    for plane in (2, 3):
+        c = Case(qmv, "q8_0", dtype, 1, 3, 64, 16, [40], [75])
+        clean = c.call(max_q=40)
+        c.check(clean)
+        half = c.data.view(torch.float16)
+        at = kr.places("q8_0", 1, 64, 16, int(c.table[0, 3]), 2)[plane]  # position 50: rows 15 .. 39 see it
+        half[at[0, 1]] = float("nan")
+        got = c.call(max_q=40)
+        assert torch.equal(got[:15], clean[:15])
+        assert bool(torch.isnan(got[15:, :, 32:]).all())
+    c = Case(qmv, "q4_0", dtype, 1, 3, 64, 16, [40], [75])
+    sets = c.data.view(torch.float16).view(-1, kr.set_bytes("q4_0", 64) // 2)
+    for scale in (60000.0, 2.0 ** -22):
+        sets[:, -64:] = scale
+        c.q = c.q * 0 + (2.0 ** -10 if scale > 1 else 1.0)
+        sets[:, -64:-32] = scale if scale < 1 else 0.5  # K; V past what f16 holds as values
+        got = c.call(max_q=40, scale=1.0)
+        if dtype != "f16":  # f16 results of these sizes are infinite
+            c.check(got, scale=1.0)
+        else:
+            assert not bool(torch.isnan(got).any())
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
