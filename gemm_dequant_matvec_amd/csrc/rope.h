@@ -72,26 +72,35 @@ struct Elem {
     if constexpr (E == 0) return v;
     else return uint16_t(pack16<E == 1>(v, 0.f));
   }
-  // n (1 .. V) values from p, in f32; the whole vector in one load
-  static __device__ __forceinline__ void load(const T* p, int n, float (&v)[V]) {
+  // n (1 .. V) values from p as they are, zeros behind them; the whole vector in one load
+  static __device__ __forceinline__ u32x4 raw(const T* p, int n) {
+    u32x4 w = {0, 0, 0, 0};
     if (n == V) {
-      u32x4 w;
       __builtin_memcpy(&w, p, 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t b = w[i];
-        if constexpr (E == 0) {
-          v[i] = __builtin_bit_cast(float, b);
-        } else {
-          v[2 * i] = unpack16<E == 1>(b & 0xFFFFu);
-          v[2 * i + 1] = unpack16<E == 1>(b >> 16);
-        }
-      }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = i < n ? get(p[i]) : 0.0f;
+      for (int i = 0; i < V; ++i)
+        if (i < n) {
+          if constexpr (E == 0) w[i] = __builtin_bit_cast(uint32_t, p[i]);
+          else w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+        }
+    }
+    return w;
+  }
+  static __device__ __forceinline__ void values(u32x4 w, float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = w[i];
+      if constexpr (E == 0) {
+        v[i] = __builtin_bit_cast(float, b);
+      } else {
+        v[2 * i] = unpack16<E == 1>(b & 0xFFFFu);
+        v[2 * i + 1] = unpack16<E == 1>(b >> 16);
+      }
     }
   }
+  // the same in f32
+  static __device__ __forceinline__ void load(const T* p, int n, float (&v)[V]) { values(raw(p, n), v); }
   static __device__ __forceinline__ void store(T* p, int n, const float (&v)[V]) {
     if (n == V) {
       u32x4 w;
