@@ -57,23 +57,31 @@ template <int CTRL>
 __device__ __forceinline__ int dpp_of(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
 }
-// Largest value of the wave, in every lane.
-__device__ __forceinline__ int wave_max(int v) {
+// f of the values of lane and lane ^ 16, then of lane ^ 32: over the four lanes of a column.
+template <class T, class F>
+__device__ __forceinline__ T over_column(T v, F f) {
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  const uint32_t y = __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(T, uint32_t(a[0])), __builtin_bit_cast(T, uint32_t(a[1]))));
+  const auto b = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+  return f(__builtin_bit_cast(T, uint32_t(b[0])), __builtin_bit_cast(T, uint32_t(b[1])));
+}
+// Largest value of 16 lanes, in each of them.
+__device__ __forceinline__ int row_max(int v) {
   v = max(v, dpp_of<0xB1>(v));
   v = max(v, dpp_of<0x4E>(v));
   v = max(v, dpp_of<0x141>(v));
-  v = max(v, dpp_of<0x140>(v));
-  v = max(v, __shfl_xor(v, 16));
-  return __builtin_amdgcn_readfirstlane(max(v, __shfl_xor(v, 32)));
+  return max(v, dpp_of<0x140>(v));
 }
-// Over the four lanes of a column (lane ^ 16, lane ^ 32).
+// Of the wave, in every lane.
+__device__ __forceinline__ int wave_max(int v) {
+  return __builtin_amdgcn_readfirstlane(over_column(row_max(v), [](int a, int b) { return max(a, b); }));
+}
 __device__ __forceinline__ float column_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  return over_column(v, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float column_sum(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  return over_column(v, [](float a, float b) { return a + b; });
 }
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -197,19 +205,26 @@ struct Rows {
   int all_lo, all_hi;  // every row sees all_lo .. all_hi - 1
   int any_lo, any_hi;  // no row sees anything outside any_lo .. any_hi - 1
 
-  __device__ __forceinline__ void load(const KvAttnArgs& a, const Row (&row)[TILES], int lane) {
+  // What the rows see, and nothing of it yet.
+  __device__ __forceinline__ void begin(const Row (&row)[TILES]) {
     int most_lo = 0, least_hi = 0x7FFFFFFF, least_lo = 0x7FFFFFFF, most_hi = 0;
 #pragma unroll
     for (int j = 0; j < TILES; ++j) {
-      if (row[j].token >= 0) {
-        most_lo = max(most_lo, row[j].lo);
-        least_hi = min(least_hi, row[j].hi);
-        if (row[j].lo < row[j].hi) {
-          least_lo = min(least_lo, row[j].lo);
-          most_hi = max(most_hi, row[j].hi);
-        }
+      const bool there = row[j].token >= 0;
+      lo[j] = there ? row[j].lo : 0;
+      hi[j] = there ? row[j].hi : 0x7FFFFFFF;
+      most_lo = max(most_lo, lo[j]);
+      least_hi = min(least_hi, hi[j]);
+      if (there && lo[j] < hi[j]) {
+        least_lo = min(least_lo, lo[j]);
+        most_hi = max(most_hi, hi[j]);
       }
-      load_q(a, j, row[j], lane);
+      ref[j] = -kInf;
+      sum[j] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) o[j][b][m] = f32x4{0, 0, 0, 0};
     }
     all_lo = wave_max(most_lo);
     all_hi = -wave_max(-least_hi);
@@ -218,37 +233,44 @@ struct Rows {
     if (any_lo >= any_hi) any_lo = any_hi = 0;
   }
 
-  __device__ __forceinline__ void load_q(const KvAttnArgs& a, int j, const Row& row, int lane) {
+  // q is fetched before the tokens and made into operands while they are on their way.
+  struct Fetched {
+    u32x4 w[NB][E == 0 ? 2 : 1];
+  };
+  static __device__ __forceinline__ void fetch_q(const KvAttnArgs& a, const Row& row, int lane, Fetched& f) {
+    const int64_t at = row.token * a.q_token + row.head * a.q_head + 8 * (lane >> 4);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int i = 0; i < (E == 0 ? 2 : 1); ++i) f.w[b][i] = u32x4{0, 0, 0, 0};
+      if (row.token >= 0) {
+        if constexpr (E == 0) __builtin_memcpy(f.w[b], static_cast<const float*>(a.q) + at + 32 * b, 32);
+        else f.w[b][0] = load8(static_cast<const uint16_t*>(a.q) + at + 32 * b);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void take_q(const KvAttnArgs& a, int j, const Fetched& fetched) {
     float x[NB][8];
     uint32_t top = 0;
-    if (row.token >= 0) {
-      const int64_t at = row.token * a.q_token + row.head * a.q_head + 8 * (lane >> 4);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         if constexpr (E == 0) {
-          __builtin_memcpy(x[b], static_cast<const float*>(a.q) + at + 32 * b, 32);
+          x[b][i] = __builtin_bit_cast(float, uint32_t(fetched.w[b][0][i]));
+          x[b][4 + i] = __builtin_bit_cast(float, uint32_t(fetched.w[b][E == 0][i]));
         } else {
-          const u32x4 w = load8(static_cast<const uint16_t*>(a.q) + at + 32 * b);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t bits = w[i];
-            x[b][2 * i] = unpack16<E == 1>(bits & 0xFFFFu);
-            x[b][2 * i + 1] = unpack16<E == 1>(bits >> 16);
-          }
+          const uint32_t bits = fetched.w[b][0][i];
+          x[b][2 * i] = unpack16<E == 1>(bits & 0xFFFFu);
+          x[b][2 * i + 1] = unpack16<E == 1>(bits >> 16);
         }
       }
-    } else {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[b][i] = 0.0f;
-    }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(uint32_t, x[b][i]) & 0x7FFFFFFFu);
-    top = max(top, uint32_t(__shfl_xor(int(top), 16)));
-    top = max(top, uint32_t(__shfl_xor(int(top), 32)));
+    top = over_column(top, [](uint32_t a, uint32_t b) { return max(a, b); });
     // 2^up brings the largest value to [2^14, 2^15); up to 2^126 for f32 that are next to nothing
     const int up = min(126, 14 - (int(top >> 23) - 127));
     const float scale = __builtin_copysignf(__builtin_bit_cast(float, uint32_t(127 + up) << 23), a.scale);
@@ -263,14 +285,6 @@ struct Rows {
         if constexpr (QP == 2) q[j][b][1][i] = pack16<true>(y - unpack16<true>(w & 0xFFFFu), z - unpack16<true>(w >> 16));
       }
     }
-    lo[j] = row.token >= 0 ? row.lo : 0;
-    hi[j] = row.token >= 0 ? row.hi : 0x7FFFFFFF;
-    ref[j] = -kInf;
-    sum[j] = 0.0f;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) o[j][b][m] = f32x4{0, 0, 0, 0};
   }
 
   // 32 tokens from position `at`; MASK: some row may not see all of them; there0, there1: the
@@ -379,45 +393,74 @@ struct Rows {
   // (bf16 calls) or as two f16 parts, without the product of two low parts.  The probabilities enter
   // as p 2^-up_v, which the reference keeps below 2^15 as above.
   template <bool MASK, class T>
-  __device__ __forceinline__ void fold_step(const T& t, int at, bool there0, bool there1, int up_k, int up_v, int lane) {
+  __device__ __forceinline__ void fold_step(const T& t, int at, bool there0, bool there1, int up_k0, int up_k1, int up_v, int lane) {
     const int quad = lane >> 4;
-    const float down_k = __builtin_bit_cast(float, uint32_t(127 - up_k) << 23), up = __builtin_bit_cast(float, uint32_t(127 + up_v) << 23);
+    const float up = __builtin_bit_cast(float, uint32_t(127 + up_v) << 23);
     f32x4 s[TILES][2];
+    // operands of the next group of blocks are on their way from LDS while the products of one run
+    constexpr int G = PP == 2 ? 1 : 2, kGroups = (NB + G - 1) / G;
+    u32x4 hold[2][G][2][PP];
+    auto load_k = [&](int g) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+      for (int c = 0; c < G; ++c)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const u32x4 k = t.k(i, b);
+        for (int i = 0; i < 2; ++i)
+          if (g * G + c < NB) {
+            hold[g & 1][c][i][0] = t.k(i, g * G + c);
+            if constexpr (PP == 2) hold[g & 1][c][i][1] = t.k_low(i, g * G + c);
+          }
+    };
+    auto load_v = [&](int g) {
 #pragma unroll
-        for (int j = 0; j < TILES; ++j) {
-          s[j][i] = mfma16<true>(k, q[j][b][0], b ? s[j][i] : f32x4{0, 0, 0, 0});
-          if constexpr (QP == 2) s[j][i] = mfma16<true>(k, q[j][b][1], s[j][i]);
+      for (int c = 0; c < G; ++c)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          if (g * G + c < NB) {
+            hold[g & 1][c][m][0] = t.v(g * G + c, m);
+            if constexpr (PP == 2) hold[g & 1][c][m][1] = t.v_low(g * G + c, m);
+          }
+    };
+    load_k(0);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      if (g + 1 < kGroups) load_k(g + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int part = 0; part < PP + QP - 1; ++part)  // K q, then K's low part, or q's
+#pragma unroll
+        for (int c = 0; c < G; ++c) {
+          const int b = g * G + c;
+          if (b >= NB) continue;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < TILES; ++j)
+              s[j][i] = mfma16<true>(hold[g & 1][c][i][part == 1], q[j][b][part == 2], b || part ? s[j][i] : f32x4{0, 0, 0, 0});
         }
-        if constexpr (PP == 2) {
-          const u32x4 kl = t.k_low(i, b);
-#pragma unroll
-          for (int j = 0; j < TILES; ++j) s[j][i] = mfma16<true>(kl, q[j][b][0], s[j][i]);
-        }
-      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    load_v(0);
     u32x4 p[TILES], pl[TILES];
 #pragma unroll
     for (int j = 0; j < TILES; ++j) {
       bool seen[2][4];
-      float most = -kInf;
+      float top[2], f[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        top[i] = -kInf;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           if constexpr (MASK) {
             const int pos = at + 16 * i + 4 * quad + r;
             seen[i][r] = (i ? there1 : there0) && pos >= lo[j] && pos < hi[j];
-            most = fmaxf(most, seen[i][r] ? s[j][i][r] : -kInf);
+            top[i] = fmaxf(top[i], seen[i][r] ? s[j][i][r] : -kInf);
           } else {
-            most = fmaxf(most, s[j][i][r]);
+            top[i] = fmaxf(top[i], s[j][i][r]);
           }
         }
-      const float f = factor[j] * down_k;
-      most = fmaf(most, f, float(-up_v));
+        f[i] = factor[j] * __builtin_bit_cast(float, uint32_t(127 - (i ? up_k1 : up_k0)) << 23);
+      }
+      const float most = fmaxf(top[0] * f[0], top[1] * f[1]) - float(up_v);
       if (__builtin_expect(__any(most > ref[j] + 15.0f), 0)) raise(j, most);
       const float from = (ref[j] == -kInf ? 0.0f : ref[j]) + float(up_v);
       float part = 0.0f;
@@ -425,7 +468,7 @@ struct Rows {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float x = __builtin_amdgcn_exp2f(fmaf(s[j][i][r], f, -from));
+          float x = __builtin_amdgcn_exp2f(fmaf(s[j][i][r], f[i], -from));
           if constexpr (MASK) x = seen[i][r] ? x : 0.0f;
           s[j][i][r] = x;
           part += x;
@@ -440,21 +483,22 @@ struct Rows {
       }
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int g = 0; g < kGroups; ++g) {
+      if (g + 1 < kGroups) load_v(g + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const u32x4 v = t.v(b, m);
+      for (int part = 0; part < 2 * PP - 1; ++part)  // V p, then V's low part, then p's
 #pragma unroll
-        for (int j = 0; j < TILES; ++j) {
-          o[j][b][m] = mfma16<true>(v, p[j], o[j][b][m]);
-          if constexpr (PP == 2) o[j][b][m] = mfma16<true>(v, pl[j], o[j][b][m]);
+        for (int c = 0; c < G; ++c) {
+          const int b = g * G + c;
+          if (b >= NB) continue;
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) o[j][b][m] = mfma16<true>(hold[g & 1][c][m][part == 1], part == 2 ? pl[j] : p[j], o[j][b][m]);
         }
-        if constexpr (PP == 2) {
-          const u32x4 vl = t.v_low(b, m);
-#pragma unroll
-          for (int j = 0; j < TILES; ++j) o[j][b][m] = mfma16<true>(vl, p[j], o[j][b][m]);
-        }
-      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   // A new reference for the columns in which products could pass 2^15: they start at 2^7 again.
@@ -590,10 +634,14 @@ __device__ __forceinline__ void wait_copies() {  // until at most N are under wa
 __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // Up to 16 queries at a time: every wave has tokens of its own, 32 of them under way to its
-// part of LDS while it works on 32 others; no barrier before the waves meet.
+// part of LDS while it works on 32 others; no barrier before the waves meet.  Bound by
+// memory where there are many tokens: 64 ragged sequences of up to 16000 (444000 in all, 32 / 8 heads of 128,
+// Q8_0, bf16) take 192 us, 5.0 TB/s.  4-bit codes cost more instructions a byte: 96 sequences of up to 1000
+// tokens of their own behind a prefix (Q4_0, f16) take 30 us, 1.9 TB/s; three workgroups a unit, where
+// they fit, instead of two: 33 -> 30.
 // grid: (k / v heads * splits * sequences (1 for the prefix), row blocks)
 template <bool Q4, int E, int NB, bool PREFIX>
-__global__ __launch_bounds__(256, 2) void kv_attention_few_kernel(const KvAttnArgs a, int splits, int first_slot) {
+__global__ __launch_bounds__(256, Q4 && NB <= 4 ? 3 : 2) void kv_attention_few_kernel(const KvAttnArgs a, int splits, int first_slot) {
   typedef Raw<Q4, NB> R;
   constexpr int kStep = 2 * R::kPieces, kMeet = 3 * NB * 2 * 64;  // 16-byte pieces
   __shared__ u32x4 ring0[kStep * 4 > kMeet ? kStep * 4 : kMeet], ring1[kStep * 4];
@@ -605,8 +653,11 @@ __global__ __launch_bounds__(256, 2) void kv_attention_few_kernel(const KvAttnAr
     Sequences seq;
     if constexpr (PREFIX) seq.look_up(kv, int(base / uint32_t(a.group)), lane);
     Row row[1] = {row_of<PREFIX>(a, seq, base + (lane & 15), sp.rows, sp.kv_head, sp.r0, sp.first_pos, PREFIX ? 0 : a.prefix, sp.cap)};
-    Rows<E, NB, 1> w;
-    w.load(a, row, lane);
+    typedef Rows<E, NB, 1> Wave;
+    Wave w;
+    typename Wave::Fetched q;
+    Wave::fetch_q(a, row[0], lane, q);
+    w.begin(row);
     int u0, u1;
     share_of(w.any_lo >> 4, (w.any_hi + 15) >> 4, splits, sp.split, 8, u0, u1);
     const int first = u0 + 2 * wave, steps = u1 > first ? (u1 - first + 7) >> 3 : 0;  // sets first + 8 n and the next
@@ -620,6 +671,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_few_kernel(const KvAttnAr
     };
     if (steps > 0) {
       fetch(ring0, 0);
+      w.take_q(a, 0, q);
       bool a0 = ahead.page(0, 0) >= 0, a1 = ahead.page(0, 1) >= 0;
       for (int n = 0; n < steps; n += 2) {
         bool b0 = false, b1 = false;
@@ -685,7 +737,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_few_kernel(const KvAttnAr
 template <int NB, int PARTS>
 struct Ready {
   u32x4 kc[PARTS][2][NB][64], vc[PARTS][NB][2][64];
-  int up_k, up_v;
+  int up_k[2], up_v;  // of K's sets
 };
 template <int NB, int PARTS>
 struct ReadyView {
@@ -716,94 +768,111 @@ __device__ __forceinline__ void put_scaled(u32x4 codes, u32x4 scales, u32x4* hi,
   if constexpr (PARTS == 2) *low = l;
 }
 
-// The largest scale of a step's K (plane 0) or V (1), as f16 bits, over the positions from
-// `lo` up to `hi` whose page is there; by a whole wave, the same in every lane.  FINITE: of those
-// that are numbers.
-template <bool FINITE, bool Q4, int NB>
-__device__ __forceinline__ uint32_t top_scale(const Raw<Q4, NB>& raw, int plane, int at, int lo, int hi, int there) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int w0 = 0; w0 < 16 * NB; w0 += 64) {  // words of two tokens
-    const int w = w0 + raw.lane, i = w >= 8 * NB, x = i ? w - 8 * NB : w;
-    if (w < 16 * NB) {
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(raw.bytes(i) + NB * (2 * Raw<Q4, NB>::C + 32 * plane) + x * 4);
-      const int p = at + 16 * i + x / (2 * NB) * 4 + 2 * (x & 1);
-      const bool ok = there >> i & 1;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t half = v >> (16 * r) & 0x7FFFu;
-        if (ok && p + r >= lo && p + r < hi && (!FINITE || half < 0x7C00u)) top = max(top, half);
-      }
-    }
-  }
-  return uint32_t(wave_max(int(top)));
-}
 // Exponent that brings scales below 2^(e - 14), e their largest biased exponent, below 2^8: with codes up to
 // 128 that is 2^15.  2^up is an f16 value.
 __device__ __forceinline__ int up_of(uint32_t top) { return min(15, 22 - int(top >> 10)); }
 __device__ __forceinline__ uint32_t two_to(int up) { return uint32_t(15 + up) << 10; }
 
-// A wave's quarter of a step's operands.  Scales of positions that no row sees are zeros in V (a probability of zero times whatever lies there is
-// zero then); a scale that is no number makes its token's scores NaN.
+// A wave's quarter of a step's operands: a set of K (waves 0 and 1), or half of V's dimensions.
+// Scales of positions outside lo .. hi - 1, which no row sees, are zeros in V (a probability of zero times
+// whatever lies there is zero then).  A scale that is no number makes its token's scores NaN, V's too, and
+// is zero in V.
 template <bool Q4, int NB, int PARTS>
 __device__ __forceinline__ void make_ready(const Raw<Q4, NB>& raw, Ready<NB, PARTS>& to, int wave, int at, int lo, int hi,
                                            int there) {
   constexpr int C = Raw<Q4, NB>::C;
-  const int lane = raw.lane, ln = lane & 15;
-  uint32_t top_k = top_scale<false>(raw, 0, at, lo, hi, there), top_v = top_scale<false>(raw, 1, at, lo, hi, there);
-  const bool bad = top_v >= 0x7C00u;
-  if (__builtin_expect(bad, 0)) top_v = top_scale<true>(raw, 1, at, lo, hi, there);
-  if (__builtin_expect(top_k >= 0x7C00u, 0)) top_k = top_scale<true>(raw, 0, at, lo, hi, there);
-  const int up_k = up_of(top_k), up_v = up_of(top_v);
-  const uint32_t mk = two_to(up_k), mv = two_to(up_v) * 0x10001u;
-  const bool plain = there == 3 && at >= lo && at + 32 <= hi && !bad;
+  const int lane = raw.lane;
+  if (wave < 2) {
+    const int i = wave, ln = lane & 15, p = at + 16 * i + ln;
+    const uint16_t* sc = reinterpret_cast<const uint16_t*>(raw.bytes(i) + 2 * NB * C) + (ln >> 2) * NB * 4 + (ln & 3);
+    uint32_t s[NB], top = 0, worst = 0;
 #pragma unroll
-  for (int x = 0; x < NB; ++x) {
-    const int y = 4 * x + wave;  // K's operands by set and block, then V's
-    if (y < 2 * NB) {
-      const int i = y & 1, b = y >> 1;
-      const uint16_t* sc = reinterpret_cast<const uint16_t*>(raw.bytes(i) + 2 * NB * C) + (ln >> 2) * NB * 4 + (ln & 3);
-      uint32_t s = sc[4 * b];
-      if (!plain && b == 0) {
-        uint32_t worst = 0;
-#pragma unroll
-        for (int z = 0; z < NB; ++z) worst = max(worst, uint32_t(sc[16 * NB + 4 * z]) & 0x7FFFu);
-        if (worst >= 0x7C00u) s = 0x7E00u;
-      }
-      s = pk_mul(s, mk) & 0xFFFFu;
-      s |= s << 16;
-      put_scaled<PARTS>(raw.k(i, b), u32x4{s, s, s, s}, &to.kc[0][i][b][lane], &to.kc[PARTS - 1][i][b][lane]);
-    } else {
-      const int b = (y - 2 * NB) >> 1, m = y & 1;
-      u32x2 s[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        s[i] = raw.vs(i, b);
-        if (!plain) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int p = at + 16 * i + 4 * (lane >> 4) + r;
-            const uint32_t w = s[i][r >> 1], half = w >> (16 * (r & 1)) & 0xFFFFu;
-            if (!(there >> i & 1) || p < lo || p >= hi || (half & 0x7FFFu) >= 0x7C00u) s[i][r >> 1] = w & (r & 1 ? 0xFFFFu : 0xFFFF0000u);
-          }
-        }
-      }
-      put_scaled<PARTS>(raw.v(b, m), u32x4{pk_mul(s[0][0], mv), pk_mul(s[0][1], mv), pk_mul(s[1][0], mv), pk_mul(s[1][1], mv)},
-                        &to.vc[0][b][m][lane], &to.vc[PARTS - 1][b][m][lane]);
+    for (int b = 0; b < NB; ++b) {
+      s[b] = sc[4 * b];
+      worst = max(worst, uint32_t(sc[16 * NB + 4 * b]) & 0x7FFFu);
     }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t half = s[b] & 0x7FFFu;
+      top = max(top, half < 0x7C00u ? half : 0u);
+    }
+    top = uint32_t(row_max((there >> i & 1) && p >= lo && p < hi ? int(top) : 0));  // the four rows hold the same tokens
+    const int up = up_of(uint32_t(__builtin_amdgcn_readfirstlane(int(top))));
+    if (worst >= 0x7C00u) s[0] = 0x7E00u;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t x = pk_mul(s[b] * 0x10001u, two_to(up) * 0x10001u);
+      put_scaled<PARTS>(raw.k(i, b), u32x4{x, x, x, x}, &to.kc[0][i][b][lane], &to.kc[PARTS - 1][i][b][lane]);
+    }
+    if (lane == 0) to.up_k[i] = up;
+  } else {
+    const int m = wave - 2;
+    u32x2 s[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[b][i] = raw.vs(i, b);
+    if (there != 3 || at < lo || at + 32 > hi) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int p = at + 16 * i + 4 * (lane >> 4) + 2 * h;
+          const uint32_t keep = (p >= lo && p < hi ? 0xFFFFu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) s[b][i][h] &= there >> i & 1 ? keep : 0u;
+        }
+    }
+    auto top_of = [&]() -> uint32_t {
+      uint32_t top = 0;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) top = max_u16(top, max_u16(s[b][i][0] & 0x7FFF7FFFu, s[b][i][1] & 0x7FFF7FFFu));
+      top = over_column(top, [](uint32_t a, uint32_t b) { return max_u16(a, b); });
+      return uint32_t(__builtin_amdgcn_readfirstlane(int(max(top & 0xFFFFu, top >> 16))));
+    };
+    uint32_t top = top_of();
+    if (__builtin_expect(top >= 0x7C00u, 0)) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w = s[b][i][h];
+            s[b][i][h] = ((w & 0x7FFFu) < 0x7C00u ? w & 0xFFFFu : 0u) | ((w >> 16 & 0x7FFFu) < 0x7C00u ? w & 0xFFFF0000u : 0u);
+          }
+      top = top_of();
+    }
+    const int up = up_of(top);
+    const uint32_t by = two_to(up) * 0x10001u;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      put_scaled<PARTS>(raw.v(b, m), u32x4{pk_mul(s[b][0][0], by), pk_mul(s[b][0][1], by), pk_mul(s[b][1][0], by), pk_mul(s[b][1][1], by)},
+                        &to.vc[0][b][m][lane], &to.vc[PARTS - 1][b][m][lane]);
+    if (m == 0 && lane == 0) to.up_v = up;
   }
-  if (wave == 0 && lane == 0) to.up_k = up_k, to.up_v = up_v;
 }
 // Many queries: each of the four waves has 16 * TILES rows of its own and all work on the
-// same 32 tokens.  A step's bytes are copied to LDS one step ahead; each wave turns a quarter
-// of its codes into operands, and then works on all of them.
+// same 32 tokens.  A step's bytes are copied to LDS two steps ahead and made into operands, a
+// quarter by each wave, one step ahead, so that a step has one barrier and its vector and
+// matrix instructions come from different steps.  Operands leave LDS a group of blocks ahead of
+// their products.  Bound by vector and matrix instructions in turn (a prefix of 8200 tokens for 384 rows of
+// each of 8 heads of 128, Q4_0, f16: 57 us, of which the steps 37: 2900 clocks for 128 rows and 32 tokens
+// against 1280 of matrix instructions, five products for the definition's two; a chunk of 700 tokens
+// with a window of 1500, 14 / 2 heads of 96, Q8_0, bf16: 29 us, of which the steps 14).  Where two workgroups of a unit would not fit its LDS with two
+// steps of bytes (or one with more than 128 dimensions), the next bytes are copied behind a second barrier.
 template <bool Q4, int E, int NB, int TILES, bool PREFIX>
 __global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(const KvAttnArgs a, int splits, int first_slot) {
   typedef Raw<Q4, NB> R;
   constexpr int kStep = 2 * R::kPieces, kRows = 64 * TILES;
   constexpr int kParts = Rows<E, NB, TILES>::PP;
-  __shared__ u32x4 raw0[kStep], raw1[kStep];
-  __shared__ Ready<NB, kParts> ready;
+  constexpr size_t kRoom = (NB > 4 ? 160 : 80) * 1024 - 64;
+  constexpr bool kTwoRaws = 2 * sizeof(Ready<NB, kParts>) + 32 * kStep <= kRoom;
+  static_assert(2 * sizeof(Ready<NB, kParts>) + 16 * kStep <= kRoom);
+  __shared__ u32x4 raws[kTwoRaws ? 2 : 1][kStep];
+  __shared__ Ready<NB, kParts> ready0, ready1;
   __shared__ int range[4][2];
   const KvArgs& kv = a.kv;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -816,10 +885,14 @@ __global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(
     for (int j = 0; j < TILES; ++j)
       row[j] = row_of<PREFIX>(a, seq, base + wave * (16 * TILES) + 16 * j + (lane & 15), sp.rows, sp.kv_head, sp.r0,
                               sp.first_pos, PREFIX ? 0 : a.prefix, sp.cap);
-    Rows<E, NB, TILES> w;
-    w.load(a, row, lane);
+    typedef Rows<E, NB, TILES> Wave;
+    Wave w;
+    typename Wave::Fetched q[TILES];
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) Wave::fetch_q(a, row[j], lane, q[j]);
+    w.begin(row);
     if (lane == 0) range[wave][0] = w.any_lo < w.any_hi ? w.any_lo : 0x7FFFFFFF, range[wave][1] = w.any_hi;
-    __syncthreads();
+    lds_barrier16();
     const int lo = __builtin_amdgcn_readfirstlane(min(min(range[0][0], range[1][0]), min(range[2][0], range[3][0])));
     const int hi = __builtin_amdgcn_readfirstlane(max(max(range[0][1], range[1][1]), max(range[2][1], range[3][1])));
     int u0, u1;
@@ -841,24 +914,46 @@ __global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(
         if (lane < kHalf % 64) copy_to_lds(src, lane * 16, (part * kHalf + kHalf / 64 * 64) * 16, dst + kHalf / 64 * 64);
       return both;
     };
-    auto turn = [&](const u32x4* raw, u32x4* raw_next, int n, int there, int& there_next) {
+    u32x4 *const raw0 = raws[0], *const raw1 = raws[kTwoRaws ? 1 : 0];
+    int there = 0, there1 = 0, there2 = 0;  // of step n and the next two
+    auto turn = [&](u32x4* raw, const u32x4* raw_next, const Ready<NB, kParts>& ready, Ready<NB, kParts>& ready_next, int n) {
       wait_copies<0>();
-      lds_barrier16();  // step n has landed; nobody works on step n - 1 any more
-      if (n + 1 < steps) there_next = fetch(raw_next, n + 1);
+      lds_barrier16();  // step n is ready, n + 1 has landed; nobody works on step n - 1 any more
       const int at = (u0 + 2 * n) * 16;
-      make_ready(R{raw, lane}, ready, wave, at, lo, hi, there);
-      lds_barrier16();
-      if (at >= w.any_hi || at + 32 <= w.any_lo) return;
-      const ReadyView<NB, kParts> view{&ready, lane};
-      const int up_k = __builtin_amdgcn_readfirstlane(ready.up_k), up_v = __builtin_amdgcn_readfirstlane(ready.up_v);
-      if (there == 3 && at >= w.all_lo && at + 32 <= w.all_hi) w.template fold_step<false>(view, at, true, true, up_k, up_v, lane);
-      else w.template fold_step<true>(view, at, there & 1, there & 2, up_k, up_v, lane);
+      if (kTwoRaws && n + 2 < steps) there2 = fetch(raw, n + 2);
+      if (n + 1 < steps) make_ready(R{raw_next, lane}, ready_next, wave, at + 32, lo, hi, there1);
+      if constexpr (!kTwoRaws) {
+        if (n + 2 < steps) {
+          lds_barrier16();
+          there2 = fetch(raw, n + 2);
+        }
+      }
+      if (at < w.any_hi && at + 32 > w.any_lo) {
+        const ReadyView<NB, kParts> view{&ready, lane};
+        const int k0 = __builtin_amdgcn_readfirstlane(ready.up_k[0]), k1 = __builtin_amdgcn_readfirstlane(ready.up_k[1]);
+        const int v = __builtin_amdgcn_readfirstlane(ready.up_v);
+        if (there == 3 && at >= w.all_lo && at + 32 <= w.all_hi) w.template fold_step<false>(view, at, true, true, k0, k1, v, lane);
+        else w.template fold_step<true>(view, at, there & 1, there & 2, k0, k1, v, lane);
+      }
+      there = there1, there1 = there2;
     };
     if (steps > 0) {
-      int there0 = fetch(raw0, 0), there1 = 0;
+      there = fetch(raw0, 0);
+      if (kTwoRaws && steps > 1) there1 = fetch(raw1, 1);
+#pragma unroll
+      for (int j = 0; j < TILES; ++j) w.take_q(a, j, q[j]);
+      wait_copies<0>();
+      lds_barrier16();
+      make_ready(R{raw0, lane}, ready0, wave, u0 * 16, lo, hi, there);
+      if constexpr (!kTwoRaws) {
+        if (steps > 1) {
+          lds_barrier16();
+          there1 = fetch(raw1, 1);
+        }
+      }
       for (int n = 0; n < steps; n += 2) {
-        turn(raw0, raw1, n, there0, there1);
-        if (n + 1 < steps) turn(raw1, raw0, n + 1, there1, there0);
+        turn(raw0, raw1, ready0, ready1, n);
+        if (n + 1 < steps) turn(raw1, raw0, ready1, ready0, n + 1);
       }
     }
 #pragma unroll

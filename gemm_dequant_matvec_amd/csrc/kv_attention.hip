@@ -8,7 +8,8 @@ namespace {
 constexpr int kThreads = 256;
 
 // out = sum of 2^(ref_i - ref) o_i / sum of 2^(ref_i - ref) sum_i over a row's partial results, in
-// their order, eight of them under way at a time.  A row has D / 4 threads.
+// their order, eight of them under way at a time.  A row has D / 4 threads.  Bound by memory: 3072
+// rows of 128 with 22 parts take 8 us, 4.2 TB/s.
 template <int E>
 __global__ __launch_bounds__(kThreads) void kv_join_kernel(const KvAttnArgs a) {
   constexpr int kAhead = 8;
@@ -62,7 +63,8 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(const KvAttnArgs a) {
 
 // How many parts to cut `tokens` into for `items` workgroups otherwise: up to two workgroups per
 // unit, of 256 tokens at least; beyond that parts of 2048 tokens, which even out sequences of
-// different lengths, up to eight workgroups per place.
+// different lengths, up to eight workgroups per place.  (Parts of a prefix of 8200 tokens with 24 items:
+// 21 of them 96 us the call, 10 of them 123, 5 of them 188.)
 int parts(int64_t items, int64_t tokens) {
   const int64_t fill = std::min(512 / items, (tokens + 255) / 256);
   const int64_t even = std::min((tokens + 2047) / 2048, (4096 + items - 1) / items);
@@ -78,7 +80,8 @@ KvAttentionPlan kv_attention_plan(const qmv_kv_cache& c, const qmv_kv_batch& b, 
     many = rows > 16;
     const int per = many ? kManyRows : 16;
     blocks = int(std::min<int64_t>((rows + per - 1) / per, 65535));
-    splits = parts(c.heads * sequences * blocks, tokens);
+    // blocks that have rows: no more than all rows fill, and one that begins in each sequence
+    splits = parts(c.heads * std::min(sequences * blocks, b.T * group / per + sequences), tokens);
   };
   const int64_t q = std::min(a.max_q, b.T);
   int64_t own = std::max<int64_t>(1, longest - a.prefix);
