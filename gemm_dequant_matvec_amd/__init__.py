@@ -914,7 +914,7 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tens
 
     Rows q_start[b] .. q_start[b + 1] - 1 are the last tokens of sequence b, which is
     kv_len[b] long with them; its page of position p is table[b][p // page] (int32,
-    all three on the device).  Rows from q_start[B] on are left out.
+    all three on the device).  Rows before q_start[0] and from q_start[B] on are left out.
     """
     if stream is not None:
         with torch.cuda.stream(stream):

@@ -17,7 +17,7 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(const KvAttnArgs a) {
   const int mine = threadIdx.x / per, x = threadIdx.x - mine * per;
   const int64_t end = int64_t(kv_row_start(a.kv, a.kv.B)) * a.q_heads;
   if (mine >= rows) return;
-  for (int64_t row = int64_t(blockIdx.x) * rows + mine; row < end; row += int64_t(gridDim.x) * rows) {
+  for (int64_t row = int64_t(kv_row_start(a.kv, 0)) * a.q_heads + int64_t(blockIdx.x) * rows + mine; row < end; row += int64_t(gridDim.x) * rows) {
     const int token = int(row / a.q_heads), h = int(row - int64_t(token) * a.q_heads);
     const float2* st = a.stats + row * a.slots;
     const float* sums = a.sums + row * a.slots * D + 4 * x;

@@ -36,7 +36,7 @@
  * with them (its kv_len[b] - 1 is the last row's position).  Position p of sequence
  * b is token p % page of page table[b][p / page].  q_start, kv_len and table lie on
  * the device and are read when the call runs, so a captured call follows them.
- * Rows from q_start[B] on belong to no sequence and are left as they are.  What does
+ * Rows before q_start[0] and from q_start[B] on belong to no sequence and are left as they are.  What does
  * not fit is absent, not read and not written: a page id outside 0 .. pages - 1, a
  * position past the table's columns, a position below 0 (more rows than kv_len).
  * q_start must not decrease (rows and positions are checked against T all the same).

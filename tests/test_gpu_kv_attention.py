@@ -423,3 +423,26 @@ def test_repeats_and_long_cache(qmv):
         out, A, _, M = attend(q[:, 2 * h:2 * h + 2].double(), k[:, h], v[:, h], torch.ones(1, n, dtype=torch.bool), D ** -0.5)
         tol = A * (128 * 2.0 ** -23 * M[..., None] + 2.0 ** -19 + (n / 32 + 100) * 2.0 ** -23) + n * 2.0 ** -31 * v[:, h].abs().max()
         assert bool(((a[:, 2 * h:2 * h + 2].double().cpu() - out).abs() <= tol + 2.0 ** -24 * out.abs()).all())
+
+
+@pytest.mark.parametrize("prefix,max_kv", [(0, 1), (0, 700), (16, 700)])
+def test_rows_before_the_first_sequence(qmv, prefix, max_kv):
+    """A call on some sequences of a larger batch: q_start begins past 0; with one part and with a join."""
+    c = Case(qmv, "q8_0", "f32", 2, 3, 64, 16, [2, 1, 3], [700, 20, 40], prefix=prefix)
+    cache = qmv.KVCache("q8_0", c.pages, 2, 64, 16, data=c.data.cuda())
+    table, kv_len, q = ints(c.table.tolist()), ints(c.lens), torch.cat([c.q.new_full((5, 6, 64), 9.0), c.q, c.q[:2]]).cuda()
+    out, lse = torch.full_like(q, 7.0), torch.full((13, 6), 7.0, device="cuda")
+    qmv.kv_attention(cache, q, table, ints([s + 5 for s in c.starts]), kv_len, prefix=prefix, max_q=3, max_kv=max_kv, out=out, lse=lse)
+    for x in (out, lse):
+        assert bool((x[:5] == 7.0).all()) and bool((x[11:] == 7.0).all())
+    c.many, c.rounded = bool(prefix), False
+    c.check(out[5:11], lse=lse[5:11])
+    kk, vv = torch.full((13, 2, 64), 7.0, device="cuda"), torch.full((13, 2, 64), 7.0, device="cuda")
+    before = c.data.clone()
+    qmv.kv_read(cache, table, ints([s + 5 for s in c.starts]), kv_len, 13, k=kk, v=vv)
+    assert bool((kk[:5] == 7.0).all()) and bool((vv[11:] == 7.0).all())
+    qmv.kv_write(cache, kk, vv, table, ints([s + 5 for s in c.starts]), kv_len)
+    again = qmv.kv_read(cache, table, ints([s + 5 for s in c.starts]), kv_len, 13, dtype=torch.float32)
+    assert bool(((again[0][5:11] - kk[5:11]).abs() <= kk[5:11].abs().amax() / 100).all())  # quantised twice: a step at most
+    held = cache.data.cpu()
+    assert int((held != before).sum()) <= 6 * 2 * 2 * (64 + 4)
