@@ -320,7 +320,7 @@ struct Rows {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         vs[i][b] = t.vs(i, b);
-        if constexpr (!MASK) top_scale = max_u16(top_scale, max_u16(vs[i][b][0], vs[i][b][1]));
+        if constexpr (!MASK) top_scale = max_u16(top_scale, max_u16(vs[i][b][0] & 0x7FFF7FFFu, vs[i][b][1] & 0x7FFF7FFFu));
       }
 #pragma unroll
     for (int j = 0; j < TILES; ++j) {
@@ -337,7 +337,7 @@ struct Rows {
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               const uint32_t w = vs[i][b][r >> 1];
-              top_v = max(top_v, seen[j][i][r] ? w >> (16 * (r & 1)) & 0xFFFFu : 0u);
+              top_v = max(top_v, seen[j][i][r] ? w >> (16 * (r & 1)) & 0x7FFFu : 0u);
             }
           }
         }

@@ -446,3 +446,20 @@ def test_rows_before_the_first_sequence(qmv, prefix, max_kv):
     assert bool(((again[0][5:11] - kk[5:11]).abs() <= kk[5:11].abs().amax() / 100).all())  # quantised twice: a step at most
     held = cache.data.cpu()
     assert int((held != before).sum()) <= 6 * 2 * 2 * (64 + 4)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0"])
+def test_negative_scales(qmv, fmt, dtype):
+    """Blocks that another program wrote: scales of either sign, the largest of them positive and next to f16's end
+    (products past f16's range if the exponent were taken from the negative ones), few rows and many."""
+    for news in ([1, 2], [1, 40]):
+        c = Case(qmv, fmt, dtype, 2, 2, 64, 16, news, [70, 300], seed=3)
+        sub, codes = kr.set_bytes(fmt, 64), 2 * (1024 if fmt == "q8_0" else 512)
+        half = c.data.view(-1, sub)[:, codes:].view(torch.float16)
+        v = half[:, half.shape[1] // 2:]
+        sign = torch.where(torch.rand(half.shape, generator=gen(5)) < 0.5, -1.0, 1.0)
+        size = torch.where(sign > 0, 500.0, 1 / 1024)[:, half.shape[1] // 2:]
+        v.copy_((v.float() * size).half())
+        half.copy_((half.float() * sign).half())
+        c.check(c.call(max_q=max(news), max_kv=300))
