@@ -894,6 +894,8 @@ def _kv_batch(cache: KVCache, T: int, device: int, table, q_start, kv_len) -> tu
     if table.dim() != 2:
         raise ValueError(f"table has shape {tuple(table.shape)}, expected [sequences][pages]")
     B, columns = table.shape
+    if B < 1 or columns < 1:
+        raise ValueError(f"table has shape {tuple(table.shape)}: no sequences or no pages")
     if q_start.numel() != B + 1 or kv_len.numel() != B:
         raise ValueError(f"q_start holds {q_start.numel()} and kv_len {kv_len.numel()} numbers, the table has {B} sequences")
     for t, what in ((table, "table"), (q_start, "q_start"), (kv_len, "kv_len")):

@@ -743,9 +743,18 @@ static int check_batch(const qmv_kv_cache* c, const qmv_kv_batch* b, bool with_p
   return QMV_OK;
 }
 
-static bool in_cache(const qmv_kv_cache& c, const void* p) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(p), d = reinterpret_cast<uintptr_t>(c.data);
-  return x >= d && x < d + uintptr_t(cache_bytes(c));
+// From the first to the last byte of strided heads (what lies between them may be another tensor's).
+static Range reach(const void* p, int64_t T, int64_t heads, int64_t D, int64_t token, int64_t head, int dtype, const char* name) {
+  typedef __int128 Wide;
+  const Wide t = Wide(T - 1) * token, h = Wide(heads - 1) * head, most = Wide(1) << 46;
+  const Wide lo = std::max<Wide>(-most, (t < 0 ? t : 0) + (h < 0 ? h : 0)), hi = std::min<Wide>(most, (t > 0 ? t : 0) + (h > 0 ? h : 0) + D);
+  const int64_t e = int64_t(element(dtype));
+  return Range{reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) + uintptr_t(int64_t(lo) * e)), int64_t(hi - lo) * e, name};
+}
+
+static bool in_cache(const qmv_kv_cache& c, const Range& r) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(r.p), d = reinterpret_cast<uintptr_t>(c.data);
+  return x < d + uintptr_t(cache_bytes(c)) && d < x + uintptr_t(r.bytes);
 }
 
 static int check_kv_dtype(int dtype) {
@@ -754,7 +763,8 @@ static int check_kv_dtype(int dtype) {
   return QMV_OK;
 }
 
-static int check_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const void* k, const void* v, int dtype) {
+static int check_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const void* k, int64_t k_token, int64_t k_head,
+                    const void* v, int64_t v_token, int64_t v_head, int dtype) {
   int st;
   size_t bytes;
   if ((st = check_cache(cache, true))) return st;
@@ -762,11 +772,12 @@ static int check_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const 
   if ((st = check_batch(cache, batch, true))) return st;
   if ((st = check_kv_dtype(dtype))) return st;
   const void* p[] = {k, v};
+  const int64_t token[] = {k_token, v_token}, head[] = {k_head, v_head};
   const char* names[] = {"k", "v"};
   for (int i = 0; i < 2; ++i) {
     if (!p[i]) continue;
     if (!aligned(p[i], element(dtype))) return fail(QMV_ERR_ALIGN, "%s is not aligned to its element", names[i]);
-    if (in_cache(*cache, p[i])) return fail(QMV_ERR_UNSUPPORTED, "%s lies in the cache", names[i]);
+    if (in_cache(*cache, reach(p[i], batch->T, cache->heads, cache->D, token[i], head[i], dtype, names[i]))) return fail(QMV_ERR_UNSUPPORTED, "%s lies in the cache", names[i]);
   }
   return QMV_OK;
 }
@@ -774,7 +785,7 @@ static int check_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const 
 int qmv_kv_write(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const void* k, int64_t k_token, int64_t k_head,
                  const void* v, int64_t v_token, int64_t v_head, int dtype, void* stream) {
   int st;
-  if ((st = check_kv(cache, batch, k, v, dtype))) return st;
+  if ((st = check_kv(cache, batch, k, k_token, k_head, v, v_token, v_head, dtype))) return st;
   if (!k) return fail(QMV_ERR_NULL, "k is NULL");
   if (!v) return fail(QMV_ERR_NULL, "v is NULL");
   if ((st = check_device())) return st;
@@ -785,7 +796,7 @@ int qmv_kv_write(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const voi
 int qmv_kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, void* k, int64_t k_token, int64_t k_head, void* v,
                 int64_t v_token, int64_t v_head, int dtype, void* stream) {
   int st;
-  if ((st = check_kv(cache, batch, k, v, dtype))) return st;
+  if ((st = check_kv(cache, batch, k, k_token, k_head, v, v_token, v_head, dtype))) return st;
   if (!k && !v) return fail(QMV_ERR_NULL, "k and v are NULL");
   if (k && meets_itself(batch->T, cache->D, cache->heads, k_token, k_head))
     return fail(QMV_ERR_UNSUPPORTED, "k holds some values more than once");
@@ -843,10 +854,12 @@ int qmv_kv_attention(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const
     return fail(QMV_ERR_UNSUPPORTED, "args->out is q with other strides");
   if (meets_itself(batch->T, cache->D, a.q_heads, a.out_token, a.out_head))
     return fail(QMV_ERR_UNSUPPORTED, "args->out holds some values more than once");
-  if (in_cache(*cache, a.out)) return fail(QMV_ERR_UNSUPPORTED, "args->out lies in the cache");
-  if (a.lse && in_cache(*cache, a.lse)) return fail(QMV_ERR_UNSUPPORTED, "args->lse lies in the cache");
-  if (a.lse && (static_cast<const void*>(a.lse) == a.q || static_cast<void*>(a.lse) == a.out))
-    return fail(QMV_ERR_UNSUPPORTED, "args->lse is the buffer of q or out");
+  const Range q = reach(a.q, batch->T, a.q_heads, cache->D, a.q_token, a.q_head, a.dtype, "args->q");
+  const Range out = reach(a.out, batch->T, a.q_heads, cache->D, a.out_token, a.out_head, a.dtype, "args->out");
+  const Range lse{a.lse, a.lse ? 4 * batch->T * a.q_heads : 0, "args->lse"};
+  if (in_cache(*cache, out)) return fail(QMV_ERR_UNSUPPORTED, "args->out lies in the cache");
+  if (a.lse && in_cache(*cache, lse)) return fail(QMV_ERR_UNSUPPORTED, "args->lse lies in the cache");
+  if (a.lse && ((st = check_apart(lse, q)) || (st = check_apart(lse, out)))) return st;
   const qmv::KvAttentionPlan plan = qmv::kv_attention_plan(*cache, *batch, a);
   if (plan.bytes) {
     if ((st = check_buffer(ws, "ws"))) return st;
@@ -854,8 +867,8 @@ int qmv_kv_attention(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const
       return fail(QMV_ERR_SHAPE, "ws_bytes=%llu, the call needs %lld", (unsigned long long)ws_bytes, (long long)plan.bytes);
     const Range w{ws, plan.bytes, "ws"};
     if ((st = check_apart(w, Range{cache->data, cache_bytes(*cache), "the cache"}))) return st;
-    if (a.lse && (st = check_apart(w, Range{a.lse, 4 * batch->T * a.q_heads, "args->lse"}))) return st;
-    if (ws == a.q || ws == a.out) return fail(QMV_ERR_UNSUPPORTED, "ws is the buffer of q or out");
+    if (a.lse && (st = check_apart(w, lse))) return st;
+    if ((st = check_apart(w, q)) || (st = check_apart(w, out))) return st;
   }
   if ((st = check_device())) return st;
   return launched(qmv::launch_kv_attention(*cache, *batch, a, plan, static_cast<uint8_t*>(ws), as_stream(stream)),

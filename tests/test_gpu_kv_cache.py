@@ -218,6 +218,21 @@ def test_many_sequences(qmv, B):
     assert torch.equal(kk.cpu().double(), kr.stands_for("q8_0", k.cpu())) and torch.equal(vv.cpu().double(), kr.stands_for("q8_0", v.cpu()))
 
 
+def test_more_sets_than_workgroups(qmv):
+    """More sequences than one launch has workgroups for: each takes several sets."""
+    B = 530000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((B, 1, 32), device="cuda", generator=g) for _ in range(2))
+    c = qmv.KVCache("q4_0", B, 1, 32, 16)
+    c.data.zero_()
+    table = torch.randperm(B, device="cuda", generator=g).int()[:, None].contiguous()
+    q_start, kv_len = torch.arange(B + 1, device="cuda").int(), (torch.arange(B, device="cuda") % 16 + 1).int()
+    qmv.kv_write(c, k, v, table, q_start, kv_len)
+    kk, vv = qmv.kv_read(c, table, q_start, kv_len, B, dtype=torch.float32)
+    for got, x in ((kk, k), (vv, v)):
+        assert torch.equal(got.cpu().double(), kr.stands_for("q4_0", x.cpu()))
+
+
 def test_past_2_32_bytes(qmv):
     """Pages whose bytes lie past 32-bit offsets."""
     heads, D, page = 8, 128, 64

@@ -69,7 +69,8 @@ def kv(q, name, **kw):
 
 @pytest.mark.parametrize("kw,status,text", SHARED + CALLS + [
     (dict(k=0), NULL, "k is"), (dict(v=0), NULL, "v is"), (dict(k=P + 1), ALIGN, "k is"), (dict(v=3 * P + 1), ALIGN, "v is"),
-    (dict(k=3 * P + 2, dtype=1), ALIGN, "k is"), (dict(k=P), UNSUP, "k lies"), (dict(v=P + 64), UNSUP, "v lies")])
+    (dict(k=3 * P + 2, dtype=1), ALIGN, "k is"), (dict(k=P), UNSUP, "k lies"), (dict(v=P + 64), UNSUP, "v lies"), (dict(k=P - 64), UNSUP, "k lies"),
+    (dict(v=P + (1 << 20), vt=-(1 << 19)), UNSUP, "v lies")])
 def test_write_refusals(q, kw, status, text):
     assert kv(q, "qmv_kv_write", **kw) == status, q.last_error()
     assert text in q.last_error()
@@ -97,7 +98,10 @@ def attend(lib, ws=8 * P, nb=1 << 24, **kw):
     (dict(out=3 * P, ot=512), UNSUP, "other strides"), (dict(ot=128), UNSUP, "more than once"), (dict(out=P), UNSUP, "in the cache"),
     (dict(lse=P), UNSUP, "in the cache"), (dict(lse=4 * P), UNSUP, "lse"), (dict(lse=3 * P), UNSUP, "lse"),
     (dict(prefix=16, ws=0), NULL, "ws"), (dict(prefix=16, ws=8 * P + 8), ALIGN, "ws"), (dict(prefix=16, nb=16), SHAPE, "ws_bytes=16"),
-    (dict(prefix=16, ws=P), UNSUP, "cache"), (dict(prefix=16, ws=3 * P), UNSUP, "ws"), (dict(prefix=16, lse=8 * P), UNSUP, "lse")])
+    (dict(prefix=16, ws=P), UNSUP, "cache"), (dict(out=P - 128), UNSUP, "in the cache"),
+    (dict(lse=P - 16), UNSUP, "in the cache"), (dict(lse=4 * P + 512), UNSUP, "overlaps"), (dict(lse=3 * P - 32), UNSUP, "overlaps"),
+    (dict(prefix=16, ws=3 * P + 64), UNSUP, "overlaps"), (dict(prefix=16, ws=4 * P - 16), UNSUP, "overlaps"),
+    (dict(out=4 * P, ot=-256, lse=4 * P - 512), UNSUP, "overlaps"), (dict(qt=1 << 62, lse=3 * P + 4096), UNSUP, "overlaps"), (dict(prefix=16, ws=3 * P), UNSUP, "ws"), (dict(prefix=16, lse=8 * P), UNSUP, "lse")])
 def test_attention_refusals(q, kw, status, text):
     assert attend(q, **kw) == status, q.last_error()
     assert text in q.last_error()
@@ -137,5 +141,9 @@ def test_binding_refusals(q):
         q.kv_attention(c, x[:, :, :16], i(1, 2), i(2), i(1))
     with pytest.raises(ValueError, match="live on the GPU"):
         q.kv_attention(c, x, i(1, 2), i(2), i(1))
+    with pytest.raises(ValueError, match="no sequences"):
+        q._kv_batch(c, 3, c.data.get_device(), i(0, 2), i(1), i(0))
+    with pytest.raises(ValueError, match="no pages"):
+        q._kv_batch(c, 3, c.data.get_device(), i(1, 0), i(2), i(1))
     with pytest.raises(ValueError, match="records no gradient"):
         q.kv_attention(c, x.requires_grad_(), i(1, 2), i(2), i(1))
