@@ -45,7 +45,7 @@ inline KvArgs kv_args(const qmv_kv_cache& c, const qmv_kv_batch& b) {
 }
 
 // How an attention call is cut: `row_blocks` workgroups share a sequence's rows (many: of the
-// kernel for more than 16 of them), each sequence's tokens go to `splits`; the same for the
+// kernel for more than 64 of them), each sequence's tokens go to `splits`; the same for the
 // shared prefix.  slots: partial results per row (0: the only workgroup of a row writes it).
 struct KvAttentionPlan {
   bool many, prefix_many;

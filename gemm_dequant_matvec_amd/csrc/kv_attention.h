@@ -185,9 +185,12 @@ __device__ __forceinline__ Span span_of(const KvAttnArgs& a, int splits) {
 }
 
 // What a split takes of the sets s0 .. s1 - 1: [u0, u1).  Shares are whole steps of `unit`
-// sets, and 256 tokens at least, so that short sequences end with fewer parts.
-__device__ __forceinline__ void share_of(int s0, int s1, int splits, int split, int unit, int& u0, int& u1) {
-  const int share = (max((s1 - s0 + splits - 1) / splits, 16) + unit - 1) / unit * unit;
+// sets, and `least` sets at least, so that short sequences end with fewer parts.  Many rows, 128 of each of 8
+// heads of 128 over 600 tokens (Q8_0, bf16): parts of 256 tokens 22 us the call, of 128 18, of 64 17; over 4000: 28,
+// 25.5 and 31.
+constexpr int kLeastFew = 16, kLeastMany = 8;
+__device__ __forceinline__ void share_of(int s0, int s1, int splits, int split, int unit, int least, int& u0, int& u1) {
+  const int share = (max((s1 - s0 + splits - 1) / splits, least) + unit - 1) / unit * unit;
   u0 = int(min(int64_t(s1), s0 + int64_t(split) * share));
   u1 = min(s1, u0 + share);
 }
@@ -633,7 +636,7 @@ __device__ __forceinline__ void wait_copies() {  // until at most N are under wa
 // What this wave has read of LDS has arrived: copies may overwrite it.
 __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// Up to 16 queries at a time: every wave has tokens of its own, 32 of them under way to its
+// Blocks of 16 queries, of a sequence that has up to 64 of a head: every wave has tokens of its own, 32 of them under way to its
 // part of LDS while it works on 32 others; no barrier before the waves meet.  Bound by
 // memory where there are many tokens: 64 ragged sequences of up to 16000 (444000 in all, 32 / 8 heads of 128,
 // Q8_0, bf16) take 192 us, 5.0 TB/s.  4-bit codes cost more instructions a byte: 96 sequences of up to 1000
@@ -659,7 +662,7 @@ __global__ __launch_bounds__(256, Q4 && NB <= 4 ? 3 : 2) void kv_attention_few_k
     Wave::fetch_q(a, row[0], lane, q);
     w.begin(row);
     int u0, u1;
-    share_of(w.any_lo >> 4, (w.any_hi + 15) >> 4, splits, sp.split, 8, u0, u1);
+    share_of(w.any_lo >> 4, (w.any_hi + 15) >> 4, splits, sp.split, 8, kLeastFew, u0, u1);
     const int first = u0 + 2 * wave, steps = u1 > first ? (u1 - first + 7) >> 3 : 0;  // sets first + 8 n and the next
     Ahead ahead;
     auto fetch = [&](u32x4* ring, int n) {
@@ -896,7 +899,7 @@ __global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(
     const int lo = __builtin_amdgcn_readfirstlane(min(min(range[0][0], range[1][0]), min(range[2][0], range[3][0])));
     const int hi = __builtin_amdgcn_readfirstlane(max(max(range[0][1], range[1][1]), max(range[2][1], range[3][1])));
     int u0, u1;
-    share_of(lo < hi ? lo >> 4 : 0, lo < hi ? (hi + 15) >> 4 : 0, splits, sp.split, 2, u0, u1);
+    share_of(lo < hi ? lo >> 4 : 0, lo < hi ? (hi + 15) >> 4 : 0, splits, sp.split, 2, kLeastMany, u0, u1);
     const int steps = u1 > u0 ? (u1 - u0 + 1) >> 1 : 0;
     Ahead ahead;
     // wave w copies half w % 2 of set w / 2; returns which sets are there, as bits

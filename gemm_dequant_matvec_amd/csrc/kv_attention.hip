@@ -62,11 +62,11 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(const KvAttnArgs a) {
 }
 
 // How many parts to cut `tokens` into for `items` workgroups otherwise: up to two workgroups per
-// unit, of 256 tokens at least; beyond that parts of 2048 tokens, which even out sequences of
+// unit, of `least` tokens at least; beyond that parts of 2048 tokens, which even out sequences of
 // different lengths, up to eight workgroups per place.  (Parts of a prefix of 8200 tokens with 24 items:
 // 21 of them 96 us the call, 10 of them 123, 5 of them 188.)
-int parts(int64_t items, int64_t tokens) {
-  const int64_t fill = std::min(512 / items, (tokens + 255) / 256);
+int parts(int64_t items, int64_t tokens, int least) {
+  const int64_t fill = std::min(512 / items, (tokens + least - 1) / least);
   const int64_t even = std::min((tokens + 2047) / 2048, (4096 + items - 1) / items);
   return int(std::max<int64_t>({1, std::min<int64_t>(fill, 64), std::min<int64_t>(even, 64)}));
 }
@@ -77,11 +77,15 @@ KvAttentionPlan kv_attention_plan(const qmv_kv_cache& c, const qmv_kv_batch& b, 
   KvAttentionPlan p{};
   const int64_t group = a.q_heads / c.heads, longest = std::min<int64_t>(a.max_kv, b.columns * c.page);
   auto cut = [&](int64_t rows, int64_t sequences, int64_t tokens, bool& many, int& blocks, int& splits) {
-    many = rows > 16;
+    // Up to four blocks of the kernel for few rows, which read the same tokens, beat one of the kernel for many.
+    // 8 sequences of 4000 tokens, 8 heads of 128, Q8_0, bf16, a call in us with 32 / 64 / 96 / 128 rows of a head: 28
+    // / 41 / 62 / 74, with the other kernel 41 / 48 / 51 / 55 (Q4_0, f16: 29 / 46 / 59 / 76 and 49 / 59 / 62 / 67).
+    many = rows > 64;
     const int per = many ? kManyRows : 16;
     blocks = int(std::min<int64_t>((rows + per - 1) / per, 65535));
     // blocks that have rows: no more than all rows fill, and one that begins in each sequence
-    splits = parts(c.heads * std::min(sequences * blocks, b.T * group / per + sequences), tokens);
+    splits = parts(c.heads * std::min(sequences * blocks, b.T * group / per + sequences), tokens,
+                   16 * (many ? kLeastMany : kLeastFew));
   };
   const int64_t q = std::min(a.max_q, b.T);
   int64_t own = std::max<int64_t>(1, longest - a.prefix);

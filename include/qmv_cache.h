@@ -122,8 +122,8 @@ typedef struct qmv_kv_attention_args {
  * products run on the 16-bit matrix cores:
  *   f32 and f16 calls: with K, V and the probabilities in operands of 22 bits (exact for K
  *   and V; two f16 parts), f32 queries too;
- *   bf16 calls: with the probabilities, and from 17 queries of a k / v head on (rows of a
- *   sequence, or of the batch over a prefix, times q_heads / heads) d * q of K and V, rounded
+ *   bf16 calls: with the probabilities, and from 65 queries of a k / v head on (max_q rows of a
+ *   sequence, or all rows over a prefix, times q_heads / heads) d * q of K and V, rounded
  *   once to f16 (11 bits against the result's 8; with an exponent of its own for
  *   every 32 tokens).
  * A row whose q holds a NaN or an infinity is NaN, and one that sees a block which reads

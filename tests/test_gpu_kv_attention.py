@@ -12,7 +12,7 @@ what lies below f16's normal values at most 2^-25 of products that start at 2^6:
 n 2^-31 max |V| for n positions.  Sums over tokens: (n / 32 + 100) 2^-23 A.  Then one
 rounding to the type.  lse: delta + 2^-21 (|lse| + 1).
 
-Calls that put more than 16 queries on a k / v head (of a sequence, or of the batch over a
+Calls that put more than 64 queries on a k / v head (of a sequence, or of the batch over a
 shared prefix) take K and V times their scales as f16 values in bf16: K's rounding adds
 2^-11 M_t to a score, V's and the probability's 2^-11 A each to the result.  In f16 and
 f32 they take two parts of each without the product of the low ones: 2^-22 M_t and
@@ -95,7 +95,7 @@ class Case:
         q = (self.q if q is None else q).cuda()
         kw.setdefault("prefix", self.prefix)
         most = min(kw.get("max_q", -(-q.shape[0] // len(self.news))), q.shape[0])
-        self.many = bool(most * self.group > 16 or (kw["prefix"] and q.shape[0] * self.group > 16))
+        self.many = bool(most * self.group > 64 or (kw["prefix"] and q.shape[0] * self.group > 64))
         self.rounded = self.many and self.dt == torch.bfloat16
         return self.qmv.kv_attention(c, q, ints(self.table.tolist()), ints(self.starts), ints(self.lens), **kw)
 
@@ -232,6 +232,31 @@ def test_what_is_masked_does_not_enter(qmv, fmt, dtype):
     c.check(got)
     assert bool((got[-1] == 0).all())
     c.check(c.call(window=20), window=20)
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_what_is_masked_does_not_enter_for_many_rows(qmv, fmt, dtype):
+    """The same with more rows than one block of few, over a prefix too."""
+    c = Case(qmv, fmt, dtype, 2, 4, 96, 16, [1, 3, 30, 1], [33, 70, 45, 16], prefix=10)
+    c.poison()
+    for kw in (dict(prefix=0), dict()):
+        got = c.call(max_q=30, **kw)
+        c.check(got)
+        assert bool(torch.isfinite(got).all())
+    c.table[1, 2], c.table[2, 1] = -1, c.pages
+    c.check(c.call(max_q=30, prefix=0, window=20), window=20)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows", [16, 17, 33, 64, 65, 128, 129])
+def test_numbers_of_rows(qmv, dtype, rows):
+    """About the ends of a tile, of a block and of the kernels' ranges, one part and several."""
+    c = Case(qmv, "q8_0", dtype, 1, 1, 64, 32, [rows, 2], [rows + 200, 50])
+    for kw in (dict(max_kv=1), dict(max_kv=rows + 200)):
+        c.check(c.call(max_q=rows, **kw))
+    c = Case(qmv, "q4_0", dtype, 2, 1, 32, 16, [1] * rows, [36 + i % 20 for i in range(rows)], prefix=35)
+    c.check(c.call(max_q=1))
 
 
 def test_table_too_short_and_numbers_out_of_order(qmv):
