@@ -11,8 +11,8 @@
 // every head that it takes, stay in registers.  A block works on one tensor (q or
 // k) and computes the sines of its tokens once, into LDS.  Forward, a head is under
 // way while the sines or the head before it are worked on: 16384 tokens of 32 + 8
-// heads of 128, bf16, 103 -> 88 us (3.8 TB/s; a copy reaches 5.1).  Backward the
-// registers that this takes cost more than it gives (117 us without, 4.3 TB/s; 139 with).
+// heads of 128, bf16, 103 -> 88 us, with no more blocks than the chip holds 67 (5.0 TB/s; a copy reaches 5.1).  Backward the
+// registers that this takes cost more than it gives (113 us without, 4.5 TB/s; 139 with).
 //
 // The weights' gradient: a lane sums g n over its heads in f32, the lanes of a wave
 // and the waves of a block that hold the same values are added in a fixed order, a
@@ -397,32 +397,60 @@ NormArgs common(int64_t T, int D, int R, int count, int w_f32, const int64_t* po
 
 }  // namespace
 
+// One launch's worth of blocks, each with its turns: 16384 tokens of 32 + 8 heads of 128, bf16, half layout, take 67
+// us with the 5 blocks that a unit holds, 71 with twice as many, 88 with one turn to a block; interleaved, 75 with 7 of the 8
+// that it may hold, 89 with 8, 82 with one turn.  The tensors share them by heads and a token's sines, which cost about two.
+constexpr int kSineHeads = 2;
+
+// Tokens of a block's turn: the fewest, up to cap, whose heads fill the groups' last round to a few percent (35
+// heads of 130, interleaved, f16, 11638 tokens: 118 us with one token, 98 with five).
+int64_t tokens_of_turn(int64_t heads, int64_t groups, int64_t cap) {
+  int64_t best = 1, best_rounds = (heads + groups - 1) / groups;
+  for (int64_t tb = 1; tb <= cap; ++tb) {
+    const int64_t rounds = (tb * heads + groups - 1) / groups;
+    if (rounds * best < best_rounds * tb) best = tb, best_rounds = rounds;
+    if (rounds * groups * 100 <= tb * heads * 103) break;
+  }
+  return best;
+}
+
 hipError_t launch_norm_rope(int64_t T, int D, int R, int layout, int count, const qmv_norm_rope_tensor* t, int dtype,
                             int w_dtype, float eps, float offset, const int64_t* pos, const float* freqs, float amplitude,
                             hipStream_t s) {
   NormArgs p = common(T, D, R, count, w_dtype == QMV_F32, pos, freqs, amplitude, eps, offset);
-  int J, first = 0, most = 1;
+  int J;
+  int64_t all = 0;
+  for (int i = 0; i < count; ++i) all += t[i].heads + kSineHeads;
   shape_of(D, R, layout == QMV_ROPE_HALF, dtype, p.L, J);
-  for (int i = 0; i < count; ++i) {
-    NormTensor& q = p.t[i];
-    q.x = t[i].x;
-    q.y = t[i].y;
-    q.w = t[i].weight;
-    q.xt = t[i].x_token, q.xh = t[i].x_head, q.yt = t[i].y_token, q.yh = t[i].y_head;
-    q.heads = int(t[i].heads);
-    const int per = q.heads * D * (dtype == QMV_F32 ? 4 : 2);  // bytes of a token
-    const int64_t tb = std::min<int64_t>({std::max(1, 16384 / per), std::max(1, kMaxPairs / (R / 2)),
-                                          std::max<int64_t>(1, T / 512)});
-    q.tb = int(tb);
-    q.first = first;
-    q.blocks = int(std::min<int64_t>((T + tb - 1) / tb, 1 << 20));
-    first += q.blocks;
-    most = std::max(most, q.tb);
-  }
-  const size_t lds = size_t(most) * (R / 2) * sizeof(float2);
   dispatch(dtype, layout == QMV_ROPE_HALF, J, [&](auto e, auto h, auto j) {
-    hipLaunchKernelGGL((norm_rope_kernel<decltype(e)::value, decltype(h)::value, decltype(j)::value>),
-                       dim3(unsigned(first)), dim3(kThreads), lds, s, p);
+    auto kernel = norm_rope_kernel<decltype(e)::value, decltype(h)::value, decltype(j)::value>;
+    static const int64_t resident = [&] {  // blocks of the whole chip
+      int n = 0;
+      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) != hipSuccess || n < 1) {
+        (void)hipGetLastError();
+        n = 4;
+      }
+      return int64_t(256) * std::min(n, 7);
+    }();
+    int first = 0, most = 1;
+    for (int i = 0; i < count; ++i) {
+      NormTensor& q = p.t[i];
+      q.x = t[i].x;
+      q.y = t[i].y;
+      q.w = t[i].weight;
+      q.xt = t[i].x_token, q.xh = t[i].x_head, q.yt = t[i].y_token, q.yh = t[i].y_head;
+      q.heads = int(t[i].heads);
+      const int64_t cap = std::max<int64_t>(1, std::min<int64_t>({32, kMaxPairs / (R / 2), T / 512}));
+      q.tb = int(tokens_of_turn(q.heads, kThreads / p.L, cap));
+      q.first = first;
+      const int64_t turns = (T + q.tb - 1) / q.tb, share = std::max<int64_t>(1, resident * (q.heads + kSineHeads) / all);
+      const int64_t each = (turns + share - 1) / share;
+      q.blocks = int((turns + each - 1) / each);
+      first += q.blocks;
+      most = std::max(most, q.tb);
+    }
+    const size_t lds = size_t(most) * (R / 2) * sizeof(float2);
+    hipLaunchKernelGGL(kernel, dim3(unsigned(first)), dim3(kThreads), lds, s, p);
   });
   return hipGetLastError();
 }
@@ -430,9 +458,11 @@ hipError_t launch_norm_rope(int64_t T, int D, int R, int layout, int count, cons
 NormBackwardPlan norm_backward_plan(int64_t T, int64_t D, int count, const int64_t* heads) {
   NormBackwardPlan plan{};
   int64_t all = 0;
-  for (int i = 0; i < count; ++i) all += heads[i];
+  for (int i = 0; i < count; ++i) all += heads[i] + kSineHeads;
   for (int i = 0; i < count; ++i) {
-    const int64_t cap = std::max<int64_t>(1, 1024 * heads[i] / all);  // four blocks per unit in all
+    // four blocks per unit in all: 16384 tokens of 32 + 8 heads of 128, bf16, half layout, 113 us, interleaved 111;
+    // with three 108 and 120, with five 134 and 113
+    const int64_t cap = std::max<int64_t>(1, 1024 * (heads[i] + kSineHeads) / all);
     const int64_t per = std::max<int64_t>(1, 2048 / (heads[i] * D));  // tokens a block takes at least
     plan.blocks[i] = int(std::max<int64_t>(1, std::min(cap, (T + per - 1) / per)));
     plan.offset[i] = plan.bytes;
