@@ -129,6 +129,19 @@ def test_parity(qmv, layout, dtype, w_dtype, T, hq, hk, D, R):
             assert ko is None and gk is None and gkw is None
 
 
+@pytest.mark.parametrize("T,hq,hk,D,R", [(12001, 5, 3, 24, 16), (7003, 35, 1, 10, 10), (70001, 1, 0, 8, 4)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_many_turns_of_a_block(qmv, layout, T, hq, hk, D, R):
+    """More tokens than one turn of the blocks that the chip holds: also in place."""
+    test_parity(qmv, layout, "bf16", "bf16", T, hq, hk, D, R)
+    q = data((T, hq, D), torch.float16, 8).cuda()
+    k = data((T, hk, D), torch.float16, 9).cuda() if hk else None
+    pos, f = torch.arange(T).cuda(), qmv.rope_freqs(R)
+    want = qmv.norm_rope(q, k, None, None, pos, f, layout=layout)
+    qmv.norm_rope(q, k, None, None, pos, f, layout=layout, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and (not hk or torch.equal(k, want[1]))
+
+
 def setup(qmv, T=37, hq=6, hk=2, D=96, R=64, dt=torch.bfloat16):
     q, k = data((T, hq, D), dt, 11).cuda(), data((T, hk, D), dt, 12).cuda()
     qw, kw = ((1 + data((D,), dt, s, 0.3)).cuda() for s in (13, 14))
