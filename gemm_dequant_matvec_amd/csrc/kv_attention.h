@@ -636,8 +636,9 @@ __device__ __forceinline__ void wait_copies() {  // until at most N are under wa
 // What this wave has read of LDS has arrived: copies may overwrite it.
 __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// Blocks of 16 queries, of a sequence that has up to 64 of a head: every wave has tokens of its own, 32 of them under way to its
-// part of LDS while it works on 32 others; no barrier before the waves meet.  Bound by
+// Blocks of 16 queries, of a sequence that has up to 64 of a head: every wave has tokens of
+// its own, 32 of them under way to its part of LDS while it works on 32 others; no barrier
+// before the waves meet.  Bound by
 // memory where there are many tokens: 64 ragged sequences of up to 16000 (444000 in all, 32 / 8 heads of 128,
 // Q8_0, bf16) take 192 us, 5.0 TB/s.  4-bit codes cost more instructions a byte: 96 sequences of up to 1000
 // tokens of their own behind a prefix (Q4_0, f16) take 30 us, 1.9 TB/s; three workgroups a unit, where
@@ -864,8 +865,9 @@ __device__ __forceinline__ void make_ready(const Raw<Q4, NB>& raw, Ready<NB, PAR
 // their products.  Bound by vector and matrix instructions in turn (a prefix of 8200 tokens for 384 rows of
 // each of 8 heads of 128, Q4_0, f16: 57 us, of which the steps 37: 2900 clocks for 128 rows and 32 tokens
 // against 1280 of matrix instructions, five products for the definition's two; a chunk of 700 tokens
-// with a window of 1500, 14 / 2 heads of 96, Q8_0, bf16: 29 us, of which the steps 14).  Where two workgroups of a unit would not fit its LDS with two
-// steps of bytes (or one with more than 128 dimensions), the next bytes are copied behind a second barrier.
+// with a window of 1500, 14 / 2 heads of 96, Q8_0, bf16: 30 us, of which the steps 14).
+// Where two workgroups of a unit would not fit its LDS with two steps of bytes (or one
+// with more than 128 dimensions), the next bytes are copied behind a second barrier.
 template <bool Q4, int E, int NB, int TILES, bool PREFIX>
 __global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(const KvAttnArgs a, int splits, int first_slot) {
   typedef Raw<Q4, NB> R;

@@ -11,8 +11,9 @@
 // every head that it takes, stay in registers.  A block works on one tensor (q or
 // k) and computes the sines of its tokens once, into LDS.  Forward, a head is under
 // way while the sines or the head before it are worked on: 16384 tokens of 32 + 8
-// heads of 128, bf16, 103 -> 88 us, with no more blocks than the chip holds 67 (5.0 TB/s; a copy reaches 5.1).  Backward the
-// registers that this takes cost more than it gives (113 us without, 4.5 TB/s; 139 with).
+// heads of 128, bf16, 103 -> 88 us, with no more blocks than the chip holds 67 (5.0
+// TB/s; a copy reaches 5.1).  Backward the registers that this takes cost more than
+// it gives (108 us without, 4.7 TB/s, of which the second launch 5; 20 more with).
 //
 // The weights' gradient: a lane sums g n over its heads in f32, the lanes of a wave
 // and the waves of a block that hold the same values are added in a fixed order, a
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_backward_kernel(const Norm
 }
 
 // dw[d] = the sum over the blocks' partial sums, rounded once.  Block: 32 values d,
-// 32 threads for each of them.
+// 32 threads for each of them, with several of their loads under way.
 struct SumArgs {
   struct {
     const float* part;
@@ -337,13 +338,20 @@ struct SumArgs {
 };
 template <int E>
 __global__ __launch_bounds__(1024) void norm_weight_kernel(const SumArgs p) {
+  constexpr int kAhead = 16;
   __shared__ float red[32][33];
   const auto& q = p.t[blockIdx.y];
   if (!q.dw) return;
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, d = blockIdx.x * 32 + x;
   float s = 0.0f;
   if (d < p.D)
-    for (int b = y; b < q.blocks; b += 32) s += q.part[int64_t(b) * p.D + d];
+    for (int b0 = y; b0 < q.blocks; b0 += 32 * kAhead) {
+      float v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) v[i] = b0 + 32 * i < q.blocks ? q.part[int64_t(b0 + 32 * i) * p.D + d] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) s += v[i];
+    }
   red[y][x] = s;
   __syncthreads();
   for (int h = 16; h > 0; h >>= 1) {
@@ -460,8 +468,8 @@ NormBackwardPlan norm_backward_plan(int64_t T, int64_t D, int count, const int64
   int64_t all = 0;
   for (int i = 0; i < count; ++i) all += heads[i] + kSineHeads;
   for (int i = 0; i < count; ++i) {
-    // four blocks per unit in all: 16384 tokens of 32 + 8 heads of 128, bf16, half layout, 113 us, interleaved 111;
-    // with three 108 and 120, with five 134 and 113
+    // four blocks per unit in all: 16384 tokens of 32 + 8 heads of 128, bf16, half layout, 113 us (before the second
+    // launch's loads ran ahead: 108 now), interleaved 111; with three 108 and 120, with five 134 and 113
     const int64_t cap = std::max<int64_t>(1, 1024 * (heads[i] + kSineHeads) / all);
     const int64_t per = std::max<int64_t>(1, 2048 / (heads[i] * D));  // tokens a block takes at least
     plan.blocks[i] = int(std::max<int64_t>(1, std::min(cap, (T + per - 1) / per)));
