@@ -488,3 +488,50 @@ def test_negative_scales(qmv, fmt, dtype):
         v.copy_((v.float() * size).half())
         half.copy_((half.float() * sign).half())
         c.check(c.call(max_q=max(news), max_kv=300))
+
+
+@pytest.mark.parametrize("group", [2, 33])
+def test_prefix_of_a_batch_with_many_sequences_without_rows(qmv, group):
+    """Rows whose sequences lie far apart, next to each other and last, in the kernels for few and for many rows."""
+    news, lens = [0] * 300, [20 + b % 7 for b in range(300)]
+    for b in (0, 90, 91, 200, 299):
+        news[b] = 1
+    news[91] = 2
+    c = Case(qmv, "q8_0", "f32", 1, group, 32, 16, news, lens, prefix=16)
+    c.check(c.call(max_q=2))
+
+
+def test_first_call_of_a_process_in_a_capture():
+    """Nothing that a first call sets up gets in the way of a capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, gemm_dequant_matvec_amd as qmv
+dev = "cuda"
+q = torch.randn(3000, 4, 64, device=dev).half(); k = torch.randn(3000, 2, 64, device=dev).half()
+pos, f = torch.arange(3000, device=dev), qmv.rope_freqs(64)
+c = qmv.KVCache("q8_0", 40, 2, 64, 128)
+c.data.zero_()
+t = torch.arange(40, device=dev).int()[None].contiguous()
+n = torch.tensor([3000], dtype=torch.int32, device=dev)
+s = torch.tensor([0, 3000], dtype=torch.int32, device=dev)
+torch.cuda.synchronize()
+def step():
+    a, b = qmv.norm_rope(q, k, None, None, pos, f)
+    qmv.kv_write(c, b, k, t, s, n)
+    return qmv.kv_attention(c, a, t, s, n), qmv.norm_rope_backward(q, k, None, None, a, b, pos, f)[0]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = step()
+for turn in range(3):
+    q.normal_(); k.normal_()
+    g.replay()
+    want = step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(out, want)), turn
+print("captured first")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=90, cwd=root)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
