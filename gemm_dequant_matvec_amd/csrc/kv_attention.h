@@ -777,17 +777,19 @@ __device__ __forceinline__ void put_scaled(u32x4 codes, u32x4 scales, u32x4* hi,
 __device__ __forceinline__ int up_of(uint32_t top) { return min(15, 22 - int(top >> 10)); }
 __device__ __forceinline__ uint32_t two_to(int up) { return uint32_t(15 + up) << 10; }
 
-// A wave's quarter of a step's operands: a set of K (waves 0 and 1), or half of V's dimensions.
+// A wave's share of a step's operands: a set of K, or half of V's dimensions; with eight waves
+// half of the blocks of those.
 // Scales of positions outside lo .. hi - 1, which no row sees, are zeros in V (a probability of zero times
 // whatever lies there is zero then).  A scale that is no number makes its token's scores NaN, V's too, and
 // is zero in V.
-template <bool Q4, int NB, int PARTS>
+template <int WAVES, bool Q4, int NB, int PARTS>
 __device__ __forceinline__ void make_ready(const Raw<Q4, NB>& raw, Ready<NB, PARTS>& to, int wave, int at, int lo, int hi,
                                            int there) {
   constexpr int C = Raw<Q4, NB>::C;
-  const int lane = raw.lane;
-  if (wave < 2) {
-    const int i = wave, ln = lane & 15, p = at + 16 * i + ln;
+  const int lane = raw.lane, share = wave >> 2;
+  auto mine = [&](int b) { return WAVES == 4 || (b >= (NB + 1) / 2) == (share != 0); };
+  if ((wave & 3) < 2) {
+    const int i = wave & 1, ln = lane & 15, p = at + 16 * i + ln;
     const uint16_t* sc = reinterpret_cast<const uint16_t*>(raw.bytes(i) + 2 * NB * C) + (ln >> 2) * NB * 4 + (ln & 3);
     uint32_t s[NB], top = 0, worst = 0;
 #pragma unroll
@@ -805,12 +807,13 @@ __device__ __forceinline__ void make_ready(const Raw<Q4, NB>& raw, Ready<NB, PAR
     if (worst >= 0x7C00u) s[0] = 0x7E00u;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+      if (!mine(b)) continue;
       const uint32_t x = pk_mul(s[b] * 0x10001u, two_to(up) * 0x10001u);
       put_scaled<PARTS>(raw.k(i, b), u32x4{x, x, x, x}, &to.kc[0][i][b][lane], &to.kc[PARTS - 1][i][b][lane]);
     }
-    if (lane == 0) to.up_k[i] = up;
+    if (!share && lane == 0) to.up_k[i] = up;
   } else {
-    const int m = wave - 2;
+    const int m = wave & 1;
     u32x2 s[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -852,13 +855,15 @@ __device__ __forceinline__ void make_ready(const Raw<Q4, NB>& raw, Ready<NB, PAR
     const int up = up_of(top);
     const uint32_t by = two_to(up) * 0x10001u;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < NB; ++b) {
+      if (!mine(b)) continue;
       put_scaled<PARTS>(raw.v(b, m), u32x4{pk_mul(s[b][0][0], by), pk_mul(s[b][0][1], by), pk_mul(s[b][1][0], by), pk_mul(s[b][1][1], by)},
                         &to.vc[0][b][m][lane], &to.vc[PARTS - 1][b][m][lane]);
-    if (m == 0 && lane == 0) to.up_v = up;
+    }
+    if (m == 0 && !share && lane == 0) to.up_v = up;
   }
 }
-// Many queries: each of the four waves has 16 * TILES rows of its own and all work on the
+// Many queries: each of the four or eight waves has 16 * TILES rows of its own and all work on the
 // same 32 tokens.  A step's bytes are copied to LDS two steps ahead and made into operands, a
 // quarter by each wave, one step ahead, so that a step has one barrier and its vector and
 // matrix instructions come from different steps.  Operands leave LDS a group of blocks ahead of
@@ -868,17 +873,17 @@ __device__ __forceinline__ void make_ready(const Raw<Q4, NB>& raw, Ready<NB, PAR
 // with a window of 1500, 14 / 2 heads of 96, Q8_0, bf16: 30 us, of which the steps 14).
 // Where two workgroups of a unit would not fit its LDS with two steps of bytes (or one
 // with more than 128 dimensions), the next bytes are copied behind a second barrier.
-template <bool Q4, int E, int NB, int TILES, bool PREFIX>
-__global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(const KvAttnArgs a, int splits, int first_slot) {
+template <bool Q4, int E, int NB, int WAVES, int TILES, bool PREFIX>
+__global__ __launch_bounds__(64 * WAVES, 2) void kv_attention_many_kernel(const KvAttnArgs a, int splits, int first_slot) {
   typedef Raw<Q4, NB> R;
-  constexpr int kStep = 2 * R::kPieces, kRows = 64 * TILES;
+  constexpr int kStep = 2 * R::kPieces, kRows = 16 * TILES * WAVES;
   constexpr int kParts = Rows<E, NB, TILES>::PP;
   constexpr size_t kRoom = (NB > 4 ? 160 : 80) * 1024 - 64;
   constexpr bool kTwoRaws = 2 * sizeof(Ready<NB, kParts>) + 32 * kStep <= kRoom;
   static_assert(2 * sizeof(Ready<NB, kParts>) + 16 * kStep <= kRoom);
   __shared__ u32x4 raws[kTwoRaws ? 2 : 1][kStep];
   __shared__ Ready<NB, kParts> ready0, ready1;
-  __shared__ int range[4][2];
+  __shared__ int range[WAVES][2];
   const KvArgs& kv = a.kv;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Span sp = span_of<PREFIX>(a, splits);
@@ -898,25 +903,28 @@ __global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(
     w.begin(row);
     if (lane == 0) range[wave][0] = w.any_lo < w.any_hi ? w.any_lo : 0x7FFFFFFF, range[wave][1] = w.any_hi;
     lds_barrier16();
-    const int lo = __builtin_amdgcn_readfirstlane(min(min(range[0][0], range[1][0]), min(range[2][0], range[3][0])));
-    const int hi = __builtin_amdgcn_readfirstlane(max(max(range[0][1], range[1][1]), max(range[2][1], range[3][1])));
+    int lo = range[0][0], hi = range[0][1];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) lo = min(lo, range[i][0]), hi = max(hi, range[i][1]);
+    lo = __builtin_amdgcn_readfirstlane(lo), hi = __builtin_amdgcn_readfirstlane(hi);
     int u0, u1;
     share_of(lo < hi ? lo >> 4 : 0, lo < hi ? (hi + 15) >> 4 : 0, splits, sp.split, 2, kLeastMany, u0, u1);
     const int steps = u1 > u0 ? (u1 - u0 + 1) >> 1 : 0;
     Ahead ahead;
-    // wave w copies half w % 2 of set w / 2; returns which sets are there, as bits
+    // half of the waves copy a set, a part each; returns which sets are there, as bits
     auto fetch = [&](u32x4* raw, int n) -> int {
       if ((n & 31) == 0) ahead.look_up(kv, sp.table, u0, 2, n, u1, lane);
-      const int i = wave >> 1, part = wave & 1, p0 = ahead.page(n, 0), p1 = ahead.page(n, 1);
+      const int i = wave / (WAVES / 2), part = wave % (WAVES / 2), p0 = ahead.page(n, 0), p1 = ahead.page(n, 1);
       const int both = int(p0 >= 0) | int(p1 >= 0) << 1;
       const Buf src = buffer_of(kv.data + max(i ? p1 : p0, 0) * kv.page_bytes + int64_t(sp.kv_head) * kv.head_bytes +
                                 (i ? ahead.place(n, 1) : ahead.place(n, 0)) * kv.set_bytes);
-      constexpr int kHalf = R::kPieces / 2;  // kPieces is even
-      u32x4* dst = raw + i * R::kPieces + part * kHalf;
+      constexpr int kPart = R::kPieces / (WAVES / 2);
+      static_assert(kPart * (WAVES / 2) == R::kPieces);
+      u32x4* dst = raw + i * R::kPieces + part * kPart;
 #pragma unroll
-      for (int c = 0; c < kHalf / 64; ++c) copy_to_lds(src, lane * 16, (part * kHalf + c * 64) * 16, dst + c * 64);
-      if constexpr (kHalf % 64 != 0)
-        if (lane < kHalf % 64) copy_to_lds(src, lane * 16, (part * kHalf + kHalf / 64 * 64) * 16, dst + kHalf / 64 * 64);
+      for (int c = 0; c < kPart / 64; ++c) copy_to_lds(src, lane * 16, (part * kPart + c * 64) * 16, dst + c * 64);
+      if constexpr (kPart % 64 != 0)
+        if (lane < kPart % 64) copy_to_lds(src, lane * 16, (part * kPart + kPart / 64 * 64) * 16, dst + kPart / 64 * 64);
       return both;
     };
     u32x4 *const raw0 = raws[0], *const raw1 = raws[kTwoRaws ? 1 : 0];
@@ -926,7 +934,7 @@ __global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(
       lds_barrier16();  // step n is ready, n + 1 has landed; nobody works on step n - 1 any more
       const int at = (u0 + 2 * n) * 16;
       if (kTwoRaws && n + 2 < steps) there2 = fetch(raw, n + 2);
-      if (n + 1 < steps) make_ready(R{raw_next, lane}, ready_next, wave, at + 32, lo, hi, there1);
+      if (n + 1 < steps) make_ready<WAVES>(R{raw_next, lane}, ready_next, wave, at + 32, lo, hi, there1);
       if constexpr (!kTwoRaws) {
         if (n + 2 < steps) {
           lds_barrier16();
@@ -949,7 +957,7 @@ __global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(
       for (int j = 0; j < TILES; ++j) w.take_q(a, j, q[j]);
       wait_copies<0>();
       lds_barrier16();
-      make_ready(R{raw0, lane}, ready0, wave, u0 * 16, lo, hi, there);
+      make_ready<WAVES>(R{raw0, lane}, ready0, wave, u0 * 16, lo, hi, there);
       if constexpr (!kTwoRaws) {
         if (steps > 1) {
           lds_barrier16();
@@ -972,24 +980,26 @@ __global__ __launch_bounds__(256, NB > 4 ? 1 : 2) void kv_attention_many_kernel(
 
 }  // namespace
 
-constexpr int kManyTiles = 2;  // tiles of 16 rows that a wave of the many-row kernel holds
-constexpr int kManyRows = 64 * kManyTiles;
+constexpr int kManyRows = 128;  // of a workgroup of the kernel for many
 
 // One head size's launches.
 template <bool Q4, int E, int NB>
 hipError_t kv_attention_go(const KvAttnArgs& a, const KvAttentionPlan& p, hipStream_t s) {
   const unsigned heads = unsigned(a.kv.heads);
-  constexpr int T = kManyTiles;
+  // 128 rows of heads of more than 128 values: eight waves of one tile, as four of two would need all registers of
+  // their unit (a chunk of 700 tokens of 16 heads over 6000, Q8_0: bf16, 256 values 240 -> 203 us, f16, 160 values 224 -> 178)
+  constexpr int W = NB > 4 ? 8 : 4, T = kManyRows / (16 * W);
+  constexpr unsigned kMany = 64 * W;
   if (a.prefix) {
     const dim3 grid(heads * unsigned(p.prefix_splits), unsigned(p.prefix_row_blocks), 1);
-    if (p.prefix_many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, T, true>), grid, dim3(256), 0, s, a, p.prefix_splits, 0);
+    if (p.prefix_many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, W, T, true>), grid, dim3(kMany), 0, s, a, p.prefix_splits, 0);
     else hipLaunchKernelGGL((kv_attention_few_kernel<Q4, E, NB, true>), grid, dim3(256), 0, s, a, p.prefix_splits, 0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const int first = a.prefix ? p.prefix_splits : 0;
   const dim3 grid(heads * unsigned(p.splits) * unsigned(a.kv.B), unsigned(p.row_blocks), 1);
-  if (p.many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, T, false>), grid, dim3(256), 0, s, a, p.splits, first);
+  if (p.many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, W, T, false>), grid, dim3(kMany), 0, s, a, p.splits, first);
   else hipLaunchKernelGGL((kv_attention_few_kernel<Q4, E, NB, false>), grid, dim3(256), 0, s, a, p.splits, first);
   return hipGetLastError();
 }

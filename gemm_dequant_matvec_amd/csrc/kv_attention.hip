@@ -80,7 +80,7 @@ KvAttentionPlan kv_attention_plan(const qmv_kv_cache& c, const qmv_kv_batch& b, 
     // Up to four blocks of the kernel for few rows, which read the same tokens, beat one of the kernel for many.
     // 8 sequences of 4000 tokens, 8 heads of 128, Q8_0, bf16, a call in us with 32 / 64 / 96 / 128 rows of a head: 28
     // / 41 / 62 / 74, with the other kernel 41 / 48 / 51 / 55 (Q4_0, f16: 29 / 46 / 59 / 76 and 49 / 59 / 62 / 67).
-    many = rows > 64;
+    many = rows > 64 && c.heads * sequences <= 1 << 22;  // up to 512 threads each, counted in 32 bits
     const int per = many ? kManyRows : 16;
     blocks = int(std::min<int64_t>((rows + per - 1) / per, 65535));
     // blocks that have rows: no more than all rows fill, and one that begins in each sequence
