@@ -744,12 +744,15 @@ static int check_batch(const qmv_kv_cache* c, const qmv_kv_batch* b, bool with_p
 }
 
 // From the first to the last byte of strided heads (what lies between them may be another tensor's).
-static Range reach(const void* p, int64_t T, int64_t heads, int64_t D, int64_t token, int64_t head, int dtype, const char* name) {
+static Range reach(const void* p, int64_t T, int64_t heads, int64_t D, int64_t token, int64_t head, int dtype,
+                   const char* name) {
   typedef __int128 Wide;
   const Wide t = Wide(T - 1) * token, h = Wide(heads - 1) * head, most = Wide(1) << 46;
-  const Wide lo = std::max<Wide>(-most, (t < 0 ? t : 0) + (h < 0 ? h : 0)), hi = std::min<Wide>(most, (t > 0 ? t : 0) + (h > 0 ? h : 0) + D);
+  const Wide lo = std::max<Wide>(-most, (t < 0 ? t : 0) + (h < 0 ? h : 0));
+  const Wide hi = std::min<Wide>(most, (t > 0 ? t : 0) + (h > 0 ? h : 0) + D);
   const int64_t e = int64_t(element(dtype));
-  return Range{reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) + uintptr_t(int64_t(lo) * e)), int64_t(hi - lo) * e, name};
+  const uintptr_t from = reinterpret_cast<uintptr_t>(p) + uintptr_t(int64_t(lo) * e);
+  return Range{reinterpret_cast<const void*>(from), int64_t(hi - lo) * e, name};
 }
 
 static bool in_cache(const qmv_kv_cache& c, const Range& r) {
@@ -777,7 +780,8 @@ static int check_kv(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const 
   for (int i = 0; i < 2; ++i) {
     if (!p[i]) continue;
     if (!aligned(p[i], element(dtype))) return fail(QMV_ERR_ALIGN, "%s is not aligned to its element", names[i]);
-    if (in_cache(*cache, reach(p[i], batch->T, cache->heads, cache->D, token[i], head[i], dtype, names[i]))) return fail(QMV_ERR_UNSUPPORTED, "%s lies in the cache", names[i]);
+    if (in_cache(*cache, reach(p[i], batch->T, cache->heads, cache->D, token[i], head[i], dtype, names[i])))
+      return fail(QMV_ERR_UNSUPPORTED, "%s lies in the cache", names[i]);
   }
   return QMV_OK;
 }

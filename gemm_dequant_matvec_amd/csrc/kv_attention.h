@@ -62,7 +62,8 @@ template <class T, class F>
 __device__ __forceinline__ T over_column(T v, F f) {
   const uint32_t x = __builtin_bit_cast(uint32_t, v);
   const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-  const uint32_t y = __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(T, uint32_t(a[0])), __builtin_bit_cast(T, uint32_t(a[1]))));
+  const T two = f(__builtin_bit_cast(T, uint32_t(a[0])), __builtin_bit_cast(T, uint32_t(a[1])));
+  const uint32_t y = __builtin_bit_cast(uint32_t, two);
   const auto b = __builtin_amdgcn_permlane32_swap(y, y, false, false);
   return f(__builtin_bit_cast(T, uint32_t(b[0])), __builtin_bit_cast(T, uint32_t(b[1])));
 }
@@ -381,7 +382,8 @@ struct Rows {
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = pack16<true>(pv[2 * i], pv[2 * i + 1]);
           p[i] = w;
-          if constexpr (PP == 2) pl[i] = pack16<true>(pv[2 * i] - unpack16<true>(w & 0xFFFFu), pv[2 * i + 1] - unpack16<true>(w >> 16));
+          if constexpr (PP == 2)
+            pl[i] = pack16<true>(pv[2 * i] - unpack16<true>(w & 0xFFFFu), pv[2 * i + 1] - unpack16<true>(w >> 16));
         }
         o[j][b][0] = mfma16<true>(v0, p, o[j][b][0]);
         o[j][b][1] = mfma16<true>(v1, p, o[j][b][1]);
@@ -396,7 +398,8 @@ struct Rows {
   // (bf16 calls) or as two f16 parts, without the product of two low parts.  The probabilities enter
   // as p 2^-up_v, which the reference keeps below 2^15 as above.
   template <bool MASK, class T>
-  __device__ __forceinline__ void fold_step(const T& t, int at, bool there0, bool there1, int up_k0, int up_k1, int up_v, int lane) {
+  __device__ __forceinline__ void fold_step(const T& t, int at, bool there0, bool there1, int up_k0, int up_k1, int up_v,
+                                            int lane) {
     const int quad = lane >> 4;
     const float up = __builtin_bit_cast(float, uint32_t(127 + up_v) << 23);
     f32x4 s[TILES][2];
@@ -498,7 +501,8 @@ struct Rows {
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int j = 0; j < TILES; ++j) o[j][b][m] = mfma16<true>(hold[g & 1][c][m][part == 1], part == 2 ? pl[j] : p[j], o[j][b][m]);
+            for (int j = 0; j < TILES; ++j)
+              o[j][b][m] = mfma16<true>(hold[g & 1][c][m][part == 1], part == 2 ? pl[j] : p[j], o[j][b][m]);
         }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -645,7 +649,8 @@ __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)"
 // they fit, instead of two: 33 -> 30.
 // grid: (k / v heads * splits * sequences (1 for the prefix), row blocks)
 template <bool Q4, int E, int NB, bool PREFIX>
-__global__ __launch_bounds__(256, Q4 && NB <= 4 ? 3 : 2) void kv_attention_few_kernel(const KvAttnArgs a, int splits, int first_slot) {
+__global__ __launch_bounds__(256, Q4 && NB <= 4 ? 3 : 2) void kv_attention_few_kernel(const KvAttnArgs a, int splits,
+                                                                                      int first_slot) {
   typedef Raw<Q4, NB> R;
   constexpr int kStep = 2 * R::kPieces, kMeet = 3 * NB * 2 * 64;  // 16-byte pieces
   __shared__ u32x4 ring0[kStep * 4 > kMeet ? kStep * 4 : kMeet], ring1[kStep * 4];
@@ -656,7 +661,8 @@ __global__ __launch_bounds__(256, Q4 && NB <= 4 ? 3 : 2) void kv_attention_few_k
   for (uint32_t base = blockIdx.y * 16; base < sp.rows; base += gridDim.y * 16) {
     Sequences seq;
     if constexpr (PREFIX) seq.look_up(kv, int(base / uint32_t(a.group)), lane);
-    Row row[1] = {row_of<PREFIX>(a, seq, base + (lane & 15), sp.rows, sp.kv_head, sp.r0, sp.first_pos, PREFIX ? 0 : a.prefix, sp.cap)};
+    Row row[1] = {row_of<PREFIX>(a, seq, base + (lane & 15), sp.rows, sp.kv_head, sp.r0, sp.first_pos, PREFIX ? 0 : a.prefix,
+                                 sp.cap)};
     typedef Rows<E, NB, 1> Wave;
     Wave w;
     typename Wave::Fetched q;
@@ -857,8 +863,8 @@ __device__ __forceinline__ void make_ready(const Raw<Q4, NB>& raw, Ready<NB, PAR
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if (!mine(b)) continue;
-      put_scaled<PARTS>(raw.v(b, m), u32x4{pk_mul(s[b][0][0], by), pk_mul(s[b][0][1], by), pk_mul(s[b][1][0], by), pk_mul(s[b][1][1], by)},
-                        &to.vc[0][b][m][lane], &to.vc[PARTS - 1][b][m][lane]);
+      const u32x4 x = {pk_mul(s[b][0][0], by), pk_mul(s[b][0][1], by), pk_mul(s[b][1][0], by), pk_mul(s[b][1][1], by)};
+      put_scaled<PARTS>(raw.v(b, m), x, &to.vc[0][b][m][lane], &to.vc[PARTS - 1][b][m][lane]);
     }
     if (m == 0 && !share && lane == 0) to.up_v = up;
   }
@@ -945,8 +951,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_attention_many_kernel(const 
         const ReadyView<NB, kParts> view{&ready, lane};
         const int k0 = __builtin_amdgcn_readfirstlane(ready.up_k[0]), k1 = __builtin_amdgcn_readfirstlane(ready.up_k[1]);
         const int v = __builtin_amdgcn_readfirstlane(ready.up_v);
-        if (there == 3 && at >= w.all_lo && at + 32 <= w.all_hi) w.template fold_step<false>(view, at, true, true, k0, k1, v, lane);
-        else w.template fold_step<true>(view, at, there & 1, there & 2, k0, k1, v, lane);
+        if (there == 3 && at >= w.all_lo && at + 32 <= w.all_hi)
+          w.template fold_step<false>(view, at, true, true, k0, k1, v, lane);
+        else
+          w.template fold_step<true>(view, at, there & 1, there & 2, k0, k1, v, lane);
       }
       there = there1, there1 = there2;
     };
@@ -992,15 +1000,16 @@ hipError_t kv_attention_go(const KvAttnArgs& a, const KvAttentionPlan& p, hipStr
   constexpr unsigned kMany = 64 * W;
   if (a.prefix) {
     const dim3 grid(heads * unsigned(p.prefix_splits), unsigned(p.prefix_row_blocks), 1);
-    if (p.prefix_many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, W, T, true>), grid, dim3(kMany), 0, s, a, p.prefix_splits, 0);
-    else hipLaunchKernelGGL((kv_attention_few_kernel<Q4, E, NB, true>), grid, dim3(256), 0, s, a, p.prefix_splits, 0);
+    const int n = p.prefix_splits;
+    if (p.prefix_many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, W, T, true>), grid, dim3(kMany), 0, s, a, n, 0);
+    else hipLaunchKernelGGL((kv_attention_few_kernel<Q4, E, NB, true>), grid, dim3(256), 0, s, a, n, 0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int first = a.prefix ? p.prefix_splits : 0;
+  const int first = a.prefix ? p.prefix_splits : 0, n = p.splits;
   const dim3 grid(heads * unsigned(p.splits) * unsigned(a.kv.B), unsigned(p.row_blocks), 1);
-  if (p.many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, W, T, false>), grid, dim3(kMany), 0, s, a, p.splits, first);
-  else hipLaunchKernelGGL((kv_attention_few_kernel<Q4, E, NB, false>), grid, dim3(256), 0, s, a, p.splits, first);
+  if (p.many) hipLaunchKernelGGL((kv_attention_many_kernel<Q4, E, NB, W, T, false>), grid, dim3(kMany), 0, s, a, n, first);
+  else hipLaunchKernelGGL((kv_attention_few_kernel<Q4, E, NB, false>), grid, dim3(256), 0, s, a, n, first);
   return hipGetLastError();
 }
 

@@ -292,8 +292,9 @@ hipError_t launch(const qmv_kv_cache& c, const qmv_kv_batch& b, const KvHeads& k
   const KvArgs a = kv_args(c, b);
   const dim3 grid(unsigned(std::min<int64_t>((b.T >> 4) + 2 * b.B, 1 << 20)));
   auto go = [&](auto e) {
-    if (c.fmt == QMV_Q4_0) hipLaunchKernelGGL((kv_cache_kernel<decltype(e)::value, true, WRITE>), grid, dim3(kThreads), 0, s, a, k, v);
-    else hipLaunchKernelGGL((kv_cache_kernel<decltype(e)::value, false, WRITE>), grid, dim3(kThreads), 0, s, a, k, v);
+    constexpr int E = decltype(e)::value;
+    if (c.fmt == QMV_Q4_0) hipLaunchKernelGGL((kv_cache_kernel<E, true, WRITE>), grid, dim3(kThreads), 0, s, a, k, v);
+    else hipLaunchKernelGGL((kv_cache_kernel<E, false, WRITE>), grid, dim3(kThreads), 0, s, a, k, v);
   };
   if (dtype == QMV_F32) go(std::integral_constant<int, 0>{});
   else if (dtype == QMV_F16) go(std::integral_constant<int, 1>{});

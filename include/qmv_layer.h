@@ -2,8 +2,8 @@
  * qmv_layer.h -- what a decoder layer over block-quantized weights needs around
  * the products of qmv.h when it takes many tokens at once: the gated
  * feed-forward products with their backward pass, the rotary positions of the q
- * and k heads, and these in one pass with the heads' norms, with the gradient.  Same library (libqmv.so), same conventions as qmv.h:
- * packed layout, device pointers, caller-owned buffers, status codes and
+ * and k heads, and these in one pass with the heads' norms, with the gradient.
+ * Same library (libqmv.so), same conventions as qmv.h: packed layout, device pointers, caller-owned buffers, status codes and
  * qmv_last_error, streams, no allocation, no synchronization, graph capture.
  */
 #ifndef QMV_LAYER_H_
